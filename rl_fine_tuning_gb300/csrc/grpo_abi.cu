@@ -5,67 +5,14 @@
 #include <cstring>
 #include <cudaTypedefs.h>
 
-#include <atomic>
-#include <mutex>
-#include <vector>
-
-#include "internal.h"
+#include "abi_common.h"
 
 namespace grpo {
 
-namespace {
-
-constexpr int kVersion = 100;   // 0.1.0
-
-// ---- launch accounting and optional per-kernel event timing
 std::atomic<unsigned long long> g_launches{0};
-
-struct ProfRecord {
-    int kind;
-    cudaEvent_t a, b;
-};
-
-// `on` is read by every launch; the records and the event pool are touched
-// only while profiling is on, under `mu`.
-struct Profiler {
-    std::atomic<bool> on{false};
-    std::mutex mu;
-    std::vector<ProfRecord> recs;
-    std::vector<cudaEvent_t> pool;
-    cudaEvent_t get() {
-        if (!pool.empty()) {
-            cudaEvent_t e = pool.back();
-            pool.pop_back();
-            return e;
-        }
-        cudaEvent_t e = nullptr;
-        if (cudaEventCreate(&e) != cudaSuccess) return nullptr;
-        return e;
-    }
-};
 Profiler g_prof;
 
-// launch one kernel through `fn`, counting it and timing it when profiling is on
-template <class F>
-cudaError_t launch(int kind, cudaStream_t st, F&& fn) {
-    if (!g_prof.on.load(std::memory_order_relaxed)) {
-        const cudaError_t e = fn();
-        if (e == cudaSuccess) g_launches.fetch_add(1, std::memory_order_relaxed);
-        return e;
-    }
-    std::lock_guard<std::mutex> lock(g_prof.mu);
-    cudaEvent_t a = g_prof.get(), b = g_prof.get();
-    if (a) cudaEventRecord(a, st);
-    const cudaError_t e = fn();
-    if (e == cudaSuccess) g_launches.fetch_add(1, std::memory_order_relaxed);
-    if (a && b) {
-        cudaEventRecord(b, st);
-        g_prof.recs.push_back(ProfRecord{kind, a, b});
-    }
-    return e;
-}
-
-inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+static constexpr int kVersion = 100;   // 0.1.0
 
 bool shape_ok(const grpo_shape& s) {
     if (s.n_groups < 1 || s.G < 1 || s.L < 1 || s.V < 1 || s.d < 64 || s.d % 64 != 0) return false;
@@ -78,18 +25,7 @@ bool shape_ok(const grpo_shape& s) {
     return true;
 }
 
-bool dtype_ok(const grpo_shape& s) { return s.dtype == GRPO_BF16 || s.dtype == GRPO_FP16; }
-bool dtype_ok_any(const grpo_shape& s) { return dtype_ok(s) || is_fp8(s.dtype); }
-
-template <class P>
-bool aligned(const P* p, size_t a) {
-    return (reinterpret_cast<uintptr_t>(p) % a) == 0;
-}
-
-struct DeviceInfo {
-    int sm_count = 0;
-    bool ok = false;
-};
+static bool dtype_ok_any(const grpo_shape& s) { return dtype_ok(s) || is_fp8(s.dtype); }
 
 int device_info(DeviceInfo* out) {
     int dev = 0;
@@ -108,7 +44,7 @@ int device_info(DeviceInfo* out) {
 }
 
 // looked up once per process (a thread-safe static initialisation)
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -121,8 +57,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// 2-D row-major matrix [rows x cols] of 16-bit elements with row pitch `pitch`
-// elements, 128-byte swizzled boxes of box_cols x box_rows.
 bool make_map(CUtensorMap* m, const void* base, bool bf16, uint64_t cols, uint64_t rows, uint64_t pitch,
               uint32_t box_cols, uint32_t box_rows) {
     auto fn = encode_fn();
@@ -139,7 +73,7 @@ bool make_map(CUtensorMap* m, const void* base, bool bf16, uint64_t cols, uint64
 }
 
 // 2-D row-major matrix of 8-bit elements (FP8 codes), 128-byte swizzled boxes
-bool make_map_u8(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t pitch, uint32_t box_cols,
+static bool make_map_u8(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t pitch, uint32_t box_cols,
                  uint32_t box_rows) {
     auto fn = encode_fn();
     if (!fn) return false;
@@ -153,7 +87,7 @@ bool make_map_u8(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
     return r == CUDA_SUCCESS;
 }
 
-int default_chunk_rows(const grpo_shape& s) {
+static int default_chunk_rows(const grpo_shape& s) {
     // 8-bit shapes: 76 tiles, so that dW's 8-bit K loop (twice as fast per row as the
     // 16-bit one) stays long against its fp32 read-modify-write epilogue
     if (is_fp8(s.dtype)) return kChunkTilesLarge * kBM;
@@ -171,8 +105,6 @@ int chunk_rows_of(const grpo_shape& s) {
     if (r > nmax) r = static_cast<int>(nmax);
     return r;
 }
-
-}  // namespace
 
 // splits of n_ntiles vocabulary tiles into at most max_splits ranges, none empty
 static void split_vocab(int n_ntiles, int max_splits, int* S, int* nps) {
