@@ -294,6 +294,137 @@ int grpo_loss_fwd_noalloc(const void* h_pol, const void* h_ref, const void* W, c
                           const uint8_t* mask, const float* adv, const grpo_shape* shape,
                           float* loss_out, float* row_stats, int32_t* status, grpo_stream_t stream);
 
+/* ---- log-probs and off-policy losses -----------------------------------
+ * Operators that share the linear algorithm above (logits from hidden states,
+ * never stored) and take the log-probs of other policies as numbers:
+ *   grpo_logprobs           log-probs of given tokens and the entropy, for
+ *                           recording the sampling policy's and the
+ *                           reference's log-probs once, for scoring, and for
+ *                           single tokens while serving
+ *   grpo_logprobs_bwd       its gradients, for a loss the caller defines
+ *   grpo_clip_loss_*        clipped policy loss with a KL term, for taking more
+ *                           than one step on a batch of completions
+ *   grpo_pair_loss_*        preference loss over pairs of completions
+ * The pages name PPO-style and preference training ("Train your own R1
+ * reasoning model with Unsloth", section 4) without formulas; those used are
+ * stated here.
+ *
+ * Common to them: h [N x d] and W [V x d] of type shape->dtype (GRPO_BF16 or
+ * GRPO_FP16; 8-bit types are refused with GRPO_ERR_DTYPE), 16-byte aligned;
+ * tokens [N] int32; mask [N] uint8, nonzero = the row counts (0 in every row of
+ * a completion leaves it empty); workspace of grpo_policy_workspace_bytes bytes,
+ * 256-byte aligned; status as everywhere (a token id outside [0, V) in a
+ * masked-in row sets GRPO_ERR_SHAPE, and that row contributes 0); fixed
+ * reduction orders and no floating-point atomics, so every output is
+ * bitwise reproducible; nothing depends on host knowledge of the data, so calls
+ * can be captured into a CUDA graph.  With z = h W^T / temperature,
+ * q = z[token] - logsumexp(z).  Log-probs are fp32 numbers whose error stays at
+ * fp32's: the tensor cores' partial sums are added in registers, and the given
+ * token's logit is computed by itself.
+ *
+ * Gradients: dH [N x d] of type shape->dtype, exactly 0 on masked rows; dW
+ * [V x d] of type shape->dtype, or fp32 with dw_f32 = 1; both 32-byte aligned,
+ * overwritten, and multiplied by loss_scale (> 0); found_inf [1] int32 <- 1 if a
+ * value of the scaled gradients is not finite.  loss_scale only has to suit the
+ * 16-bit outputs: inside, fp16 dlogits carry a scale of their own.
+ *
+ * shape->objective has to be GRPO_OBJ_GRPO for grpo_clip_loss_*; the others
+ * ignore it, and all but grpo_clip_loss_* ignore loss_mode.  chunk_rows is the
+ * rows per chunk, as for grpo_loss_fwd_bwd. */
+
+/* Operators, for grpo_policy_workspace_bytes. */
+enum { GRPO_OP_LOGPROBS = 0, GRPO_OP_LOGPROBS_BWD = 1, GRPO_OP_CLIP = 2, GRPO_OP_PAIR = 3 };
+
+/* Options of grpo_clip_loss_*.  grpo_clip_opts_init: temperature 1, clips 0.2.
+ *   temperature : > 0; logits are divided by it
+ *   clip_low    : in [0, 1]; clip_high: >= 0 (INFINITY: no upper clip)
+ *   dw_f32      : dW is fp32 (1) or of type shape->dtype (0) */
+typedef struct {
+    float temperature, clip_low, clip_high;
+    int dw_f32;
+} grpo_clip_opts;
+
+/* Kinds of preference loss, with m the margin (see grpo_pair_loss_fwd). */
+enum {
+    GRPO_PAIR_SIGMOID = 0,   /* -(1-e) log sigmoid(m) - e log sigmoid(-m), e = label_smoothing */
+    GRPO_PAIR_HINGE = 1,     /* max(0, 1 - m) */
+    GRPO_PAIR_SQUARE = 2     /* (m / beta - 1 / (2 beta))^2 */
+};
+
+/* Options of grpo_pair_loss_*.  grpo_pair_opts_init: sigmoid, no smoothing, sums.
+ *   label_smoothing : in [0, 0.5); 0 unless kind is GRPO_PAIR_SIGMOID
+ *   length_mean     : log-ratios are averaged over a completion's rows (1) or summed (0)
+ *   dw_f32          : as above */
+typedef struct {
+    int kind;
+    float label_smoothing;
+    int length_mean, dw_f32;
+} grpo_pair_opts;
+
+void grpo_clip_opts_init(grpo_clip_opts* o);
+void grpo_pair_opts_init(grpo_pair_opts* o);
+
+/* Bytes of workspace of operator `op` (GRPO_OP_*) with this dW type (ignored
+ * for GRPO_OP_LOGPROBS): O(chunk_rows * (V + d) + N), plus 4 V d when a 16-bit
+ * dW is summed over several chunks.  GRPO_OP_PAIR: chunks hold a whole pair
+ * (2 L rows) up to 19456 rows unless chunk_rows says otherwise.  0 for an
+ * invalid shape or op. */
+size_t grpo_policy_workspace_bytes(const grpo_shape* shape, int op, int dw_f32);
+
+/* Log-probs of given tokens.
+ *   mask: NULL counts every row
+ *   logp_out [N] fp32 <- q, 0 on masked rows
+ *   entropy_out: NULL or [N] fp32 <- entropy of softmax(z), 0 on masked rows
+ * Up to 32 rows take one pass over W (serving: one token per sequence). */
+int grpo_logprobs(const void* h, const void* W, const int32_t* tokens, const uint8_t* mask, const grpo_shape* shape,
+                  float temperature, void* workspace, size_t ws_bytes, float* logp_out, float* entropy_out,
+                  int32_t* status, grpo_stream_t stream);
+
+/* Gradients of sum_t dlogp[t] q_t over the masked-in rows.
+ *   dlogp [N] fp32 (device, read; masked rows are not read) */
+int grpo_logprobs_bwd(const void* h, const void* W, const int32_t* tokens, const uint8_t* mask, const float* dlogp,
+                      const grpo_shape* shape, float temperature, float loss_scale, int dw_f32, void* workspace,
+                      size_t ws_bytes, void* dH, void* dW, int32_t* found_inf, int32_t* status, grpo_stream_t stream);
+
+/* Clipped policy loss.  With r = exp(q - logp_old), A the completion's
+ * advantage, x = logp_ref - q and beta = shape->beta:
+ *   ell = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + beta (e^x - x - 1)
+ *   loss = mean of ell as shape->loss_mode says, 0 if no row counts
+ * A row whose minimum is the clipped term gets no gradient from it; a ratio
+ * exactly at a border counts as not clipped.
+ *   adv [n_groups*G], logp_old [N], logp_ref [N] fp32 (device, read; logp_ref
+ *   may be NULL when beta is 0, and is not read then)
+ *   row_stats: NULL or [N x 3] fp32 <- (q, r, e^x - x - 1), zeros on masked rows
+ * loss and row_stats of the two entry points are the same bits. */
+int grpo_clip_loss_fwd(const void* h, const void* W, const int32_t* tokens, const uint8_t* mask, const float* adv,
+                       const float* logp_old, const float* logp_ref, const grpo_shape* shape, const grpo_clip_opts* opts,
+                       void* workspace, size_t ws_bytes, float* loss_out, float* row_stats, int32_t* status,
+                       grpo_stream_t stream);
+int grpo_clip_loss_fwd_bwd(const void* h, const void* W, const int32_t* tokens, const uint8_t* mask, const float* adv,
+                           const float* logp_old, const float* logp_ref, const grpo_shape* shape,
+                           const grpo_clip_opts* opts, float loss_scale, void* workspace, size_t ws_bytes, float* loss_out,
+                           void* dH, void* dW, int32_t* found_inf, float* row_stats, int32_t* status,
+                           grpo_stream_t stream);
+
+/* Preference loss.  shape->G is 2: in each of the n_groups pairs completion 0 is
+ * the preferred one.  With S_i the sum (or mean) over completion i's rows of
+ * q - logp_ref (0 for an empty completion), beta = shape->beta > 0:
+ *   m = beta (S_0 - S_1);  loss = mean of the chosen function of m over the
+ *   pairs with at least one masked-in row, 0 if there is none
+ *   logp_ref [N] fp32 (device, read)
+ *   logp_out: NULL or [N] fp32 <- q, 0 on masked rows
+ *   pair_stats: NULL or [n_groups x 4] fp32 <- (beta S_0, beta S_1, m, the pair's
+ *               loss); the loss entry is 0 for a pair without rows
+ * When 2 L rows fit a chunk, the logits are computed once for loss and
+ * gradients, else twice. */
+int grpo_pair_loss_fwd(const void* h, const void* W, const int32_t* tokens, const uint8_t* mask, const float* logp_ref,
+                       const grpo_shape* shape, const grpo_pair_opts* opts, void* workspace, size_t ws_bytes,
+                       float* loss_out, float* logp_out, float* pair_stats, int32_t* status, grpo_stream_t stream);
+int grpo_pair_loss_fwd_bwd(const void* h, const void* W, const int32_t* tokens, const uint8_t* mask, const float* logp_ref,
+                           const grpo_shape* shape, const grpo_pair_opts* opts, float loss_scale, void* workspace,
+                           size_t ws_bytes, float* loss_out, void* dH, void* dW, int32_t* found_inf, float* logp_out,
+                           float* pair_stats, int32_t* status, grpo_stream_t stream);
+
 /* ---- diagnostics ------------------------------------------------------
  * Per-kernel device time.  While enabled, the library records a CUDA event
  * pair on the launching stream around every kernel it launches.

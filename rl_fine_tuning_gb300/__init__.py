@@ -21,7 +21,9 @@ __all__ = [
     "grpo_shard_counts", "grpo_loss_fwd_shard", "grpo_loss_fwd_bwd_shard", "grpo_loss_fwd_bwd_fp8",
     "grpo_status_string", "grpo_version", "library_path", "grpo_profile_enable", "grpo_profile_collect",
     "grpo_kernel_launches", "grpo_device_checks", "grpo_selftest_bounds_check", "grpo_selftest_wait_timeout",
-    "PROF_KINDS",
+    "PROF_KINDS", "GrpoClipOpts", "GrpoPairOpts", "HEAD_OPS", "PAIR_KINDS", "clip_opts", "pair_opts",
+    "grpo_policy_workspace_bytes", "grpo_logprobs", "grpo_logprobs_bwd", "grpo_clip_loss_fwd", "grpo_clip_loss_fwd_bwd",
+    "grpo_pair_loss_fwd", "grpo_pair_loss_fwd_bwd",
 ]
 
 # kernel kinds of the diagnostics interface, in the order of the GRPO_PROF_* enum
@@ -29,6 +31,9 @@ PROF_KINDS = ("advantages", "mask", "index", "fwd", "merge", "clear", "gather", 
 
 BF16, FP16, E4M3, E5M2 = 0, 1, 2, 3
 TOKEN_MEAN, SEQUENCE_MEAN = 0, 1
+# operators of grpo_policy_workspace_bytes, and kinds of preference loss
+HEAD_OPS = {"logp": 0, "logp_grad": 1, "clip": 2, "pair": 3}
+PAIR_KINDS = {"sigmoid": 0, "hinge": 1, "square": 2}
 OBJECTIVES = {"grpo": 0, "no_detach": 1, "reverse_kl_q": 2, "forward_kl": 3}
 
 
@@ -50,6 +55,18 @@ class GrpoShape(ctypes.Structure):
     @property
     def N(self) -> int:
         return self.n_groups * self.G * self.L
+
+
+class GrpoClipOpts(ctypes.Structure):
+    """Mirror of grpo_clip_opts in include/grpo.h."""
+    _fields_ = [("temperature", ctypes.c_float), ("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float),
+                ("dw_f32", ctypes.c_int)]
+
+
+class GrpoPairOpts(ctypes.Structure):
+    """Mirror of grpo_pair_opts in include/grpo.h."""
+    _fields_ = [("kind", ctypes.c_int), ("label_smoothing", ctypes.c_float), ("length_mean", ctypes.c_int),
+                ("dw_f32", ctypes.c_int)]
 
 
 _lib = None
@@ -94,6 +111,17 @@ def _declare(lib):
         "grpo_shard_counts": ([p, sp, p, p], i32),
         "grpo_loss_fwd_shard": ([p, p, p, p, p, p, sp, p, p, sz, p, p, p, p], i32),
         "grpo_loss_fwd_bwd_shard": ([p, p, p, p, p, p, sp, p, f32, p, sz, p, p, p, p, p, p, p], i32),
+        "grpo_clip_opts_init": ([ctypes.POINTER(GrpoClipOpts)], None),
+        "grpo_pair_opts_init": ([ctypes.POINTER(GrpoPairOpts)], None),
+        "grpo_policy_workspace_bytes": ([sp, i32, i32], sz),
+        "grpo_logprobs": ([p, p, p, p, sp, f32, p, sz, p, p, p, p], i32),
+        "grpo_logprobs_bwd": ([p, p, p, p, p, sp, f32, f32, i32, p, sz, p, p, p, p, p], i32),
+        "grpo_clip_loss_fwd": ([p, p, p, p, p, p, p, sp, ctypes.POINTER(GrpoClipOpts), p, sz, p, p, p, p], i32),
+        "grpo_clip_loss_fwd_bwd": ([p, p, p, p, p, p, p, sp, ctypes.POINTER(GrpoClipOpts), f32, p, sz, p, p, p, p, p, p,
+                                    p], i32),
+        "grpo_pair_loss_fwd": ([p, p, p, p, p, sp, ctypes.POINTER(GrpoPairOpts), p, sz, p, p, p, p, p], i32),
+        "grpo_pair_loss_fwd_bwd": ([p, p, p, p, p, sp, ctypes.POINTER(GrpoPairOpts), f32, p, sz, p, p, p, p, p, p, p, p],
+                                   i32),
         "grpo_profile_enable": ([i32], i32),
         "grpo_profile_collect": ([ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_longlong), i32], i32),
         "grpo_kernel_launches": ([], ctypes.c_ulonglong),
@@ -272,3 +300,132 @@ def grpo_selftest_bounds_check(status, stream=None):
 def grpo_selftest_wait_timeout(status, waited_ns, stream=None):
     _check(load().grpo_selftest_wait_timeout(_ptr(status), _ptr(waited_ns), _stream(stream)),
            "grpo_selftest_wait_timeout")
+
+
+# ---------------------------------------------------------------- log-probs and off-policy losses
+# Tensor arguments of these are checked: a tensor has to be a contiguous CUDA
+# tensor of the stated type and number of elements (the C interface sees only
+# its pointer).  Integers pass as raw pointers, unchecked.
+
+def _arg(x, name, dtypes, numel):
+    if x is None or isinstance(x, int):
+        return _ptr(x)
+    if not x.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is wanted")
+    if str(x.dtype).replace("torch.", "") not in dtypes:
+        raise ValueError(f"{name}: type {x.dtype}, wanted {' or '.join(dtypes)}")
+    if x.numel() != numel:
+        raise ValueError(f"{name}: {x.numel()} elements, wanted {numel}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is wanted")
+    return _ptr(x)
+
+
+_F32, _I32 = ("float32",), ("int32",)
+
+
+def _head_type(shape):
+    return {BF16: ("bfloat16",), FP16: ("float16",)}.get(shape.dtype, ())
+
+
+def _inputs(h, W, tokens, mask, shape):
+    t = _head_type(shape)
+    if not t:
+        raise GrpoError(5, "dtype check")
+    return (_arg(h, "h", t, shape.N * shape.d), _arg(W, "W", t, shape.V * shape.d), _arg(tokens, "tokens", _I32, shape.N),
+            _arg(mask, "mask", ("uint8", "bool"), shape.N))
+
+
+def _grads(dH, dW, found_inf, shape, dw_f32):
+    t = _head_type(shape)
+    return (_arg(dH, "dH", t, shape.N * shape.d), _arg(dW, "dW", _F32 if dw_f32 else t, shape.V * shape.d),
+            _arg(found_inf, "found_inf", _I32, 1))
+
+
+def _workspace(ws):
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("workspace: a contiguous CUDA tensor is wanted")
+    return _ptr(ws), _nbytes(ws)
+
+
+def clip_opts(temperature=1.0, clip_low=0.2, clip_high=0.2, dw_f32=False) -> GrpoClipOpts:
+    o = GrpoClipOpts()
+    load().grpo_clip_opts_init(ctypes.byref(o))
+    o.temperature, o.clip_low, o.clip_high, o.dw_f32 = temperature, clip_low, clip_high, int(bool(dw_f32))
+    return o
+
+
+def pair_opts(kind="sigmoid", label_smoothing=0.0, length_mean=False, dw_f32=False) -> GrpoPairOpts:
+    o = GrpoPairOpts()
+    load().grpo_pair_opts_init(ctypes.byref(o))
+    o.kind = PAIR_KINDS[kind] if isinstance(kind, str) else int(kind)
+    o.label_smoothing, o.length_mean, o.dw_f32 = label_smoothing, int(bool(length_mean)), int(bool(dw_f32))
+    return o
+
+
+def grpo_policy_workspace_bytes(shape: GrpoShape, op, dw_f32=False) -> int:
+    """Workspace of an operator: "logp", "logp_grad", "clip" or "pair" (or its GRPO_OP_* number)."""
+    code = HEAD_OPS[op] if isinstance(op, str) else int(op)
+    return int(load().grpo_policy_workspace_bytes(ctypes.byref(shape), code, int(bool(dw_f32))))
+
+
+def grpo_logprobs(h, W, tokens, mask, shape, temperature, workspace, logp_out, entropy_out, status, stream=None):
+    """q (and the entropy, unless None) of every row's token; mask None counts every row."""
+    N = shape.N
+    _check(load().grpo_logprobs(*_inputs(h, W, tokens, mask, shape), ctypes.byref(shape), float(temperature),
+                                *_workspace(workspace), _arg(logp_out, "logp_out", _F32, N),
+                                _arg(entropy_out, "entropy_out", _F32, N), _arg(status, "status", _I32, 1),
+                                _stream(stream)), "grpo_logprobs")
+
+
+def grpo_logprobs_bwd(h, W, tokens, mask, dlogp, shape, temperature, loss_scale, workspace, dH, dW, found_inf, status,
+                      dw_f32=False, stream=None):
+    """Gradients of sum dlogp q."""
+    g = _grads(dH, dW, found_inf, shape, dw_f32)
+    _check(load().grpo_logprobs_bwd(*_inputs(h, W, tokens, mask, shape), _arg(dlogp, "dlogp", _F32, shape.N),
+                                    ctypes.byref(shape), float(temperature), float(loss_scale), int(bool(dw_f32)),
+                                    *_workspace(workspace), *g, _arg(status, "status", _I32, 1), _stream(stream)),
+           "grpo_logprobs_bwd")
+
+
+def _clip_inputs(h, W, tokens, mask, adv, logp_old, logp_ref, shape):
+    return (*_inputs(h, W, tokens, mask, shape), _arg(adv, "adv", _F32, shape.n_groups * shape.G),
+            _arg(logp_old, "logp_old", _F32, shape.N), _arg(logp_ref, "logp_ref", _F32, shape.N))
+
+
+def grpo_clip_loss_fwd(h, W, tokens, mask, adv, logp_old, logp_ref, shape, opts, workspace, loss_out, row_stats, status,
+                       stream=None):
+    _check(load().grpo_clip_loss_fwd(*_clip_inputs(h, W, tokens, mask, adv, logp_old, logp_ref, shape),
+                                     ctypes.byref(shape), ctypes.byref(opts), *_workspace(workspace),
+                                     _arg(loss_out, "loss_out", _F32, 1), _arg(row_stats, "row_stats", _F32, 3 * shape.N),
+                                     _arg(status, "status", _I32, 1), _stream(stream)), "grpo_clip_loss_fwd")
+
+
+def grpo_clip_loss_fwd_bwd(h, W, tokens, mask, adv, logp_old, logp_ref, shape, opts, loss_scale, workspace, loss_out, dH,
+                           dW, found_inf, row_stats, status, stream=None):
+    g = _grads(dH, dW, found_inf, shape, opts.dw_f32)
+    _check(load().grpo_clip_loss_fwd_bwd(*_clip_inputs(h, W, tokens, mask, adv, logp_old, logp_ref, shape),
+                                         ctypes.byref(shape), ctypes.byref(opts), float(loss_scale),
+                                         *_workspace(workspace), _arg(loss_out, "loss_out", _F32, 1), *g,
+                                         _arg(row_stats, "row_stats", _F32, 3 * shape.N),
+                                         _arg(status, "status", _I32, 1), _stream(stream)), "grpo_clip_loss_fwd_bwd")
+
+
+def grpo_pair_loss_fwd(h, W, tokens, mask, logp_ref, shape, opts, workspace, loss_out, logp_out, pair_stats, status,
+                       stream=None):
+    _check(load().grpo_pair_loss_fwd(*_inputs(h, W, tokens, mask, shape), _arg(logp_ref, "logp_ref", _F32, shape.N),
+                                     ctypes.byref(shape), ctypes.byref(opts), *_workspace(workspace),
+                                     _arg(loss_out, "loss_out", _F32, 1), _arg(logp_out, "logp_out", _F32, shape.N),
+                                     _arg(pair_stats, "pair_stats", _F32, 4 * shape.n_groups),
+                                     _arg(status, "status", _I32, 1), _stream(stream)), "grpo_pair_loss_fwd")
+
+
+def grpo_pair_loss_fwd_bwd(h, W, tokens, mask, logp_ref, shape, opts, loss_scale, workspace, loss_out, dH, dW, found_inf,
+                           logp_out, pair_stats, status, stream=None):
+    g = _grads(dH, dW, found_inf, shape, opts.dw_f32)
+    _check(load().grpo_pair_loss_fwd_bwd(*_inputs(h, W, tokens, mask, shape), _arg(logp_ref, "logp_ref", _F32, shape.N),
+                                         ctypes.byref(shape), ctypes.byref(opts), float(loss_scale),
+                                         *_workspace(workspace), _arg(loss_out, "loss_out", _F32, 1), *g,
+                                         _arg(logp_out, "logp_out", _F32, shape.N),
+                                         _arg(pair_stats, "pair_stats", _F32, 4 * shape.n_groups),
+                                         _arg(status, "status", _I32, 1), _stream(stream)), "grpo_pair_loss_fwd_bwd")

@@ -24,8 +24,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libgrpo.so")
 LIB_CHECKED = os.path.join(BUILD, "libgrpo_checked.so")
 VARIANTS = {LIB: [], LIB_CHECKED: ["-DGRPO_DEVICE_CHECKS"]}
-SOURCES = ["tc_kernels.cu", "small_kernels.cu", "grpo_abi.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "tc_pair.cuh", "abi_common.h"]
+SOURCES = ["tc_kernels.cu", "small_kernels.cu", "grpo_abi.cu", "head_tc.cu", "head_kernels.cu", "head_abi.cu"]
+HEADERS = ["ptx.cuh", "internal.h", "tc_pair.cuh", "abi_common.h", "head.h", "head_join.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

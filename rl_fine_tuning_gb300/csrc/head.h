@@ -1,0 +1,178 @@
+// Declarations of the head operators: log-probs of given tokens, the clipped
+// policy loss and the preference loss, all from hidden states and W.
+//
+// One call runs, per chunk of masked-in rows (at most R of them):
+//   gather     compact (and transposed) copies of the rows; the given token's
+//              logit of each row by itself
+//   logits     z = h . W^T, streaming (max, sum exp, sum z exp); with a
+//              backward the exponentials stay in the chunk buffer
+//   merge      per row: logsumexp, q, entropy; the operator's d loss / d q
+//   dlogits, dH, dW
+// A chunk's bounds, like every count, are device data (k_plan).
+#pragma once
+#include "internal.h"
+
+namespace grpo {
+
+enum HeadMode {
+    HEAD_LOGP = 0,    // q and entropy out
+    HEAD_GRAD = 1,    // d loss / d q is an input
+    HEAD_CLIP = 2,    // clipped policy loss
+    HEAD_PAIR = 3     // preference loss: d loss / d q follows from sums over pairs of completions
+};
+
+constexpr int kPieceK = 256;        // K elements the tensor cores add up before the sum moves to registers
+constexpr int kHeadThreads = 384;   // a warpgroup with the producer and MMA warps, two of epilogue warps
+constexpr int kHeadSplitsMax = 512;
+constexpr int kDhSlotsMax = 304;    // 256 x 256 partial tiles of dH (4 per SM pair)
+constexpr int kFewRows = 32;        // rows of the few-row kernel
+constexpr int kFewVocab = 128;      // vocabulary rows per tile of the few-row kernel
+// what stands for a logit that does not count (the given token's own, columns
+// past V): finite, so no inf - inf can form, far below every logit, and a
+// power of two, so its product with log2 e is that constant's rounding, exactly
+constexpr float kNoLogit = -1267650600228229401496703205376.f;   // -2^100
+constexpr float kNoLogit2 = kNoLogit * 1.4426950408889634f;
+
+struct PlanParams {
+    const uint8_t* mask;    // nullptr: every row counts
+    int64_t N;
+    int L, n_seq, R;
+    int by_pair;            // chunks of whole pairs of completions
+    int pairs_of_g2;        // completions 2i and 2i + 1 are a pair: count pairs, not completions, with a valid row
+    int max_chunks;
+    int n_nt, ks, n_pairs, slots_max;   // dH: 256-wide d tiles, K-stages, SM pairs, partial tiles (0: no backward)
+    int* counts;
+    int* off;               // [n_seq + 1] valid rows before completion i
+    int* cb;                // [max_chunks + 1] first valid row of chunk c
+    int* pb;                // [max_chunks + 1] first pair of chunk c (by_pair)
+    int2* dh_plan;          // [max_chunks] (units in one piece, K pieces of the rest)
+    unsigned* gmax;         // [max_chunks] largest |d loss / d q| (float bits), zeroed
+    int* rows;              // [N] valid rows, ascending
+    int* found_inf;         // nullable, zeroed
+    int* status;            // zeroed
+};
+
+struct GatherParams {
+    const int* counts;
+    const int* cb;
+    const int* rows;
+    const int* tokens;
+    const uint8_t* mask;
+    const uint16_t* h;
+    const uint16_t* W;
+    uint16_t* hc;           // [R x d]
+    uint16_t* hct;          // [d x R], nullable
+    double* zt;             // [N] logit of the given token
+    uint16_t* dH;           // nullable: rows of masked rows are zeroed with chunk 0
+    void* dW;               // nullable: zeroed with chunk 0 when no row counts
+    int64_t dw_bytes;
+    float* out0;            // nullable per-row outputs, zeroed on masked rows with chunk 0
+    float* out1;
+    float* stats;           // [N x 3]
+    float zscale;
+    int64_t N;
+    int d, V, R, chunk;
+    int* status;
+};
+
+struct LogitsParams {
+    const int* counts;
+    const int* cb;
+    const int* rows;
+    const int* tokens;
+    float4* part;           // [R x 2S] (m, s, u, -) of each half split, m in base 2
+    uint16_t* E;            // [R x V_pad] bf16 2^(z log2 e - running max), with a backward
+    float* mx;              // [R x nc32] running max per 32 columns, base 2
+    float zscale;           // 1 / temperature
+    int64_t N;
+    int chunk, V, d, S, nps, n_ntiles, V_pad, nc32, R;
+    int* status;
+};
+
+struct FewParams {
+    const int* tokens;
+    const uint8_t* mask;    // nullable
+    const double* zt;       // [N] logit of the given token
+    float4* part;           // [N x grid]
+    int* counter;
+    float* logp;
+    float* entropy;         // nullable
+    float zscale;
+    int N, V, d, n_tiles;
+    int* status;
+};
+
+struct HeadMergeParams {
+    const float4* part;
+    int S2;                 // partials per row
+    const int* counts;
+    const int* cb;
+    const int* off;
+    const int* rows;
+    const int* tokens;
+    const double* zt;
+    float* lse;
+    float* gco;
+    float* ell;
+    unsigned* gmax;
+    float* logp;            // nullable [N]
+    float* entropy;         // nullable [N]
+    const float* dlogp;     // HEAD_GRAD
+    const float* adv;       // HEAD_CLIP ...
+    const float* logp_old;
+    const float* logp_ref;  // nullable
+    float* stats;           // nullable [N x 3]
+    float beta, clip_lo, clip_hi, inv_t;
+    int mode, loss_mode, chunk, L, V, R;
+    int64_t N;
+    int* status;
+};
+
+struct PairParams {
+    const int* counts;
+    const int* off;
+    const int* pb;          // nullptr: every pair
+    const int* rows;
+    const float* logp;
+    const float* logp_ref;
+    float* gco;
+    unsigned* gmax;         // of this chunk
+    double* pair_ell;       // [n_pairs]
+    float* pair_stats;      // nullable [n_pairs x 4]
+    float beta, smoothing;
+    int kind, length_mean, n_pairs, chunk;
+    int64_t N;
+    int* status;
+};
+
+// ChunkParams of the head operators' GEMMs
+struct HeadChunkParams : ChunkParams {
+    float* dw_acc;          // fp32 dW (the caller's, or the workspace's when dw16 is given and there are several chunks)
+    uint16_t* dw16;         // 16-bit dW, nullable
+    float* dh_part;         // [slots][2][128 x 256] fp32
+    const int2* dh_plan;
+    const float* logp;      // [N] q
+    const unsigned* gmax;
+    int gmax_chunk;         // which entry of gmax holds this chunk's
+    float loss_scale;
+};
+
+cudaError_t launch_plan(const PlanParams& p, cudaStream_t st);
+cudaError_t launch_head_gather(const GatherParams& p, bool bf16, int sm_count, cudaStream_t st);
+cudaError_t launch_head_logits(const LogitsParams& p, const CUtensorMap& mH, const CUtensorMap& mW, int n_sm, bool bf16,
+                               bool keep, bool entropy, cudaStream_t st);
+cudaError_t launch_head_merge(const HeadMergeParams& p, cudaStream_t st);
+cudaError_t launch_pair_coef(const PairParams& p, cudaStream_t st);
+cudaError_t launch_head_dlogits(const HeadChunkParams& p, float* oscale, bool bf16, int sm_count, cudaStream_t st);
+cudaError_t launch_head_dh(const HeadChunkParams& p, const CUtensorMap& mDS, const CUtensorMap& mWmn, int n_sm, bool bf16,
+                           cudaStream_t st);
+cudaError_t launch_head_dh_join(const HeadChunkParams& p, bool bf16, int sm_count, cudaStream_t st);
+cudaError_t launch_head_dw(const HeadChunkParams& p, const CUtensorMap& mDSmn, const CUtensorMap& mHct, int n_sm, bool bf16,
+                           cudaStream_t st);
+cudaError_t launch_row_loss(const float* ell, const int* counts, float* loss, cudaStream_t st);
+cudaError_t launch_pair_loss(const double* ell, int n_pairs, const int* counts, float* loss, cudaStream_t st);
+cudaError_t launch_few_prep(const FewParams& p, const uint16_t* h, const uint16_t* W, bool bf16, double* zt, cudaStream_t st);
+cudaError_t launch_few(const FewParams& p, const CUtensorMap& mH, const CUtensorMap& mW, int grid, bool bf16, int nc,
+                       cudaStream_t st);
+
+}  // namespace grpo

@@ -1,0 +1,810 @@
+// Tensor-core kernels of the head operators (tcgen05 + TMEM, fed by TMA).
+//
+//   head_logits_kernel  z = h . W^T of a chunk on SM pairs (M = 256: two row
+//       tiles), with a streaming (max, sum exp) per row; the logits are never
+//       written.  With a backward it keeps exp(z - running max).
+//   head_few_kernel     the same for at most 32 rows, W as the M operand, so
+//       that W streams through the SMs once: bound by HBM.
+//   head_dh_kernel      dH = dlogits . W, its last wave split over K
+//   head_dw_kernel      dW = dlogits^T . h, written in the type of W or in fp32
+//
+// Sums over K.  tcgen05.mma adds to its fp32 accumulator with rounding towards
+// zero: after d / 16 additions a logit of 11 was 4.6e-5 too small at d = 4096
+// (measured), a bias that stays in every log-prob, in ratios near 1 and in
+// sums of log-probs over a completion.  The two forward kernels therefore let
+// the tensor cores add only kPieceK = 256 products at a time and add the
+// pieces in registers, rounding to nearest: 16 times fewer biased additions on
+// numbers 16 times smaller.  Eight epilogue warps hold one 128 x 256
+// accumulator (128 registers a thread); a piece takes the tensor cores about
+// 2100 clocks and the epilogue about 500, so nothing waits for it.
+#include <cfloat>
+
+#include "head_join.cuh"
+#include "tc_pair.cuh"
+
+namespace grpo {
+
+namespace {
+
+constexpr int kStagesPerPiece = kPieceK / kBK;
+
+// ====================================================================== logits of a chunk
+
+constexpr int kLgStages = 6;
+constexpr int kLgStageBytes = 16384 + 16384;   // A (128 rows x 64), B half (128 vocabulary rows x 64)
+constexpr int kLgSmem = kLgStages * kLgStageBytes + 1024 + 512;
+
+// units: (row-tile pair, vocabulary split), row-tile pairs fastest within
+// groups of kFwdGroup so that a W tile is shared in L2
+struct LgSched {
+    int n_units, ks, n_pc, n_mp, c0, n_c;
+};
+
+__device__ __forceinline__ bool lg_setup(const LogitsParams& p, LgSched& sc) {
+    if (p.chunk >= p.counts[C_NCHUNKS]) return false;
+    sc.c0 = p.cb[p.chunk];
+    sc.n_c = p.cb[p.chunk + 1] - sc.c0;
+    sc.n_mp = (sc.n_c + 2 * kBM - 1) / (2 * kBM);
+    sc.n_units = sc.n_mp * p.S;
+    sc.ks = p.d / kBK;
+    sc.n_pc = (sc.ks + kStagesPerPiece - 1) / kStagesPerPiece;
+    return sc.n_units > 0;
+}
+
+__device__ __forceinline__ int lg_items(const LogitsParams& p, int split) {
+    return min(split * p.nps + p.nps, p.n_ntiles) - split * p.nps;
+}
+
+// One row's running statistics over the columns a thread sees: m = max of
+// z log2 e as rounded, s = sum 2^(z log2 e - m), u = sum z 2^(z log2 e - m).  In
+// base 2 the rounding of m cancels; e^(z - m) with m log2 e rounded would not.
+struct RowStat {
+    float m, s, u;
+};
+
+template <bool kBf16, bool kKeep, bool kEnt>
+__device__ __forceinline__ void lg_body(const LogitsParams& p, const CUtensorMap& mA, const CUtensorMap& mB) {
+    extern __shared__ uint8_t smem_raw[];
+    LgSched sc;
+    if (!lg_setup(p, sc)) return;
+    const int cid = static_cast<int>(blockIdx.x) >> 1;
+    const int n_pairs = static_cast<int>(gridDim.x) >> 1;
+    if (cid >= sc.n_units) return;   // uniform across the pair
+    const int rank = static_cast<int>(cluster_ctarank());
+    const bool leader = rank == 0;
+    Smem sm = carve_smem<kLgStages, kLgStageBytes>(smem_raw);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    int* status = p.status;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kLgStages; ++s) {
+            mbar_init(&sm.full[s], 1);    // leader: its producer's expect_tx + both CTAs' bytes
+            mbar_init(&sm.empty[s], 1);   // the leader's MMA commit, multicast to both CTAs
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sm.acc_full[b], 1);     // the leader's commit, multicast
+            mbar_init(&sm.acc_empty[b], 16);   // leader: the eight epilogue warps of both CTAs
+        }
+        mbar_init(sm.drain, 1);
+        *sm.abort_flag = 0;
+        sm.ld_count[0] = sm.ld_count[1] = sm.ld_count[2] = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&mA);
+        tma_prefetch_desc(&mB);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(sm.tmem_slot, kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *sm.tmem_slot;
+    const uint32_t full0 = map_cluster(smem_u32(&sm.full[0]), 0);
+    const uint32_t acc_empty0 = map_cluster(smem_u32(&sm.acc_empty[0]), 0);
+
+    // 3 x 128 threads at 168 registers: the epilogue's two warpgroups take 216 each,
+    // the first keeps 64 (216 + 216 + 64 <= 3 x 168)
+    if (warp >= 4) {
+        setmaxnreg_inc<216>();
+        // ------------------------------------------------ epilogue: warp w holds lanes 32 (w % 4) .. + 31
+        // and columns 128 half .. + 127 of the accumulator, one row per thread
+        const int half = (warp - 4) >> 2;
+        const int row = lane + 32 * (warp & 3);
+        const uint32_t tq = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 128u * half;
+        int it = 0;
+        for (int unit = cid; unit < sc.n_units; unit += n_pairs) {
+            int mp, split;
+            decode_grouped(unit, sc.n_mp, p.S, kFwdGroup, &mp, &split);
+            const int n_items = lg_items(p, split);
+            const int slot = (2 * mp + rank) * kBM + row;
+            bool valid = slot < sc.n_c && GRPO_DCHECK(slot < p.R, status);
+            const int t = valid ? p.rows[sc.c0 + slot] : 0;
+            if (valid && !GRPO_DCHECK(t >= 0 && t < p.N, status)) valid = false;
+            const int tok = valid ? p.tokens[t] : -1;
+            RowStat e{kNoLogit2, 0.f, 0.f};
+            for (int item = 0; item < n_items; ++item) {
+                float a[128];
+                for (int pc = 0; pc < sc.n_pc; ++pc, ++it) {
+                    const int b = it & 1;
+                    if (!mbar_wait(&sm.acc_full[b], (it >> 1) & 1u, sm.abort_flag, status)) goto epi_done;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float v[32];
+                        tmem_ld32(tq + b * 256 + c * 32, v);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) a[32 * c + j] = pc == 0 ? v[j] : a[32 * c + j] + v[j];
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (leader) mbar_arrive(&sm.acc_empty[b]);
+                        else mbar_arrive_cluster(acc_empty0 + 8u * b);
+                    }
+                }
+                const int n0 = (split * p.nps + item) * kBN + 128 * half;
+                uint16_t* erow = kKeep && valid ? p.E + static_cast<int64_t>(slot) * p.V_pad + n0 : nullptr;
+                float mv[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int col0 = n0 + 32 * c;
+                    mv[c] = 0.f;
+                    if (col0 >= p.V) continue;
+                    float* v = a + 32 * c;
+                    if (p.zscale != 1.f) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] *= p.zscale;
+                    }
+                    // columns past V and the row's own token do not count here
+                    const int nvalid = p.V - col0;
+                    if (nvalid < 32) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j >= nvalid) v[j] = kNoLogit;
+                    }
+                    if (__any_sync(0xffffffffu, static_cast<unsigned>(tok - col0) < 32u)) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (tok == col0 + j) v[j] = kNoLogit;
+                    }
+                    float cmax = v[0];
+#pragma unroll
+                    for (int j = 1; j < 32; ++j) cmax = fmaxf(cmax, v[j]);
+                    const float m_new = fmaxf(e.m, cmax * kLog2e);
+                    float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float x0 = fast_exp2(fmaf(v[j], kLog2e, -m_new));
+                        const float x1 = fast_exp2(fmaf(v[j + 1], kLog2e, -m_new));
+                        s0 += x0;
+                        s1 += x1;
+                        if (kEnt) {
+                            u0 = fmaf(x0, v[j], u0);
+                            u1 = fmaf(x1, v[j + 1], u1);
+                        }
+                        v[j] = x0;
+                        v[j + 1] = x1;
+                    }
+                    const float f = fast_exp2(e.m - m_new);
+                    e.s = fmaf(e.s, f, s0 + s1);
+                    if (kEnt) e.u = fmaf(e.u, f, u0 + u1);
+                    e.m = m_new;
+                    mv[c] = m_new;
+                    if (kKeep && valid && GRPO_DCHECK(col0 + 32 <= p.V_pad, status)) {
+                        // 64 bytes of one row as two whole 32-byte sectors
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float* w = v + 16 * h;
+                            st_global_v8(erow + 32 * c + 16 * h, pack2(w[0], w[1], true), pack2(w[2], w[3], true),
+                                         pack2(w[4], w[5], true), pack2(w[6], w[7], true), pack2(w[8], w[9], true),
+                                         pack2(w[10], w[11], true), pack2(w[12], w[13], true),
+                                         pack2(w[14], w[15], true));
+                        }
+                    }
+                }
+                // nc32 is a multiple of 8 and n0 of 128: 16-byte aligned
+                if (kKeep && valid && GRPO_DCHECK((n0 >> 5) + 4 <= p.nc32, status))
+                    *reinterpret_cast<float4*>(p.mx + static_cast<int64_t>(slot) * p.nc32 + (n0 >> 5)) =
+                        make_float4(mv[0], mv[1], mv[2], mv[3]);
+            }
+            if (valid && GRPO_DCHECK(split >= 0 && split < p.S, status))
+                p.part[static_cast<int64_t>(slot) * (2 * p.S) + 2 * split + half] = make_float4(e.m, e.s, e.u, 0.f);
+        }
+    epi_done:;
+    } else {
+        setmaxnreg_dec<64>();
+        if (warp == 0) {
+            // ------------------------------------------------ TMA producer (both CTAs)
+            if (lane == 0) {
+                int s = 0, n_issued = 0;
+                uint32_t ph = 0;
+                for (int unit = cid; unit < sc.n_units; unit += n_pairs) {
+                    int mp, split;
+                    decode_grouped(unit, sc.n_mp, p.S, kFwdGroup, &mp, &split);
+                    const int m0 = (2 * mp + rank) * kBM;
+                    const int n_items = lg_items(p, split);
+                    for (int item = 0; item < n_items; ++item) {
+                        const int n0 = (split * p.nps + item) * kBN + rank * 128;
+                        for (int k = 0; k < sc.ks; ++k) {
+                            if (!mbar_wait(&sm.empty[s], ph ^ 1u, sm.abort_flag, status)) goto producer_done;
+                            uint8_t* st = sm.stages + s * kLgStageBytes;
+                            if (leader) mbar_arrive_expect_tx(&sm.full[s], 2 * kLgStageBytes);
+                            tma_load_2d_pair(&mA, full0 + 8u * s, st, k * kBK, m0);
+                            tma_load_2d_pair(&mB, full0 + 8u * s, st + 16384, k * kBK, n0);
+                            ++n_issued;
+                            if (++s == kLgStages) {
+                                s = 0;
+                                ph ^= 1u;
+                            }
+                        }
+                    }
+                }
+            producer_done:
+                sm.ld_count[0] = n_issued;
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------ MMA issuer (leader only)
+            if (lane == 0 && leader) {
+                constexpr uint32_t idesc = make_idesc_f16(256, 256, kBf16, false, false);
+                int s = 0, n_used = 0;
+                uint32_t ph = 0;
+                int it = 0;
+                for (int unit = cid; unit < sc.n_units; unit += n_pairs) {
+                    int mp, split;
+                    decode_grouped(unit, sc.n_mp, p.S, kFwdGroup, &mp, &split);
+                    const int n_items = lg_items(p, split);
+                    for (int item = 0; item < n_items; ++item)
+                        for (int k0 = 0; k0 < sc.ks; k0 += kStagesPerPiece, ++it) {
+                            const int b = it & 1;
+                            if (!mbar_wait(&sm.acc_empty[b], ((it >> 1) & 1u) ^ 1u, sm.abort_flag, status)) goto mma_done;
+                            tc_fence_after();
+                            const uint32_t acc = tmem + b * 256;
+                            const int k1 = min(k0 + kStagesPerPiece, sc.ks);
+                            for (int k = k0; k < k1; ++k) {
+                                if (!mbar_wait(&sm.full[s], ph, sm.abort_flag, status)) goto mma_done;
+                                ++n_used;
+                                tc_fence_after();
+                                const uint32_t st = smem_u32(sm.stages + s * kLgStageBytes);
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    umma_pair_f16(acc, desc_kmajor(st + kk * 32), desc_kmajor(st + 16384 + kk * 32), idesc,
+                                                  (k == k0 && kk == 0) ? 0u : 1u);
+                                umma_pair_commit_both(&sm.empty[s]);
+                                if (++s == kLgStages) {
+                                    s = 0;
+                                    ph ^= 1u;
+                                }
+                            }
+                            umma_pair_commit_both(&sm.acc_full[b]);
+                        }
+                }
+            mma_done:
+                sm.ld_count[1] = n_used;
+                umma_pair_commit(sm.drain);
+                {
+                    const uint32_t a = smem_u32(sm.drain);
+                    const uint64_t t0 = globaltimer();
+                    while (!mbar_try_wait(a, 0)) {
+                        if (globaltimer() - t0 > kWaitTimeoutNs) {
+                            atomicCAS(status, 0, GRPO_ERR_TIMEOUT);
+                            break;
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    // The end of tc_pair_body: after an abort in either CTA, the loads in
+    // flight land before either CTA leaves; nobody leaves before both are done.
+    cluster_sync();
+    if (leader && threadIdx.x == 0) {
+        const uint32_t peer_cnt = map_cluster(smem_u32(const_cast<int*>(sm.ld_count)), 1);
+        const uint32_t peer_abort = map_cluster(smem_u32(const_cast<int*>(sm.abort_flag)), 1);
+        const int peer_issued = static_cast<int>(ld_shared_cluster_u32(peer_cnt));
+        const bool aborted = *sm.abort_flag || ld_shared_cluster_u32(peer_abort) != 0;
+        int settled = 1;
+        if (aborted) {
+            const int issued = sm.ld_count[0], used = sm.ld_count[1];
+            const int both = min(issued, peer_issued);
+            settled = wait_inflight<kLgStages>(sm.full, used, both) && issued == peer_issued ? 1 : 0;
+        }
+        sm.ld_count[2] = settled;
+        st_shared_cluster_u32(peer_cnt + 8u, static_cast<uint32_t>(settled));
+    }
+    cluster_sync();
+    if (!sm.ld_count[2]) abort_grace(sm.abort_flag, true);
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+template <bool kBf16, bool kKeep, bool kEnt>
+__global__ void __launch_bounds__(kHeadThreads, 1)
+    head_logits_kernel(const __grid_constant__ LogitsParams p, const __grid_constant__ CUtensorMap mA,
+                       const __grid_constant__ CUtensorMap mB) {
+    lg_body<kBf16, kKeep, kEnt>(p, mA, mB);
+}
+
+template <class K>
+cudaError_t launch_logits(K kern, const LogitsParams& p, const CUtensorMap& a, const CUtensorMap& b, int n_sm,
+                          cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLgSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.blockDim = dim3(kHeadThreads);
+    cfg.dynamicSmemBytes = kLgSmem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = n_sm / 2;
+    cfg.gridDim = dim3(clusters * 2);
+    int active = 0;
+    if (cudaOccupancyMaxActiveClusters(&active, kern, &cfg) == cudaSuccess && active > 0 && active < clusters)
+        clusters = active;
+    if (clusters < 1) return cudaErrorInvalidConfiguration;
+    cfg.gridDim = dim3(clusters * 2);
+    return cudaLaunchKernelEx(&cfg, kern, p, a, b);
+}
+
+// ====================================================================== few rows
+// z^T = W . h^T: a tile is 128 vocabulary rows (M) by kNC hidden rows (N), so
+// W goes through shared memory once and nothing else of size does.  A thread
+// owns one vocabulary row of the tile: its columns are the hidden rows, whose
+// running (max, sum exp, sum z exp) it keeps over all of its CTA's tiles; the
+// 128 threads are joined once at the end, and the last CTA to finish joins the
+// CTAs' partials.  The bytes of W are the floor.
+template <int kNC>
+struct FewShape {
+    static constexpr int kStageBytes = 16384 + kNC * 128;
+    static constexpr int kStages = 200 * 1024 / kStageBytes;
+    static constexpr int kSmem = kStages * kStageBytes + 1024 + 512;
+};
+
+template <bool kBf16, int kNC>
+__global__ void __launch_bounds__(kThreads, 1)
+    head_few_kernel(const __grid_constant__ FewParams p, const __grid_constant__ CUtensorMap mH,
+                    const __grid_constant__ CUtensorMap mW) {
+    using F = FewShape<kNC>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int s_tok[kNC];
+    __shared__ float s_part[4][kNC][3];
+    __shared__ int s_last;
+    Smem sm = carve_smem<F::kStages, F::kStageBytes>(smem_raw);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    int* status = p.status;
+    const int ks = p.d / kBK;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < F::kStages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sm.acc_full[b], 1);
+            mbar_init(&sm.acc_empty[b], 4);
+        }
+        mbar_init(sm.drain, 1);
+        *sm.abort_flag = 0;
+        sm.ld_count[0] = sm.ld_count[1] = sm.ld_count[2] = 0;
+        fence_barrier_init();
+    }
+    if (threadIdx.x < kNC) s_tok[threadIdx.x] = static_cast<int>(threadIdx.x) < p.N ? p.tokens[threadIdx.x] : -1;
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&mH);
+        tma_prefetch_desc(&mW);
+    }
+    if (warp == 1) {
+        tmem_alloc(sm.tmem_slot, 2 * kNC);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *sm.tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0, n_issued = 0;
+            uint32_t ph = 0;
+            for (int tile = blockIdx.x; tile < p.n_tiles; tile += gridDim.x)
+                for (int k = 0; k < ks; ++k) {
+                    if (!mbar_wait(&sm.empty[s], ph ^ 1u, sm.abort_flag, status)) goto producer_done;
+                    uint8_t* st = sm.stages + s * F::kStageBytes;
+                    mbar_arrive_expect_tx(&sm.full[s], F::kStageBytes);
+                    tma_load_2d(&mW, &sm.full[s], st, k * kBK, tile * kFewVocab);
+                    tma_load_2d(&mH, &sm.full[s], st + 16384, k * kBK, 0);
+                    ++n_issued;
+                    if (++s == F::kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+        producer_done:
+            sm.ld_count[0] = n_issued;
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = make_idesc_f16(128, kNC, kBf16, false, false);
+            int s = 0, n_used = 0, it = 0;
+            uint32_t ph = 0;
+            for (int tile = blockIdx.x; tile < p.n_tiles; tile += gridDim.x)
+                for (int k0 = 0; k0 < ks; k0 += kStagesPerPiece, ++it) {
+                    const int b = it & 1;
+                    if (!mbar_wait(&sm.acc_empty[b], ((it >> 1) & 1u) ^ 1u, sm.abort_flag, status)) goto mma_done;
+                    tc_fence_after();
+                    const int k1 = min(k0 + kStagesPerPiece, ks);
+                    for (int k = k0; k < k1; ++k) {
+                        if (!mbar_wait(&sm.full[s], ph, sm.abort_flag, status)) goto mma_done;
+                        ++n_used;
+                        tc_fence_after();
+                        const uint32_t st = smem_u32(sm.stages + s * F::kStageBytes);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_f16(tmem + b * kNC, desc_kmajor(st + kk * 32), desc_kmajor(st + 16384 + kk * 32), idesc,
+                                     (k == k0 && kk == 0) ? 0u : 1u);
+                        umma_commit(&sm.empty[s]);
+                        if (++s == F::kStages) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                    umma_commit(&sm.acc_full[b]);
+                }
+        mma_done:
+            sm.ld_count[1] = n_used;
+            umma_commit(sm.drain);
+            {
+                const uint32_t a = smem_u32(sm.drain);
+                const uint64_t t0 = globaltimer();
+                while (!mbar_try_wait(a, 0)) {
+                    if (globaltimer() - t0 > kWaitTimeoutNs) {
+                        atomicCAS(status, 0, GRPO_ERR_TIMEOUT);
+                        break;
+                    }
+                }
+            }
+        }
+    } else {
+        const int quarter = warp & 3;
+        const uint32_t tq = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+        float m[kNC], s[kNC], u[kNC];
+#pragma unroll
+        for (int n = 0; n < kNC; ++n) {
+            m[n] = kNoLogit2;
+            s[n] = u[n] = 0.f;
+        }
+        int it = 0;
+        for (int tile = blockIdx.x; tile < p.n_tiles; tile += gridDim.x) {
+            float a[kNC];
+            for (int k0 = 0; k0 < ks; k0 += kStagesPerPiece, ++it) {
+                const int b = it & 1;
+                if (!mbar_wait(&sm.acc_full[b], (it >> 1) & 1u, sm.abort_flag, status)) goto epi_done;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < kNC / 16; ++c) {
+                    float v[16];
+                    tmem_ld16(tq + b * kNC + 16 * c, v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) a[16 * c + j] = k0 == 0 ? v[j] : a[16 * c + j] + v[j];
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.acc_empty[b]);
+            }
+            const int vr = tile * kFewVocab + 32 * quarter + lane;
+#pragma unroll
+            for (int n = 0; n < kNC; ++n) {
+                const float z = vr < p.V && vr != s_tok[n] ? a[n] * p.zscale : kNoLogit;
+                const float mn = fmaxf(m[n], z * kLog2e);
+                const float f = fast_exp2(m[n] - mn), x = fast_exp2(fmaf(z, kLog2e, -mn));
+                s[n] = fmaf(s[n], f, x);
+                u[n] = fmaf(u[n], f, x * z);
+                m[n] = mn;
+            }
+        }
+        // the 32 vocabulary rows of the warp, then the four warps through shared memory
+#pragma unroll
+        for (int n = 0; n < kNC; ++n) {
+            float mw = m[n];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, o));
+            const float f = fast_exp2(m[n] - mw);
+            float sw = s[n] * f, uw = u[n] * f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                sw += __shfl_xor_sync(0xffffffffu, sw, o);
+                uw += __shfl_xor_sync(0xffffffffu, uw, o);
+            }
+            if (lane == 0) {
+                s_part[quarter][n][0] = mw;
+                s_part[quarter][n][1] = sw;
+                s_part[quarter][n][2] = uw;
+            }
+        }
+    epi_done:;
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (*sm.abort_flag) {
+        if (threadIdx.x == 0)
+            sm.ld_count[2] = wait_inflight<F::kStages>(sm.full, sm.ld_count[1], sm.ld_count[0]) ? 1 : 0;
+        __syncthreads();
+        if (!sm.ld_count[2]) abort_grace(sm.abort_flag);
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 2 * kNC);
+    }
+    // this CTA's partial of each row
+    const int n_cta = static_cast<int>(gridDim.x);
+    if (static_cast<int>(threadIdx.x) < min(kNC, p.N)) {
+        const int n = threadIdx.x;
+        float mm = s_part[0][n][0], ss = 0.f, uu = 0.f;
+#pragma unroll
+        for (int w = 1; w < 4; ++w) mm = fmaxf(mm, s_part[w][n][0]);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float f = exp2f(s_part[w][n][0] - mm);
+            ss = fmaf(s_part[w][n][1], f, ss);
+            uu = fmaf(s_part[w][n][2], f, uu);
+        }
+        p.part[static_cast<int64_t>(n) * n_cta + blockIdx.x] = make_float4(mm, ss, uu, 0.f);
+        __threadfence();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) s_last = atomicAdd(p.counter, 1) == n_cta - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    for (int n = warp; n < p.N; n += kThreads / 32) {
+        const int tok = s_tok[n];
+        const bool on = !p.mask || p.mask[n] != 0;
+        const bool ok = tok >= 0 && tok < p.V;
+        RowSum r{0.0, 0.0, 0.f};
+        if (on && ok) r = join_row(p.part + static_cast<int64_t>(n) * n_cta, n_cta, lane, p.zt[n]);
+        if (lane == 0) {
+            if (on && !ok) atomicCAS(status, 0, GRPO_ERR_SHAPE);
+            p.logp[n] = static_cast<float>(r.q);
+            if (p.entropy) p.entropy[n] = r.ent;
+        }
+    }
+}
+
+// ====================================================================== dH, last wave split
+struct HeadDhT : DhPairT {
+    using Params = HeadChunkParams;
+    struct Sched : ChunkSched {
+        int n_full, pieces, rem, kper;
+    };
+    struct Coord {
+        int m0, n0, k0;
+    };
+    __device__ static bool setup(const Params& p, Sched& sc) {
+        if (!DhPairT::setup(p, sc)) return false;
+        const int units = sc.n_units;
+        const int2 plan = p.dh_plan[p.chunk];
+        sc.n_full = plan.x;
+        sc.pieces = plan.y;
+        sc.rem = units - plan.x;
+        sc.kper = (sc.ks + plan.y - 1) / plan.y;
+        sc.n_units = sc.n_full + sc.rem * sc.pieces;
+        return sc.n_units > 0;
+    }
+    // unit -> (tile unit, K piece; -1 for all of K).  Pieces are the slow index: the
+    // tiles of one K range run together and share its W rows in L2.
+    __device__ static int2 piece(const Sched& sc, int unit) {
+        if (unit < sc.n_full) return make_int2(unit, -1);
+        const int r = unit - sc.n_full;
+        return make_int2(sc.n_full + r % sc.rem, r / sc.rem);
+    }
+    __device__ static int ksteps(const Params&, const Sched& sc, int unit) {
+        const int2 u = piece(sc, unit);
+        return u.y < 0 ? sc.ks : min(sc.kper, sc.ks - u.y * sc.kper);
+    }
+    __device__ static Coord coord(const Params&, const Sched& sc, int unit, int, int rank) {
+        const int2 u = piece(sc, unit);
+        return Coord{mtile(sc, u.x, rank) * kBM, dtile(sc, u.x) * kBN, u.y < 0 ? 0 : u.y * sc.kper};
+    }
+    __device__ static uint32_t tx_bytes(const Params& p, const Sched&, const Coord& c) {
+        return 2 * 16384 + 8192 * min(4, (p.d - c.n0) / 64);
+    }
+    __device__ static void load(const Params& p, const Sched& sc, const Coord& c, int k, uint8_t* st, uint32_t bar,
+                                const CUtensorMap* mA, const CUtensorMap* mA2, const CUtensorMap* mB, int rank) {
+        DhPairT::load(p, sc, DhPairT::Coord{c.m0, c.n0}, c.k0 + k, st, bar, mA, mA2, mB, rank);
+    }
+    __device__ static void epi_begin(const Params&, const Sched&, int, int, int, Epi&) {}
+    template <bool kBf16>
+    __device__ static void epi_item(const Params& p, const Sched& sc, int unit, int, int rank, uint32_t tacc, Epi&) {
+        const int row = (threadIdx.x & 31) + 32 * ((threadIdx.x >> 5) & 3);
+        const int2 u = piece(sc, unit);
+        const int slot = mtile(sc, u.x, rank) * kBM + row;
+        const int n0 = dtile(sc, u.x) * kBN;
+        bool valid = slot < sc.n_c;
+        if (!__any_sync(0xffffffffu, valid)) return;
+        if (u.y >= 0) {
+            // partial tile: [piece][tile][256 rows][256 columns] fp32
+            const int64_t tile = static_cast<int64_t>(u.y) * sc.rem + (u.x - sc.n_full);
+            float* out = p.dh_part + ((tile * 2 + rank) * kBM + row) * kBN;
+#pragma unroll 1
+            for (int c = 0; c < kBN / 32; ++c) {
+                if (n0 + c * 32 >= p.d) break;
+                float v[32];
+                tmem_ld32(tacc + c * 32, v);
+                if (valid) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        st_global_v8(out + c * 32 + 8 * h, __float_as_uint(v[8 * h]), __float_as_uint(v[8 * h + 1]),
+                                     __float_as_uint(v[8 * h + 2]), __float_as_uint(v[8 * h + 3]),
+                                     __float_as_uint(v[8 * h + 4]), __float_as_uint(v[8 * h + 5]),
+                                     __float_as_uint(v[8 * h + 6]), __float_as_uint(v[8 * h + 7]));
+                }
+            }
+            return;
+        }
+        const int t = valid ? p.rows[sc.c0 + slot] : 0;
+        if (valid && !GRPO_DCHECK(t >= 0 && t < p.N, p.status)) valid = false;
+        uint16_t* out = p.dH + static_cast<int64_t>(t) * p.d;
+        bool bad = false;
+#pragma unroll 1
+        for (int c = 0; c < kBN / 32; ++c) {
+            const int col0 = n0 + c * 32;
+            if (col0 >= p.d) break;
+            float v[32];
+            tmem_ld32(tacc + c * 32, v);
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+                v[j] *= sc.winv;
+                v[j + 1] *= sc.winv;
+                pk[j / 2] = pack2(v[j], v[j + 1], kBf16);
+                bad |= !kBf16 ? half2_nonfinite(pk[j / 2]) : !(isfinite(v[j]) && isfinite(v[j + 1]));
+            }
+            if (valid) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    st_global_v8(out + col0 + 16 * h, pk[8 * h], pk[8 * h + 1], pk[8 * h + 2], pk[8 * h + 3],
+                                 pk[8 * h + 4], pk[8 * h + 5], pk[8 * h + 6], pk[8 * h + 7]);
+            }
+        }
+        if (bad && valid) atomicOr(p.found_inf, 1);
+    }
+    __device__ static void epi_end(const Params&, const Sched&, int, Epi&) {}
+};
+
+// ====================================================================== dW
+// DwPairT with the operators' output: chunks add up in fp32 (dw_acc), and with
+// dw16 the last chunk (often the only one) rounds the sum to the type of W.
+struct HeadDwT : DwPairT {
+    using Params = HeadChunkParams;
+    template <bool kBf16>
+    __device__ static void epi_item(const Params& p, const Sched& sc, int unit, int, int rank, uint32_t tacc, Epi&) {
+        const int row = (threadIdx.x & 31) + 32 * ((threadIdx.x >> 5) & 3);
+        const int v = vtile(sc, unit, rank) * kBM + row;
+        const int n0 = dtile(sc, unit) * kBN;
+        const bool valid = v < p.V;
+        if (!__any_sync(0xffffffffu, valid)) return;
+        const bool first = p.chunk == 0;
+        const bool last = p.dw16 && p.chunk + 1 == p.counts[C_NCHUNKS];
+        const int64_t at = static_cast<int64_t>(valid ? v : 0) * p.d;
+        bool bad = false;
+#pragma unroll 1
+        for (int c = 0; c < kBN / 32; ++c) {
+            const int col0 = n0 + c * 32;
+            if (col0 >= p.d) break;
+            float x[32];
+            tmem_ld32(tacc + c * 32, x);
+            if (!valid) continue;
+            float* acc = p.dw_acc + at + col0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] *= sc.winv;
+            if (!first) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float prev[8];
+                    ld_global_v8(acc + 8 * j, prev);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[8 * j + i] += prev[i];
+                }
+            }
+            if (last) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    pk[j] = pack2(x[2 * j], x[2 * j + 1], kBf16);
+                    bad |= !kBf16 ? half2_nonfinite(pk[j]) : !(isfinite(x[2 * j]) && isfinite(x[2 * j + 1]));
+                }
+                uint16_t* out = p.dw16 + at + col0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    st_global_v8(out + 16 * h, pk[8 * h], pk[8 * h + 1], pk[8 * h + 2], pk[8 * h + 3], pk[8 * h + 4],
+                                 pk[8 * h + 5], pk[8 * h + 6], pk[8 * h + 7]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) bad |= !isfinite(x[j]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    st_global_v8(acc + 8 * j, __float_as_uint(x[8 * j]), __float_as_uint(x[8 * j + 1]),
+                                 __float_as_uint(x[8 * j + 2]), __float_as_uint(x[8 * j + 3]),
+                                 __float_as_uint(x[8 * j + 4]), __float_as_uint(x[8 * j + 5]),
+                                 __float_as_uint(x[8 * j + 6]), __float_as_uint(x[8 * j + 7]));
+            }
+        }
+        if (bad) atomicOr(p.found_inf, 1);
+    }
+};
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    head_dh_kernel(const __grid_constant__ HeadChunkParams p, const __grid_constant__ CUtensorMap mA,
+                   const __grid_constant__ CUtensorMap mA2, const __grid_constant__ CUtensorMap mB) {
+    tc_pair_body<HeadDhT, kBf16>(p, mA, mA2, mB);
+}
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    head_dw_kernel(const __grid_constant__ HeadChunkParams p, const __grid_constant__ CUtensorMap mA,
+                   const __grid_constant__ CUtensorMap mA2, const __grid_constant__ CUtensorMap mB) {
+    tc_pair_body<HeadDwT, kBf16>(p, mA, mA2, mB);
+}
+
+}  // namespace
+
+cudaError_t launch_head_logits(const LogitsParams& p, const CUtensorMap& mH, const CUtensorMap& mW, int n_sm, bool bf16,
+                               bool keep, bool entropy, cudaStream_t st) {
+    if (keep)
+        return bf16 ? launch_logits(head_logits_kernel<true, true, false>, p, mH, mW, n_sm, st)
+                    : launch_logits(head_logits_kernel<false, true, false>, p, mH, mW, n_sm, st);
+    if (entropy)
+        return bf16 ? launch_logits(head_logits_kernel<true, false, true>, p, mH, mW, n_sm, st)
+                    : launch_logits(head_logits_kernel<false, false, true>, p, mH, mW, n_sm, st);
+    return bf16 ? launch_logits(head_logits_kernel<true, false, false>, p, mH, mW, n_sm, st)
+                : launch_logits(head_logits_kernel<false, false, false>, p, mH, mW, n_sm, st);
+}
+
+cudaError_t launch_head_dh(const HeadChunkParams& p, const CUtensorMap& mDS, const CUtensorMap& mWmn, int n_sm, bool bf16,
+                           cudaStream_t st) {
+    return bf16 ? launch_tc<HeadDhT, 2>(head_dh_kernel<true>, p, mDS, mDS, mWmn, n_sm, st)
+                : launch_tc<HeadDhT, 2>(head_dh_kernel<false>, p, mDS, mDS, mWmn, n_sm, st);
+}
+
+cudaError_t launch_head_dw(const HeadChunkParams& p, const CUtensorMap& mDSmn, const CUtensorMap& mHct, int n_sm, bool bf16,
+                           cudaStream_t st) {
+    return bf16 ? launch_tc<HeadDwT, 2>(head_dw_kernel<true>, p, mDSmn, mDSmn, mHct, n_sm, st)
+                : launch_tc<HeadDwT, 2>(head_dw_kernel<false>, p, mDSmn, mDSmn, mHct, n_sm, st);
+}
+
+template <bool kBf16, int kNC>
+static cudaError_t launch_few_t(const FewParams& p, const CUtensorMap& mH, const CUtensorMap& mW, int grid, cudaStream_t st) {
+    auto kern = head_few_kernel<kBf16, kNC>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, FewShape<kNC>::kSmem);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, kThreads, FewShape<kNC>::kSmem, st>>>(p, mH, mW);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_few(const FewParams& p, const CUtensorMap& mH, const CUtensorMap& mW, int grid, bool bf16, int nc,
+                       cudaStream_t st) {
+    if (nc <= 16)
+        return bf16 ? launch_few_t<true, 16>(p, mH, mW, grid, st) : launch_few_t<false, 16>(p, mH, mW, grid, st);
+    return bf16 ? launch_few_t<true, 32>(p, mH, mW, grid, st) : launch_few_t<false, 32>(p, mH, mW, grid, st);
+}
+
+}  // namespace grpo

@@ -148,6 +148,10 @@ struct ChunkParams {
     const uint8_t* wq;      // 8-bit W [V x d]
     float scale_h, scale_w; // per-tensor scales of the 8-bit h_pol and W
     int e5m2;               // code format: E5M2 (1) or E4M3 (0)
+    // the head operators (head.h): chunk c holds the valid rows cb[c] .. cb[c+1]-1
+    // and its gradients are multiplied by oscale[c]
+    const int* cb = nullptr;
+    const float* oscale = nullptr;
 };
 
 struct MergeParams {

@@ -108,12 +108,18 @@ struct ChunkSched {
 
 __device__ __forceinline__ bool chunk_setup(const ChunkParams& p, ChunkSched& sc, int C) {
     if (p.chunk >= p.counts[C_NCHUNKS]) return false;
-    const int rc = p.counts[C_CHUNK_ROWS];
     sc.C = C;
-    sc.c0 = p.chunk * rc;
-    sc.n_c = min(rc, p.counts[C_NVALID] - sc.c0);
+    if (p.cb) {
+        sc.c0 = p.cb[p.chunk];
+        sc.n_c = p.cb[p.chunk + 1] - sc.c0;
+        sc.winv = p.oscale[p.chunk];
+    } else {
+        const int rc = p.counts[C_CHUNK_ROWS];
+        sc.c0 = p.chunk * rc;
+        sc.n_c = min(rc, p.counts[C_NVALID] - sc.c0);
+        sc.winv = __int_as_float(p.counts[C_WINV]);
+    }
     sc.n_mt = (sc.n_c + kBM - 1) / kBM;
-    sc.winv = __int_as_float(p.counts[C_WINV]);
     return sc.n_c > 0;
 }
 

@@ -1,0 +1,436 @@
+"""Log-probs, clipped policy loss and preference loss on the GPU against their fp64 definitions, element by element,
+within bounds counted from the roundings the operators make (head_reference.py)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import head_reference as R
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+import rl_fine_tuning_gb300 as rg  # noqa: E402
+
+TORCH = {"bf16": torch.bfloat16, "fp16": torch.float16}
+CODE = {"bf16": rg.BF16, "fp16": rg.FP16}
+
+
+def host(x):
+    return x.double().cpu().numpy()
+
+
+class Case:
+    """Random inputs on the device, and their exact values as a reference problem."""
+
+    def __init__(self, n_groups, G, L, d, V, dtype="bf16", mask="ragged", T=1.0, seed=0, chunk_rows=0, likely=True,
+                 beta=0.04, loss_mode=0, hscale=1.0):
+        g = torch.Generator().manual_seed(seed)
+        rng = np.random.default_rng(seed)
+        N, n = n_groups * G * L, n_groups * G
+        W = (torch.randn(V, d, generator=g) * d ** -0.5).to(TORCH[dtype])
+        tok = torch.randint(0, V, (N,), generator=g, dtype=torch.int32)
+        h = hscale * torch.randn(N, d, generator=g)
+        if likely:
+            h = h + (2 + 10 * torch.rand(N, 1, generator=g)) * W[tok.long()].float()
+        h = h.to(TORCH[dtype])
+        if mask == "ragged":
+            lens = rng.integers(0, L + 1, n)
+            lens[rng.integers(0, n)] = L
+            m = (np.arange(L)[None] < lens[:, None]).reshape(-1)
+        elif mask == "holes":
+            m = rng.random(N) < 0.5
+        elif mask == "none":
+            m = np.zeros(N, bool)
+        elif mask == "one":
+            m = np.zeros(N, bool)
+            m[N // 2] = True
+        else:
+            m = np.ones(N, bool)
+        self.P = R.Problem(n_groups, G, L, h.double().numpy(), W.double().numpy(), tok.numpy(), m, float(np.float32(T)))
+        self.dtype, self.T, self.n = dtype, T, n
+        self.shape = rg.make_shape(n_groups, G, L, d, V, CODE[dtype], beta=beta, chunk_rows=chunk_rows, loss_mode=loss_mode)
+        self.beta = float(np.float32(beta))
+        self.seq_mean = bool(loss_mode)
+        self.h, self.W, self.tok = h.cuda(), W.cuda(), tok.cuda()
+        self.mask = torch.from_numpy(m.astype(np.uint8)).cuda()
+        self.status = torch.full((1,), 9, dtype=torch.int32, device="cuda")
+        self.inf = torch.full((1,), 9, dtype=torch.int32, device="cuda")
+        self.rng = rng
+
+    def ws(self, op, dw_f32=False):
+        # 0xFF everywhere: what the operators read of it, they have to write first
+        return torch.full((rg.grpo_policy_workspace_bytes(self.shape, op, dw_f32),), 255, dtype=torch.uint8, device="cuda")
+
+    def f32(self, *n):
+        return torch.full(n, 7.0, dtype=torch.float32, device="cuda")
+
+    def grads(self, dw_f32=False):
+        return (torch.full_like(self.h, 7.0), torch.full_like(self.W, 7.0, dtype=torch.float32 if dw_f32 else self.W.dtype))
+
+    def logp(self, entropy=True, mask=True):
+        q, e = self.f32(len(self.tok)), self.f32(len(self.tok)) if entropy else None
+        rg.grpo_logprobs(self.h, self.W, self.tok, self.mask if mask else None, self.shape, self.T, self.ws("logp"), q, e,
+                         self.status)
+        torch.cuda.synchronize()
+        return q, e
+
+    def logp_bwd(self, dq, scale=1.0, dw_f32=False):
+        dH, dW = self.grads(dw_f32)
+        rg.grpo_logprobs_bwd(self.h, self.W, self.tok, self.mask, dq, self.shape, self.T, scale,
+                             self.ws("logp_grad", dw_f32), dH, dW, self.inf, self.status, dw_f32=dw_f32)
+        torch.cuda.synchronize()
+        return dH, dW
+
+    def clip(self, adv, old, ref, opts, scale=1.0, bwd=True):
+        loss, st = self.f32(1), self.f32(len(self.tok), 3)
+        ws = self.ws("clip", opts.dw_f32)
+        if not bwd:
+            rg.grpo_clip_loss_fwd(self.h, self.W, self.tok, self.mask, adv, old, ref, self.shape, opts, ws, loss, st,
+                                  self.status)
+            torch.cuda.synchronize()
+            return loss, st
+        dH, dW = self.grads(opts.dw_f32)
+        rg.grpo_clip_loss_fwd_bwd(self.h, self.W, self.tok, self.mask, adv, old, ref, self.shape, opts, scale, ws, loss, dH,
+                                  dW, self.inf, st, self.status)
+        torch.cuda.synchronize()
+        return loss, st, dH, dW
+
+    def pair(self, ref, opts, scale=1.0, bwd=True):
+        loss, q, st = self.f32(1), self.f32(len(self.tok)), self.f32(self.shape.n_groups, 4)
+        ws = self.ws("pair", opts.dw_f32)
+        if not bwd:
+            rg.grpo_pair_loss_fwd(self.h, self.W, self.tok, self.mask, ref, self.shape, opts, ws, loss, q, st, self.status)
+            torch.cuda.synchronize()
+            return loss, q, st
+        dH, dW = self.grads(opts.dw_f32)
+        rg.grpo_pair_loss_fwd_bwd(self.h, self.W, self.tok, self.mask, ref, self.shape, opts, scale, ws, loss, dH, dW,
+                                  self.inf, q, st, self.status)
+        torch.cuda.synchronize()
+        return loss, q, st, dH, dW
+
+    def old_ref(self, spread=0.15, away=1e-3, lo=0.2, hi=0.28):
+        """Stored log-probs whose ratios stay `away` from the clip borders (fp32 values, exact in the reference)."""
+        q = R.logp_entropy(self.P)[0]
+        lr = spread * self.rng.normal(size=len(q))
+        near = (np.abs(np.exp(lr) - (1 - lo)) < away) | (np.abs(np.exp(lr) - (1 + hi)) < away)
+        old = (q - np.where(near, lr + 5 * away, lr)).astype(np.float32)
+        ref = (q + 0.3 * self.rng.normal(size=len(q))).astype(np.float32)
+        # masked rows are never read: not even a NaN there may show
+        old[~self.P.mask] = np.nan
+        ref[~self.P.mask] = np.inf
+        return old, ref
+
+
+def clean(x, mask):
+    return np.where(mask, np.nan_to_num(x.astype(np.float64), posinf=0, neginf=0), 0.0)
+
+
+def check_logp(c, q, ent):
+    rq, re, _ = R.logp_entropy(c.P)
+    bound = R.logp_bound(c.P)
+    assert int(c.status) == 0
+    assert np.all(np.abs(host(q) - rq) <= bound), np.max(np.abs(host(q) - rq) / bound)
+    assert not host(q)[~c.P.mask].any()
+    if ent is not None:
+        V = c.P.W.shape[0]
+        eb = bound * (2 + np.log(V)) + 1e-6 * (1 + np.abs(R.logits(c.P)).max(1))
+        assert np.all(np.abs(host(ent) - re) <= eb), np.max(np.abs(host(ent) - re) / eb)
+        assert not host(ent)[~c.P.mask].any()
+
+
+def check_grads(c, dH, dW, g, lp, scale=1.0, dw_f32=False):
+    rH, rW, aH, aW = R.gradients(c.P, g, lp)
+    q_err = R.logp_bound(c.P).max()
+    assert int(c.status) == 0 and int(c.inf) == 0
+    bH = R.grad_bound(scale * rH, scale * aH, c.dtype, c.dtype, q_err, scale)
+    bW = R.grad_bound(scale * rW, scale * aW, c.dtype, "f32" if dw_f32 else c.dtype, q_err, scale)
+    eH, eW = np.abs(host(dH) - scale * rH), np.abs(host(dW) - scale * rW)
+    assert np.all(eH <= bH), ("dH", np.max(eH / bH))
+    assert np.all(eW <= bW), ("dW", np.max(eW / bW))
+    assert not host(dH)[~c.P.mask].any()
+
+
+# (n_groups, G, L, d, V, dtype, mask, chunk_rows)
+SHAPES = [
+    (1, 1, 1, 64, 1, "bf16", "all", 0),            # one token, a vocabulary of one: q = 0, no gradient
+    (1, 1, 1, 64, 7, "fp16", "all", 0),
+    (1, 2, 3, 128, 257, "bf16", "holes", 0),       # the few-row kernel, masked rows among them
+    (1, 8, 2, 192, 1000, "fp16", "all", 0),
+    (1, 17, 1, 320, 389, "bf16", "all", 0),        # 17 rows: the wider few-row kernel
+    (1, 32, 1, 64, 130, "bf16", "ragged", 0),
+    (1, 33, 1, 64, 130, "bf16", "ragged", 0),      # one row more: the chunked path
+    (2, 4, 37, 320, 1000, "bf16", "ragged", 0),
+    (1, 3, 211, 128, 515, "fp16", "holes", 128),   # five chunks
+    (1, 2, 300, 576, 333, "bf16", "all", 256),
+    (1, 1, 700, 64, 2049, "bf16", "ragged", 384),
+    (3, 2, 41, 1088, 64, "fp16", "ragged", 0),
+    (1, 4, 50, 128, 700, "bf16", "none", 0),       # no row counts
+    (1, 4, 50, 128, 700, "bf16", "one", 128),
+]
+
+
+@pytest.mark.parametrize("s", SHAPES, ids=str)
+@pytest.mark.parametrize("T", [1.0, 0.7])
+def test_logprobs(s, T):
+    n, G, L, d, V, dt, mask, cr = s
+    c = Case(n, G, L, d, V, dt, mask, T, seed=1, chunk_rows=cr)
+    check_logp(c, *c.logp())
+    q, _ = c.logp(entropy=False)
+    check_logp(c, q, None)
+    if mask == "all":
+        assert torch.equal(c.logp(mask=False)[0], c.logp()[0])
+
+
+def test_logprobs_are_exact_enough_to_sum():
+    """Sums of q over a completion: the tensor cores' rounding towards zero, left in, makes every logit of about 11 at
+    d = 4096 some 4e-5 too small; here the sum over 512 rows stays within 512 times 2e-6, the other roundings' size."""
+    c = Case(1, 1, 512, 4096, 1031, "bf16", "all", seed=5)
+    q, e = c.logp()
+    check_logp(c, q, e)
+    assert abs((host(q) - R.logp_entropy(c.P)[0]).sum()) <= 512 * 2e-6
+
+
+@pytest.mark.parametrize("s", SHAPES, ids=str)
+@pytest.mark.parametrize("dw_f32", [False, True])
+def test_logprobs_bwd(s, dw_f32):
+    n, G, L, d, V, dt, mask, cr = s
+    c = Case(n, G, L, d, V, dt, mask, 1.3, seed=2, chunk_rows=cr)
+    dq = c.rng.normal(size=len(c.tok)).astype(np.float32)
+    dq[~c.P.mask] = np.nan
+    dH, dW = c.logp_bwd(torch.from_numpy(dq).cuda(), 64.0, dw_f32)
+    check_grads(c, dH, dW, clean(dq, c.P.mask), R.logp_entropy(c.P)[2], 64.0, dw_f32)
+
+
+@pytest.mark.parametrize("size", [1e-7, 1.0, 1e4])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_logprobs_bwd_scales_with_its_input(size, dt):
+    """d loss / d q of any size: the fp16 dlogits keep their precision, the loss scale only places the outputs."""
+    c = Case(1, 2, 60, 128, 500, dt, "ragged", seed=3)
+    dq = (size * c.rng.normal(size=len(c.tok))).astype(np.float32)
+    dH, dW = c.logp_bwd(torch.from_numpy(dq).cuda(), 1.0 / size)
+    check_grads(c, dH, dW, clean(dq, c.P.mask), R.logp_entropy(c.P)[2], 1.0 / size)
+
+
+@pytest.mark.parametrize("s", SHAPES, ids=str)
+@pytest.mark.parametrize("beta,loss_mode,T", [(0.04, 0, 1.0), (0.0, 1, 1.5)])
+def test_clip_loss(s, beta, loss_mode, T):
+    n, G, L, d, V, dt, mask, cr = s
+    c = Case(n, G, L, d, V, dt, mask, T, seed=4, chunk_rows=cr, beta=beta, loss_mode=loss_mode)
+    old, ref = c.old_ref()
+    adv = c.rng.normal(size=c.n).astype(np.float32)
+    adv[::3] = 0.0
+    opts = rg.clip_opts(temperature=T, clip_low=0.2, clip_high=0.28)
+    scale = 256.0 if dt == "fp16" else 1.0
+    t = lambda x: torch.from_numpy(x).cuda()  # noqa: E731
+    loss, st, dH, dW = c.clip(t(adv), t(old), t(ref) if beta else None, opts, scale)
+    rl, rs, g, lp = R.clip_loss(c.P, adv, clean(old, c.P.mask), clean(ref, c.P.mask), c.beta, 0.2, 0.28, c.seq_mean)
+    qb = R.logp_bound(c.P)
+    sb = np.stack([qb, (qb + 4e-7) * rs[:, 1], qb * np.abs(np.expm1(0.3 * 6)) + 1e-6], 1)
+    assert np.all(np.abs(host(st) - rs) <= sb * c.P.mask[:, None]), np.max(np.abs(host(st) - rs) / (sb + 1e-30))
+    per = (np.abs(adv).max(initial=0) * rs[:, 1].max(initial=0) + c.beta * 6) * qb.max() + 2e-6
+    assert abs(float(loss) - rl) <= per
+    check_grads(c, dH, dW, g, lp, scale)
+    l2, s2 = c.clip(t(adv), t(old), t(ref) if beta else None, opts, bwd=False)
+    assert torch.equal(l2, loss) and torch.equal(s2, st)
+
+
+@pytest.mark.parametrize("A,r,kept", [(1.0, 2.0, False), (1.0, 0.5, True), (-1.0, 2.0, True), (-1.0, 0.5, False),
+                                      (0.0, 2.0, True)])
+def test_clip_cuts_on_the_right_side(A, r, kept):
+    c = Case(1, 1, 40, 64, 100, "bf16", "all", seed=6, beta=0.0)
+    q = R.logp_entropy(c.P)[0]
+    old = torch.from_numpy((q - np.log(r)).astype(np.float32)).cuda()
+    _, st, dH, dW = c.clip(torch.full((1,), A, device="cuda"), old, None, rg.clip_opts())
+    assert bool(dH.any()) == (kept and A != 0) and bool(dW.any()) == (kept and A != 0)
+    np.testing.assert_allclose(host(st)[:, 1], r, rtol=1e-4)
+
+
+def test_clip_without_an_upper_border():
+    c = Case(1, 1, 40, 64, 100, "bf16", "all", seed=6, beta=0.0)
+    old = torch.from_numpy((R.logp_entropy(c.P)[0] - 2).astype(np.float32)).cuda()
+    _, _, dH, _ = c.clip(torch.ones(1, device="cuda"), old, None, rg.clip_opts(clip_high=float("inf")))
+    assert bool(dH.any())
+
+
+PAIRS = [(n, L, d, V, dt, mask, cr) for n, L, d, V, dt, mask, cr in [
+    (1, 1, 64, 5, "bf16", "all", 0),
+    (3, 37, 128, 515, "bf16", "ragged", 0),
+    (5, 50, 320, 300, "fp16", "holes", 128),       # one pair a chunk
+    (7, 30, 192, 260, "bf16", "ragged", 256),      # several pairs a chunk, uneven
+    (2, 150, 128, 700, "bf16", "ragged", 128),     # a pair does not fit: the logits twice
+    (2, 150, 128, 700, "fp16", "all", 256),
+    (4, 20, 64, 130, "bf16", "none", 0),
+    (4, 20, 64, 130, "bf16", "one", 0),
+]]
+
+
+@pytest.mark.parametrize("s", PAIRS, ids=str)
+@pytest.mark.parametrize("kind,e,mean,beta", [("sigmoid", 0.0, False, 0.1), ("sigmoid", 0.1, True, 2.0),
+                                              ("hinge", 0.0, False, 0.05), ("square", 0.0, True, 0.5)])
+def test_pair_loss(s, kind, e, mean, beta):
+    n, L, d, V, dt, mask, cr = s
+    c = Case(n, 2, L, d, V, dt, mask, seed=7, chunk_rows=cr, beta=beta)
+    _, ref = c.old_ref()
+    opts = rg.pair_opts(kind, e, mean)
+    scale = 16.0 if dt == "fp16" else 1.0
+    ref_d = torch.from_numpy(ref).cuda()
+    loss, q, st, dH, dW = c.pair(ref_d, opts, scale)
+    rl, rs, g, lp = R.pair_loss(c.P, clean(ref, c.P.mask), c.beta, kind, float(np.float32(e)), mean)
+    check_logp(c, q, None)
+    qb = R.logp_bound(c.P).max() + 1e-7 * np.abs(lp[np.arange(len(ref)), c.P.tokens]).max()
+    S_err = (1 if mean else L) * qb
+    step = max(1.0, np.abs(rs).max())
+    assert np.all(np.abs(host(st)[:, :3] - rs[:, :3]) <= 2 * c.beta * S_err + 1e-6 * step)
+    slope = 1.0 if kind != "square" else 2 * np.abs(rs[:, 2] / c.beta - 0.5 / c.beta).max() / c.beta + 1
+    lb = slope * (2 * c.beta * S_err) + 1e-6 * step
+    assert abs(float(loss) - rl) <= lb and np.all(np.abs(host(st)[:, 3] - rs[:, 3]) <= lb)
+    # d loss / d q moves with the margin: its error is that of q times the curvature, at most 1 (square: 2)
+    extra = (2 * c.beta * S_err) * 2 / max(1e-30, 1.0)
+    rH, rW, aH, aW = R.gradients(c.P, g, lp)
+    full = np.where(c.P.mask, (2 if kind == "square" else c.beta) / np.maximum(1, int(c.P.mask.any())), 0.0)
+    _, _, xH, xW = R.gradients(c.P, full, lp)
+    assert int(c.status) == 0 and int(c.inf) == 0
+    qe = R.logp_bound(c.P).max()
+    bH = R.grad_bound(scale * rH, scale * aH, dt, dt, qe, scale) + scale * extra * xH
+    bW = R.grad_bound(scale * rW, scale * aW, dt, dt, qe, scale) + scale * extra * xW
+    assert np.all(np.abs(host(dH) - scale * rH) <= bH)
+    assert np.all(np.abs(host(dW) - scale * rW) <= bW)
+    assert not host(dH)[~c.P.mask].any()
+    l2, q2, s2 = c.pair(ref_d, opts, bwd=False)
+    assert torch.equal(l2, loss) and torch.equal(q2, q) and torch.equal(s2, st)
+
+
+@pytest.mark.parametrize("mask", ["ragged", "none"])
+def test_pair_chunkings_agree(mask):
+    """Whole pairs in one chunk, in several, and the logits twice: the same loss and log-probs, gradients within a rounding."""
+    outs = []
+    for cr in (0, 256, 128):
+        c = Case(6, 2, 80, 128, 300, "bf16", mask, seed=8, chunk_rows=cr, beta=0.1)
+        _, ref = c.old_ref()
+        outs.append(c.pair(torch.from_numpy(ref).cuda(), rg.pair_opts()))
+    for o in outs[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(o[:3], outs[0][:3]))
+        for k in (3, 4):
+            torch.testing.assert_close(o[k].float(), outs[0][k].float(), rtol=2 ** -7, atol=1e-6)
+
+
+def test_results_do_not_depend_on_the_workspace_or_the_stream():
+    c = Case(2, 3, 120, 192, 600, "bf16", "ragged", seed=9, chunk_rows=256)
+    old, ref = (torch.from_numpy(x).cuda() for x in c.old_ref())
+    adv = torch.randn(6, device="cuda")
+    a = c.clip(adv, old, ref, rg.clip_opts())
+    b = c.clip(adv, old, ref, rg.clip_opts())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        d = c.clip(adv, old, ref, rg.clip_opts())
+    for x, y, z in zip(a, b, d):
+        assert torch.equal(x, y) and torch.equal(x, z)
+
+
+def test_graph_replays_on_new_inputs():
+    c = Case(2, 2, 90, 128, 400, "bf16", "ragged", seed=10, chunk_rows=128, beta=0.1)
+    c2 = Case(2, 2, 90, 128, 400, "bf16", "holes", seed=11, chunk_rows=128, beta=0.1)
+    _, ref = c.old_ref()
+    ref = torch.from_numpy(clean(ref, c.P.mask).astype(np.float32)).cuda()
+    ws, loss, q, st = c.ws("pair"), c.f32(1), c.f32(360), c.f32(2, 4)
+    dH, dW = c.grads()
+    few = Case(1, 4, 1, 128, 400, "bf16", "all", seed=12)
+    fws, fq = few.ws("logp"), few.f32(4)
+
+    def call():
+        rg.grpo_pair_loss_fwd_bwd(c.h, c.W, c.tok, c.mask, ref, c.shape, rg.pair_opts(), 1.0, ws, loss, dH, dW, c.inf, q, st,
+                                  c.status)
+        rg.grpo_logprobs(few.h, few.W, few.tok, None, few.shape, 1.0, fws, fq, None, few.status)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for src in (c, c2):
+        for name in ("h", "W", "tok", "mask"):
+            getattr(c, name).copy_(getattr(src, name))
+        few.h.copy_(src.h[:4])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in (loss, q, st, dH, dW, fq)]
+        call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, (loss, q, st, dH, dW, fq)))
+        assert int(c.status) == 0 and int(few.status) == 0
+
+
+@pytest.mark.parametrize("rows", [4, 100])
+def test_a_bad_token_is_reported_and_contributes_nothing(rows):
+    c = Case(1, 1, rows, 128, 200, "bf16", "all", seed=13)
+    bad = c.tok.clone()
+    bad[1], bad[2] = 200, -1
+    c.tok, good = bad, c.tok
+    q, e = c.logp()
+    assert int(c.status) == 2 and host(q)[1] == host(q)[2] == host(e)[1] == 0
+    dq = torch.ones(rows, device="cuda")
+    dH, dW = c.logp_bwd(dq)
+    assert int(c.status) == 2 and not dH[1].any() and not dH[2].any()
+    c.tok = good
+    c.P.mask[1:3] = False
+    keep = np.ones(rows, bool)
+    keep[1:3] = False
+    rH, _, aH, _ = R.gradients(c.P, np.ones(rows), R.logp_entropy(c.P)[2])
+    bH = R.grad_bound(rH, aH, "bf16", "bf16", 1e-4, 1.0)
+    assert np.all(np.abs(host(dH) - rH)[keep] <= bH[keep])
+
+
+def test_found_inf_is_set_when_a_gradient_leaves_the_type():
+    c = Case(1, 1, 64, 128, 300, "fp16", "all", seed=14)
+    dq = torch.ones(64, device="cuda")
+    c.logp_bwd(dq, 1.0)
+    assert int(c.inf) == 0
+    c.logp_bwd(dq, 1e7)
+    assert int(c.inf) == 1
+    c.logp_bwd(dq * float("inf"), 1.0)
+    assert int(c.inf) == 1
+
+
+def test_mask_at_any_address_and_of_any_nonzero_value():
+    c = Case(1, 3, 100, 64, 130, "bf16", "holes", seed=15)
+    want, _ = c.logp()
+    buf = torch.zeros(301, dtype=torch.uint8, device="cuda")
+    buf[1:] = c.mask * 200
+    c.mask = buf[1:]
+    assert torch.equal(c.logp()[0], want)
+
+
+def test_checked_build_finds_no_bad_index():
+    from rl_fine_tuning_gb300 import build
+    lib = ctypes.CDLL(build.LIB_CHECKED)
+    rg._declare(lib)
+    normal, rg._lib = rg.load(), lib
+    try:
+        for cr, G, L in ((0, 2, 100), (128, 2, 100), (256, 2, 40)):
+            c = Case(3, G, L, 128, 500, "bf16", "ragged", seed=16, chunk_rows=cr, beta=0.1)
+            old, ref = (torch.from_numpy(x).cuda() for x in c.old_ref())
+            check_logp(c, *c.logp())
+            c.clip(torch.randn(c.n, device="cuda"), old, ref, rg.clip_opts())
+            assert int(c.status) == 0
+            c.pair(ref, rg.pair_opts())
+            assert int(c.status) == 0
+    finally:
+        rg._lib = normal
+
+
+def test_the_binding_refuses_what_the_c_interface_cannot_see():
+    c = Case(1, 2, 10, 64, 100, "bf16", "all", seed=17)
+    q = c.f32(20)
+    call = lambda h=c.h, W=c.W, tok=c.tok, out=q: rg.grpo_logprobs(h, W, tok, c.mask, c.shape, 1.0, c.ws("logp"), out,  # noqa: E731
+                                                                   None, c.status)
+    call()
+    wide = torch.zeros(20, 128, dtype=torch.bfloat16, device="cuda")
+    for kw in (dict(h=wide[:, ::2]), dict(h=c.h.float()), dict(h=c.h[:19]), dict(tok=c.tok.long()), dict(W=c.W.cpu()),
+               dict(out=q.double()), dict(W=torch.empty(64, 100, dtype=torch.bfloat16, device="cuda").t())):
+        with pytest.raises(ValueError):
+            call(**kw)
