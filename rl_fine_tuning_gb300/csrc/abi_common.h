@@ -71,7 +71,7 @@ struct DeviceInfo {
 int device_info(DeviceInfo* out);
 bool shape_ok(const grpo_shape& s);
 inline bool dtype_ok(const grpo_shape& s) { return s.dtype == GRPO_BF16 || s.dtype == GRPO_FP16; }
-int chunk_rows_of(const grpo_shape& s);
+
 
 // 2-D row-major matrix [rows x cols] of 16-bit elements with row pitch `pitch`
 // elements, 128-byte swizzled boxes of box_cols x box_rows.

@@ -97,7 +97,7 @@ static int default_chunk_rows(const grpo_shape& s) {
     return tiles * kBM;
 }
 
-int chunk_rows_of(const grpo_shape& s) {
+static int chunk_rows_of(const grpo_shape& s) {
     int r = s.chunk_rows > 0 ? s.chunk_rows : default_chunk_rows(s);
     r = (r + kBM - 1) / kBM * kBM;
     const int64_t N = static_cast<int64_t>(s.n_groups) * s.G * s.L;

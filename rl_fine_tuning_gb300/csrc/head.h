@@ -21,9 +21,10 @@ enum HeadMode {
     HEAD_PAIR = 3     // preference loss: d loss / d q follows from sums over pairs of completions
 };
 
-constexpr int kPieceK = 256;        // K elements the tensor cores add up before the sum moves to registers
+constexpr int kPieceK = 1024;       // K elements the tensor cores add up before the sum moves to registers
 constexpr int kHeadThreads = 384;   // a warpgroup with the producer and MMA warps, two of epilogue warps
-constexpr int kHeadSplitsMax = 512;
+constexpr int kHeadSplitsMax = 512;    // vocabulary splits of the logits kernel
+constexpr int kHeadChunkTiles = 76;    // default rows per chunk, in tiles of 128
 constexpr int kDhSlotsMax = 304;    // 256 x 256 partial tiles of dH (4 per SM pair)
 constexpr int kFewRows = 32;        // rows of the few-row kernel
 constexpr int kFewVocab = 128;      // vocabulary rows per tile of the few-row kernel
@@ -32,6 +33,11 @@ constexpr int kFewVocab = 128;      // vocabulary rows per tile of the few-row k
 // power of two, so its product with log2 e is that constant's rounding, exactly
 constexpr float kNoLogit = -1267650600228229401496703205376.f;   // -2^100
 constexpr float kNoLogit2 = kNoLogit * 1.4426950408889634f;
+// Correction of the tensor cores' rounding towards zero: n additions make a sum
+// too small by kAddLoss n of itself (see head_tc.cu)
+constexpr double kAddLoss = 1.45e-8;
+// q below this (p = 2^-100) does not fit the relative dlogits (see k_head_scale)
+constexpr float kLeastQ = -69.3f;
 
 struct PlanParams {
     const uint8_t* mask;    // nullptr: every row counts
@@ -46,7 +52,10 @@ struct PlanParams {
     int* cb;                // [max_chunks + 1] first valid row of chunk c
     int* pb;                // [max_chunks + 1] first pair of chunk c (by_pair)
     int2* dh_plan;          // [max_chunks] (units in one piece, K pieces of the rest)
+    int2* lg_plan;          // [max_chunks] (vocabulary splits, tiles per split) of the logits kernel
+    int n_ntiles, s_max;    // vocabulary tiles, most splits
     unsigned* gmax;         // [max_chunks] largest |d loss / d q| (float bits), zeroed
+    int* far;               // [max_chunks], zeroed
     int* rows;              // [N] valid rows, ascending
     int* found_inf;         // nullable, zeroed
     int* status;            // zeroed
@@ -75,17 +84,29 @@ struct GatherParams {
     int* status;
 };
 
+// What the logits kernel keeps
+enum LogitsMode {
+    LG_STATS = 0,      // (m, s) per row
+    LG_ENTROPY = 1,    // (m, s, u)
+    LG_KEEP_MAX = 2,   // (m, s) and the exponentials relative to the running maximum, fp16
+    LG_KEEP_TOKEN = 3  // s and the exponentials relative to the given token's logit, bf16
+};
+
 struct LogitsParams {
     const int* counts;
     const int* cb;
     const int* rows;
     const int* tokens;
+    const double* zt;       // [N] logit of the given token (LG_KEEP_TOKEN)
+    const int* only_if;     // nullable: nothing to do unless *only_if
     float4* part;           // [R x 2S] (m, s, u, -) of each half split, m in base 2
-    uint16_t* E;            // [R x V_pad] bf16 2^(z log2 e - running max), with a backward
+    uint16_t* E;            // [R x V_pad] exponentials; nullptr (LG_KEEP_TOKEN): not stored
     float* mx;              // [R x nc32] running max per 32 columns, base 2
-    float zscale;           // 1 / temperature
+    float zscale;           // logit = zscale * accumulator: 1 / temperature and the rounding's correction
+    float zscale2;          // zscale log2 e
     int64_t N;
-    int chunk, V, d, S, nps, n_ntiles, V_pad, nc32, R;
+    const int2* plan;       // [max_chunks] (S, nps)
+    int chunk, V, d, n_ntiles, V_pad, nc32, R;
     int* status;
 };
 
@@ -97,14 +118,18 @@ struct FewParams {
     int* counter;
     float* logp;
     float* entropy;         // nullable
-    float zscale;
+    float inv_t;            // 1 / temperature
+    float zscale, zscale2;  // as in LogitsParams
     int N, V, d, n_tiles;
     int* status;
 };
 
 struct HeadMergeParams {
     const float4* part;
-    int S2;                 // partials per row
+    const int2* plan;       // [max_chunks] (S, nps): 2 S partials a row
+    int relative;           // the partials are relative to the given token's logit (LG_KEEP_TOKEN)
+    const int* only_if;     // nullable: nothing to do unless *only_if
+    int* far;               // nullable: [max_chunks] <- 1 if a row of the chunk has q < kLeastQ
     const int* counts;
     const int* cb;
     const int* off;
@@ -152,18 +177,29 @@ struct HeadChunkParams : ChunkParams {
     float* dh_part;         // [slots][2][128 x 256] fp32
     const int2* dh_plan;
     const float* logp;      // [N] q
+    float* rowf;            // nullable: [R] factor of a dlogits row (relative dlogits)
+    uint16_t* hct;          // [d x R]
+    const uint16_t* hc;     // [R x d]
+    const int* far;         // nullable: [max_chunks]
     const unsigned* gmax;
     int gmax_chunk;         // which entry of gmax holds this chunk's
     float loss_scale;
 };
 
+// What the tensor cores' rounding takes from a sum over the vocabulary in `pieces`
+// parts: 1e-4 of it at V = 100352, which fp16 outputs would show
+__device__ __forceinline__ float dh_gain(int V, int pieces) {
+    return 1.f + static_cast<float>(kAddLoss) * static_cast<float>(V / (16 * pieces));
+}
+
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t st);
 cudaError_t launch_head_gather(const GatherParams& p, bool bf16, int sm_count, cudaStream_t st);
 cudaError_t launch_head_logits(const LogitsParams& p, const CUtensorMap& mH, const CUtensorMap& mW, int n_sm, bool bf16,
-                               bool keep, bool entropy, cudaStream_t st);
+                               int mode, cudaStream_t st);
 cudaError_t launch_head_merge(const HeadMergeParams& p, cudaStream_t st);
 cudaError_t launch_pair_coef(const PairParams& p, cudaStream_t st);
 cudaError_t launch_head_dlogits(const HeadChunkParams& p, float* oscale, bool bf16, int sm_count, cudaStream_t st);
+cudaError_t launch_head_scale(const HeadChunkParams& p, float* oscale, int sm_count, cudaStream_t st);
 cudaError_t launch_head_dh(const HeadChunkParams& p, const CUtensorMap& mDS, const CUtensorMap& mWmn, int n_sm, bool bf16,
                            cudaStream_t st);
 cudaError_t launch_head_dh_join(const HeadChunkParams& p, bool bf16, int sm_count, cudaStream_t st);

@@ -12,11 +12,15 @@ namespace {
 
 constexpr int64_t kPairChunkRowsMax = 19456;   // default chunks grow to hold one whole pair up to this (152 tiles of 128)
 
+// bf16 chunks of at least this many logits use relative dlogits (k_head_scale)
+// instead of a pass over the dlogits; below, the pass is the shorter way
+constexpr int64_t kRelativeMin = 1 << 24;
+
 struct HeadLayout {
-    size_t counts, off, cb, pb, dh_plan, gmax, oscale, rows, zt, lse, gco, ell, q, pair_ell, hc, part, mx, ds, hct, dh_part,
+    size_t counts, off, cb, pb, dh_plan, lg_plan, gmax, far, oscale, rowf, rows, zt, lse, gco, ell, q, pair_ell, hc, part, mx, ds, hct, dh_part,
         dw_acc, total;
     int64_t N;
-    int n_seq, R, max_chunks, S, nps, n_ntiles, V_pad, nc32, slots, by_pair;
+    int n_seq, R, max_chunks, S, n_ntiles, V_pad, nc32, slots, by_pair, relative;
 };
 
 bool head_shape_ok(const grpo_shape& s, int op) {
@@ -27,40 +31,23 @@ bool head_shape_ok(const grpo_shape& s, int op) {
 
 bool has_backward(int op) { return op != GRPO_OP_LOGPROBS; }
 
-// Rows per chunk: grpo_chunk_rows' choice.  The preference loss grows it to one
-// whole pair (2 L rows) unless the caller chose it: with whole pairs in a chunk
-// the logits are computed once instead of twice (6 N V d operations instead of
-// 8 N V d).  Above kPairChunkRowsMax the chunk's buffers (V 2 bytes a row) would
-// outgrow their use, and the logits are computed twice.
+// Rows per chunk.  Default: 76 tiles of 128 (9728).  A chunk's dlogits take
+// V 2 bytes a row; fewer, larger chunks add fewer times to dW's fp32 sum (8 V d
+// bytes each time).  The preference loss grows a default chunk to one whole
+// pair (2 L rows): with whole pairs in a chunk the logits are computed once
+// instead of twice, 6 N V d operations instead of 8 N V d.  Above
+// kPairChunkRowsMax a chunk's buffers would outgrow that.
 int head_chunk_rows(const grpo_shape& s, int op) {
-    int64_t r = chunk_rows_of(s);
     const int64_t N = static_cast<int64_t>(s.n_groups) * s.G * s.L;
+    const int64_t nmax = (N + kBM - 1) / kBM * kBM;
+    int64_t r = s.chunk_rows > 0 ? (s.chunk_rows + static_cast<int64_t>(kBM) - 1) / kBM * kBM
+                                 : static_cast<int64_t>(kHeadChunkTiles) * kBM;
     if (op == GRPO_OP_PAIR && s.chunk_rows == 0) {
         const int64_t pair = (2LL * s.L + kBM - 1) / kBM * kBM;
-        const int64_t nmax = (N + kBM - 1) / kBM * kBM;
-        if (pair > r && pair <= kPairChunkRowsMax) r = pair < nmax ? pair : nmax;
+        if (pair > r && pair <= kPairChunkRowsMax) r = pair;
     }
-    return static_cast<int>(r);
+    return static_cast<int>(r < nmax ? r : nmax);
 }
-
-// Vocabulary splits of the logits kernel: the tiles per split for which the
-// units of a full chunk, one per SM pair at a time, take the fewest tile times;
-// among equals the larger, which leaves fewer partials.
-void head_splits(int n_ntiles, int row_pairs, int sm_pairs, int* S, int* nps) {
-    int64_t best = -1;
-    for (int k = 1; k <= n_ntiles && k <= 64; ++k) {
-        const int s = (n_ntiles + k - 1) / k;
-        if (s > kHeadSplitsMax && k < n_ntiles && k < 64) continue;
-        const int64_t cost = (static_cast<int64_t>(row_pairs) * s + sm_pairs - 1) / sm_pairs * k;
-        if (best < 0 || cost <= best) {
-            best = cost;
-            *nps = k;
-            *S = s;
-        }
-    }
-}
-
-constexpr int kSmPairs = 76;   // GB300; other counts are right too, only unevenly loaded
 
 bool head_layout(const grpo_shape& s, int op, int dw_f32, HeadLayout* o) {
     if (!head_shape_ok(s, op)) return false;
@@ -74,8 +61,11 @@ bool head_layout(const grpo_shape& s, int op, int dw_f32, HeadLayout* o) {
         const int ppc = static_cast<int>(o->R / (2LL * s.L));
         o->max_chunks = (s.n_groups + ppc - 1) / ppc;
     }
+    o->relative = has_backward(op) && s.dtype == GRPO_BF16 && static_cast<int64_t>(o->R) * s.V >= kRelativeMin;
     o->n_ntiles = (s.V + kBN - 1) / kBN;
-    head_splits(o->n_ntiles, (o->R + 2 * kBM - 1) / (2 * kBM), kSmPairs, &o->S, &o->nps);
+    // splits: at most kHeadSplitsMax, and at least what 64 tiles a split give
+    const int least = (o->n_ntiles + 63) / 64;
+    o->S = o->n_ntiles < kHeadSplitsMax ? o->n_ntiles : least > kHeadSplitsMax ? least : kHeadSplitsMax;
     o->V_pad = (s.V + 63) / 64 * 64;
     o->nc32 = ((s.V + 31) / 32 + 7) / 8 * 8;
     const int64_t units = static_cast<int64_t>((o->R + 2 * kBM - 1) / (2 * kBM)) * ((s.d + kBN - 1) / kBN);
@@ -93,7 +83,9 @@ bool head_layout(const grpo_shape& s, int op, int dw_f32, HeadLayout* o) {
     o->cb = take((mc + 1) * 4);
     o->pb = take((mc + 1) * 4);
     o->dh_plan = take(mc * 8);
+    o->lg_plan = take(mc * 8);
     o->gmax = take(mc * 4);
+    o->far = take(mc * 4);
     o->oscale = take(mc * 4);
     o->rows = take(n * 4);
     o->zt = take(n * 8);
@@ -107,8 +99,9 @@ bool head_layout(const grpo_shape& s, int op, int dw_f32, HeadLayout* o) {
     const size_t few = static_cast<size_t>(kFewRows) * 256 * 16;   // the few-row kernel: one partial per row and CTA
     if (op == GRPO_OP_LOGPROBS && part < few) part = few;
     o->part = take(part);
-    o->mx = o->ds = o->hct = o->dh_part = o->dw_acc = off;
+    o->rowf = o->mx = o->ds = o->hct = o->dh_part = o->dw_acc = off;
     if (has_backward(op)) {
+        o->rowf = take(R * 4);
         o->mx = take(R * o->nc32 * 4);
         o->ds = take(R * o->V_pad * 2);
         o->hct = take(R * s.d * 2);
@@ -183,6 +176,17 @@ int head_validate(const HeadCall& c, HeadLayout* L) {
         if (launch(kind, st, [&] { return call; }) != cudaSuccess) return GRPO_ERR_LAUNCH; \
     } while (0)
 
+// logit = zscale * accumulator, with the correction of the tensor cores' rounding
+// (see head_tc.cu): a piece of n_i additions holds n_i / n of the sum and loses
+// kAddLoss n_i of that.
+void logit_scale(const HeadCall& c, float* zscale, float* zscale2) {
+    const int d = c.shape->d, full = d / kPieceK * kPieceK, rest = d - full;
+    const double n_eff = (static_cast<double>(full) * kPieceK + static_cast<double>(rest) * rest) / d / 16.0;
+    const double z = (1.0 + kAddLoss * n_eff) / static_cast<double>(c.temperature);
+    *zscale = static_cast<float>(z);
+    *zscale2 = static_cast<float>(z * 1.4426950408889634074);
+}
+
 // Log-probs of at most kFewRows rows: no plan, no copies, one pass over W.
 int run_few(const HeadCall& c, const HeadLayout& L, const DeviceInfo& dev, cudaStream_t st) {
     const grpo_shape& s = *c.shape;
@@ -200,7 +204,8 @@ int run_few(const HeadCall& c, const HeadLayout& L, const DeviceInfo& dev, cudaS
     p.counter = reinterpret_cast<int*>(w + L.counts);
     p.logp = c.logp;
     p.entropy = c.entropy;
-    p.zscale = 1.f / c.temperature;
+    p.inv_t = 1.f / c.temperature;
+    logit_scale(c, &p.zscale, &p.zscale2);
     p.N = N;
     p.V = s.V;
     p.d = s.d;
@@ -259,7 +264,11 @@ struct HeadRun {
         p.cb = at<int>(L.cb);
         p.pb = at<int>(L.pb);
         p.dh_plan = at<int2>(L.dh_plan);
+        p.lg_plan = at<int2>(L.lg_plan);
+        p.n_ntiles = L.n_ntiles;
+        p.s_max = L.S;
         p.gmax = at<unsigned>(L.gmax);
+        p.far = at<int>(L.far);
         p.rows = at<int>(L.rows);
         p.found_inf = c.found_inf;
         p.status = c.status;
@@ -269,7 +278,7 @@ struct HeadRun {
     }
 
     // compact rows of a chunk, and with them (first: once per call) the zeros of masked rows
-    int gather(int chunk, bool with_grad, bool first) {
+    int gather(int chunk, bool with_t, bool first) {
         const grpo_shape& s = *c.shape;
         GatherParams p = {};
         p.counts = at<int>(L.counts);
@@ -280,7 +289,7 @@ struct HeadRun {
         p.h = static_cast<const uint16_t*>(c.h);
         p.W = static_cast<const uint16_t*>(c.W);
         p.hc = at<uint16_t>(L.hc);
-        p.hct = with_grad ? at<uint16_t>(L.hct) : nullptr;
+        p.hct = with_t ? at<uint16_t>(L.hct) : nullptr;
         p.zt = at<double>(L.zt);
         if (first) {
             p.dH = static_cast<uint16_t*>(c.dH);
@@ -301,7 +310,7 @@ struct HeadRun {
         return GRPO_OK;
     }
 
-    int logits(int chunk, bool keep) {
+    int logits(int chunk, int mode, bool store, const int* only_if = nullptr) {
         const grpo_shape& s = *c.shape;
         LogitsParams p = {};
         p.counts = at<int>(L.counts);
@@ -309,29 +318,34 @@ struct HeadRun {
         p.rows = at<int>(L.rows);
         p.tokens = c.tokens;
         p.part = at<float4>(L.part);
-        p.E = keep ? at<uint16_t>(L.ds) : nullptr;
-        p.mx = keep ? at<float>(L.mx) : nullptr;
-        p.zscale = 1.f / c.temperature;
+        p.E = store ? at<uint16_t>(L.ds) : nullptr;
+        p.mx = store ? at<float>(L.mx) : nullptr;
+        logit_scale(c, &p.zscale, &p.zscale2);
+        p.zt = at<double>(L.zt);
+        p.only_if = only_if;
         p.N = L.N;
         p.chunk = chunk;
         p.V = s.V;
         p.d = s.d;
-        p.S = L.S;
-        p.nps = L.nps;
+        p.plan = at<int2>(L.lg_plan);
         p.n_ntiles = L.n_ntiles;
         p.V_pad = L.V_pad;
         p.nc32 = L.nc32;
         p.R = L.R;
         p.status = c.status;
-        HEAD_LAUNCH(GRPO_PROF_FWD, launch_head_logits(p, mH_k, mW_k, dev.sm_count, bf16, keep, c.entropy != nullptr, st));
+        HEAD_LAUNCH(GRPO_PROF_FWD, launch_head_logits(p, mH_k, mW_k, dev.sm_count, bf16, mode, st));
         return GRPO_OK;
     }
 
-    int merge(int chunk) {
+    // far: the chunk's word of the far list (set when a row's q is below kLeastQ)
+    int merge(int chunk, bool relative, const int* only_if, bool set_far) {
         const grpo_shape& s = *c.shape;
         HeadMergeParams p = {};
+        p.relative = relative;
+        p.only_if = only_if;
+        p.far = set_far ? at<int>(L.far) : nullptr;
         p.part = at<float4>(L.part);
-        p.S2 = 2 * L.S;
+        p.plan = at<int2>(L.lg_plan);
         p.counts = at<int>(L.counts);
         p.cb = at<int>(L.cb);
         p.off = at<int>(L.off);
@@ -422,7 +436,12 @@ struct HeadRun {
         p.gmax = at<unsigned>(L.gmax);
         p.gmax_chunk = gmax_chunk;
         p.loss_scale = c.loss_scale;
+        p.hct = at<uint16_t>(L.hct);
+        p.hc = at<uint16_t>(L.hc);
+        p.rowf = L.relative ? at<float>(L.rowf) : nullptr;
+        p.far = L.relative ? at<int>(L.far) : nullptr;
         HEAD_LAUNCH(GRPO_PROF_DLOGITS, launch_head_dlogits(p, at<float>(L.oscale), bf16, dev.sm_count, st));
+        if (L.relative) HEAD_LAUNCH(GRPO_PROF_DLOGITS, launch_head_scale(p, at<float>(L.oscale), dev.sm_count, st));
         HEAD_LAUNCH(GRPO_PROF_DH, launch_head_dh(p, mDS_k, mW_mn, dev.sm_count, bf16, st));
         HEAD_LAUNCH(GRPO_PROF_DH, launch_head_dh_join(p, bf16, dev.sm_count, st));
         HEAD_LAUNCH(GRPO_PROF_DW, launch_head_dw(p, mDS_mn, mHct, dev.sm_count, bf16, st));
@@ -440,19 +459,29 @@ struct HeadRun {
         HEAD_STEP(plan());
         // a preference loss whose chunks do not hold whole pairs: all log-probs first, then the logits again
         const bool twice = c.mode == HEAD_PAIR && c.backward && !L.by_pair;
+        const bool rel = L.relative;
+        const int keep = rel ? LG_KEEP_TOKEN : LG_KEEP_MAX;
+        // without gradients the same arithmetic, nothing kept: the same bits
+        const int stats = rel ? LG_KEEP_TOKEN : c.entropy ? LG_ENTROPY : LG_STATS;
         for (int i = 0; i < L.max_chunks; ++i) {
-            const bool keep = c.backward && !twice;
-            HEAD_STEP(gather(i, keep, i == 0));
-            HEAD_STEP(logits(i, keep));
-            HEAD_STEP(merge(i));
-            if (!keep) continue;
+            const bool grad = c.backward && !twice;
+            const int* far = at<int>(L.far) + i;
+            HEAD_STEP(gather(i, grad && !rel, i == 0));
+            HEAD_STEP(logits(i, grad ? keep : stats, grad));
+            HEAD_STEP(merge(i, rel, nullptr, rel));
+            if (rel) {   // only for a chunk with a far row
+                HEAD_STEP(logits(i, grad ? LG_KEEP_MAX : LG_STATS, grad, far));
+                HEAD_STEP(merge(i, false, far, false));
+            }
+            if (!grad) continue;
             if (c.mode == HEAD_PAIR) HEAD_STEP(pair_coef(i));
             HEAD_STEP(gradients(i, i));
         }
         if (c.mode == HEAD_PAIR && (twice || !c.backward)) HEAD_STEP(pair_coef(-1));
         for (int i = 0; twice && i < L.max_chunks; ++i) {
-            HEAD_STEP(gather(i, true, false));
-            HEAD_STEP(logits(i, true));
+            HEAD_STEP(gather(i, !rel, false));
+            HEAD_STEP(logits(i, keep, true));
+            if (rel) HEAD_STEP(logits(i, LG_KEEP_MAX, true, at<int>(L.far) + i));
             HEAD_STEP(gradients(i, 0));
         }
         if (c.mode == HEAD_CLIP)

@@ -42,4 +42,21 @@ __device__ __forceinline__ RowSum join_row(const float4* part, int S2, int lane,
     return r;
 }
 
+// The same from sums relative to the given token's logit, part.x the fp32 value
+// of z_tok log2 e that was the base: s = sum e^(z - z_tok) over the other
+// columns, q = -log(1 + s).  s overflows when another logit is far above the
+// token's; q is then -inf and the caller takes another way.
+__device__ __forceinline__ RowSum join_row_relative(const float4* part, int S2, int lane, double zt) {
+    float s = 0.f;
+    for (int k = lane; k < S2; k += 32) s += __ldcg(part + k).y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const double base = static_cast<double>(__ldcg(part).x);
+    RowSum r;
+    r.q = -log1p(static_cast<double>(s) * exp2(base - zt * 1.4426950408889634074));
+    r.lse = zt - r.q;
+    r.ent = 0.f;
+    return r;
+}
+
 }  // namespace grpo

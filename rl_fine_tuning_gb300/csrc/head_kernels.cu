@@ -55,6 +55,20 @@ __device__ __forceinline__ double block_sum(double v, double* sh) {
     return r;
 }
 
+// the choice of the lane with the lowest cost (ties: the smaller choice)
+__device__ __forceinline__ int warp_best(float cost, int choice) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float oc = __shfl_xor_sync(0xffffffffu, cost, o);
+        const int ob = __shfl_xor_sync(0xffffffffu, choice, o);
+        if (oc < cost || (oc == cost && ob < choice)) {
+            cost = oc;
+            choice = ob;
+        }
+    }
+    return choice;
+}
+
 // (first valid row, valid rows) of a chunk; 0 rows past the last one
 __device__ __forceinline__ int2 chunk_bounds(const int* counts, const int* cb, int chunk) {
     if (chunk >= counts[C_NCHUNKS]) return make_int2(0, 0);
@@ -106,7 +120,11 @@ __device__ __forceinline__ double token_logit(const uint4* a, const uint4* b, in
 // ------------------------------------------------------------ plan
 // One block walks the mask in segments of 16,384 rows and writes the valid
 // rows in order, the number of valid rows before each completion, the chunk
-// bounds and, for each chunk, how dH's units are split.
+// bounds and, for each chunk, how the logits' and dH's units are split.
+//
+// Logits split: a unit is (256 rows, nps vocabulary tiles of 256); nps is the one
+// for which the units, one per SM pair at a time, take the fewest tile times,
+// with 0.002 of a tile time for each split's partials.
 //
 // Chunks hold R rows, or (by_pair) as many whole pairs of completions as fit R
 // rows: a pair's d loss / d q needs the sums over both completions, so a chunk
@@ -161,7 +179,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(const PlanParams p) {
     }
     const int nv = carry;
     if (tid == 0) p.off[p.n_seq] = nv;
-    for (int c = tid; c < p.max_chunks; c += kPlanThreads) p.gmax[c] = 0u;
+    for (int c = tid; c < p.max_chunks; c += kPlanThreads) {
+        p.gmax[c] = 0u;
+        p.far[c] = 0;
+    }
     __syncthreads();   // off is complete
     if (p.by_pair) {
         const int n_pr = p.n_seq / 2;
@@ -203,26 +224,46 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(const PlanParams p) {
         p.counts[C_NVALID] = nv;
         p.counts[C_NACT] = s_act;
     }
-    if (p.slots_max > 0) {
-        const int n_chunks = p.counts[C_NCHUNKS];
-        for (int c = tid; c < n_chunks; c += kPlanThreads) {
-            const int n_c = p.cb[c + 1] - p.cb[c];
-            const int units = ((n_c + 2 * kBM - 1) / (2 * kBM)) * p.n_nt;
-            const int full = units / p.n_pairs * p.n_pairs, rem = units - full;
-            int best = 1;
-            float best_cost = 3e38f;
-            for (int s = 1; rem > 0 && s <= 64 && s <= p.ks && rem * s <= p.slots_max; ++s) {
-                const int kper = (p.ks + s - 1) / s;
-                if ((s - 1) * kper >= p.ks) continue;   // the last piece would be empty
-                const float waves = static_cast<float>((rem * s + p.n_pairs - 1) / p.n_pairs);
-                const float cost = waves * (kper + 12) + (s > 1 ? 0.3f * rem * s : 0.f);
-                if (cost < best_cost) {
-                    best_cost = cost;
-                    best = s;
-                }
+    // one warp per chunk; a lane weighs two numbers of splits or pieces
+    const int n_chunks = p.counts[C_NCHUNKS];
+    const int lane = tid & 31;
+    for (int c = tid >> 5; c < n_chunks; c += kPlanThreads / 32) {
+        const int row_pairs = (p.cb[c + 1] - p.cb[c] + 2 * kBM - 1) / (2 * kBM);
+        float best_cost = 3e38f;
+        int best = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = lane + 1 + 32 * h;   // tiles per split
+            const int s = (p.n_ntiles + k - 1) / k;
+            if (k > p.n_ntiles || s > p.s_max) continue;
+            const float cost = static_cast<float>((row_pairs * s + p.n_pairs - 1) / p.n_pairs) * k + 0.002f * s;
+            if (cost < best_cost) {
+                best_cost = cost;
+                best = k;
             }
-            p.dh_plan[c] = make_int2(best > 1 ? full : units, best);
         }
+        best = warp_best(best_cost, best);
+        if (lane == 0) p.lg_plan[c] = make_int2((p.n_ntiles + best - 1) / best, best);
+        if (p.slots_max <= 0) continue;
+        const int units = row_pairs * p.n_nt;
+        const int full = units / p.n_pairs * p.n_pairs, rem = units - full;
+        best_cost = 3e38f;
+        best = 1;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int s = lane + 1 + 32 * h;
+            if (rem == 0 || s > p.ks || (s > 1 && rem * s > p.slots_max)) continue;
+            const int kper = (p.ks + s - 1) / s;
+            if ((s - 1) * kper >= p.ks) continue;   // the last piece would be empty
+            const float waves = static_cast<float>((rem * s + p.n_pairs - 1) / p.n_pairs);
+            const float cost = waves * (kper + 12) + (s > 1 ? 0.3f * rem * s : 0.f);
+            if (cost < best_cost) {
+                best_cost = cost;
+                best = s;
+            }
+        }
+        best = warp_best(best_cost, best);
+        if (lane == 0) p.dh_plan[c] = make_int2(best > 1 ? full : units, best);
     }
 }
 
@@ -350,7 +391,7 @@ __global__ void __launch_bounds__(32) k_few_prep(const FewParams p, const uint4*
     const int tok = p.tokens[n];
     if ((p.mask && !p.mask[n]) || tok < 0 || tok >= p.V) return;
     const double z = token_logit<kBf16>(h + static_cast<int64_t>(n) * vpr, W + static_cast<int64_t>(tok) * vpr, vpr, lane);
-    if (lane == 0) zt[n] = z * static_cast<double>(p.zscale);
+    if (lane == 0) zt[n] = z * static_cast<double>(p.inv_t);
 }
 
 cudaError_t launch_few_prep(const FewParams& p, const uint16_t* h, const uint16_t* W, bool bf16, double* zt,
@@ -371,6 +412,8 @@ constexpr int kHeadMergeThreads = 256;
 
 __global__ void __launch_bounds__(kHeadMergeThreads) k_head_merge(const HeadMergeParams p) {
     __shared__ unsigned s_max;
+    if (p.chunk >= p.counts[C_NCHUNKS] || (p.only_if && *p.only_if == 0)) return;
+    const int S2 = 2 * p.plan[p.chunk].x;
     const int2 cbn = chunk_bounds(p.counts, p.cb, p.chunk);
     const int c0 = cbn.x, n_c = cbn.y;
     const int lane = threadIdx.x & 31;
@@ -384,10 +427,12 @@ __global__ void __launch_bounds__(kHeadMergeThreads) k_head_merge(const HeadMerg
             const int tok = p.tokens[t];
             const bool ok = tok >= 0 && tok < p.V;
             RowSum r{0.0, 0.0, 0.f};
-            if (ok) r = join_row(p.part + static_cast<int64_t>(slot) * p.S2, p.S2, lane, p.zt[t]);
+            if (ok) r = p.relative ? join_row_relative(p.part + static_cast<int64_t>(slot) * S2, S2, lane, p.zt[t])
+                                   : join_row(p.part + static_cast<int64_t>(slot) * S2, S2, lane, p.zt[t]);
             if (lane == 0) {
                 if (!ok) atomicCAS(p.status, 0, GRPO_ERR_SHAPE);
                 const float q = static_cast<float>(r.q);
+                if (p.far && !(q >= kLeastQ)) atomicOr(p.far + p.chunk, 1);
                 float g = 0.f, ell = 0.f, ratio = 0.f, pen = 0.f;
                 if (ok && p.mode == HEAD_GRAD) g = p.dlogp[t];
                 if (ok && p.mode == HEAD_CLIP) {
@@ -546,10 +591,10 @@ cudaError_t launch_pair_loss(const double* ell, int n_pairs, const int* counts, 
 }
 
 // ------------------------------------------------------------ dlogits
-// In place: the kept exponentials E = 2^(z log2 e - m) of a row become
-//   dS = g (onehot(tok) - E 2^(m - lse log2 e)),   m the running maximum of the column's group of 32
-// rounded to the input type, which the two GEMMs need (one rounding of 2^-9 on
-// top of E's; the GEMMs sum thousands of them).  fp16 has no exponent range to
+// In place: the kept exponentials E = 2^(z log2 e - m) (fp16) of a row become
+//   dS = g (onehot(tok) - E 2^(m - lse log2 e)),   m the base of the column's group of 32
+// rounded to the input type, which the two GEMMs need (E's rounding, 2^-12, is
+// small beside bf16's).  fp16 has no exponent range to
 // spare: there g is divided by the power of two above the chunk's largest |g|
 // and multiplied by 2^14, and the GEMMs' epilogues undo it (oscale), whatever
 // the caller's loss scale is.  Reads and writes the chunk once: bound by HBM.
@@ -557,7 +602,7 @@ template <bool kBf16>
 __global__ void __launch_bounds__(kTransformThreads) k_head_dlogits(const HeadChunkParams p, float* oscale) {
     const int2 cbn = chunk_bounds(p.counts, p.cb, p.chunk);
     const int c0 = cbn.x, n_c = cbn.y;
-    if (n_c == 0) return;
+    if (n_c == 0 || (p.far && p.far[p.chunk] == 0)) return;
     float up = 1.f;
     if (!kBf16) {
         const float gm = __uint_as_float(p.gmax[p.gmax_chunk]);
@@ -578,7 +623,7 @@ __global__ void __launch_bounds__(kTransformThreads) k_head_dlogits(const HeadCh
         if (!GRPO_DCHECK(t >= 0 && t < p.N, p.status)) continue;
         const int tok = p.tokens[t];
         const float lse2 = p.lse[t] * 1.4426950408889634f;
-        const float coef = up * p.gco[t];
+        const float coef = tok >= 0 && tok < p.V ? up * p.gco[t] : 0.f;
         const float dtok = -coef * expm1f(p.logp[t]);   // g (1 - p_tok)
         const float* mrow = p.mx + static_cast<int64_t>(slot) * p.nc32;
         for (int i = threadIdx.x; i < nvec; i += kTransformThreads) {
@@ -590,7 +635,8 @@ __global__ void __launch_bounds__(kTransformThreads) k_head_dlogits(const HeadCh
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int va = v0 + 2 * j, vb = va + 1;
-                float d0 = -c * __uint_as_float(w[j] << 16), d1 = -c * __uint_as_float(w[j] & 0xFFFF0000u);
+                const float2 e = unpack16<false>(w[j]);
+                float d0 = -c * e.x, d1 = -c * e.y;
                 if (va == tok) d0 = dtok;
                 if (vb == tok) d1 = dtok;
                 if (va >= p.V) d0 = 0.f;
@@ -612,6 +658,95 @@ cudaError_t launch_head_dlogits(const HeadChunkParams& p, float* oscale, bool bf
     return cudaGetLastError();
 }
 
+// ------------------------------------------------------------ relative dlogits
+// Without a pass over the dlogits.  The logits kernel knows the given token's
+// logit beforehand and keeps A_v = e^(z_v - z_tok) = p_v / p_tok, so with
+// s = sum of A over the other columns, p_tok = 1 / (1 + s) and
+//   dS_v = g (onehot - p_v) = f A_v  with  f = -g p_tok  and  A_tok = -s.
+// f is a factor of the row: dH's epilogue applies it, and for dW, where rows are
+// summed, the rows of h carry it.  A is rounded once to bf16 (any exponent that
+// q >= kLeastQ leaves is in range), f h once more.  The row's largest entry is
+// the token's: f is taken as -g (1 - p_tok) / A_tok with A_tok as rounded, so
+// that entry is exact and dH has one rounding less than with the pass.  On 5.9K rows of a 152K vocabulary this kernel and the
+// empty fallback take 0.05 ms where the pass took 0.53.
+//
+// This kernel writes A_tok, f, and f h transposed for dW's K-major operand.  In
+// a chunk that holds a row with q < kLeastQ (far), the logits kernel ran again
+// with running maxima and the pass made the dlogits; f is 1 there.
+__global__ void __launch_bounds__(256) k_head_scale(const HeadChunkParams p, float* oscale) {
+    __shared__ uint32_t tile[kGTile][kGTile / 2 + 1];
+    __shared__ float s_f[kGTile];
+    const int2 cbn = chunk_bounds(p.counts, p.cb, p.chunk);
+    const int c0 = cbn.x, n_c = cbn.y;
+    if (n_c == 0) return;
+    const bool far = p.far[p.chunk] != 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) oscale[p.chunk] = p.loss_scale;
+    const int n_fill = min(p.R, (n_c + kBM - 1) / kBM * kBM);   // a multiple of 128
+    const int nt_d = p.d / kGTile, vpr = p.d / 8;
+    const int64_t n_tiles = static_cast<int64_t>(n_fill / kGTile) * nt_d;
+    for (int64_t it = blockIdx.x; it < n_tiles; it += gridDim.x) {
+        const int r0 = static_cast<int>(it / nt_d) * kGTile;
+        const int d0 = static_cast<int>(it % nt_d) * kGTile;
+        if (threadIdx.x < kGTile) {
+            const int slot = r0 + threadIdx.x;
+            float f = 0.f;
+            if (slot < n_c) {
+                const int t = p.rows[c0 + slot];
+                if (GRPO_DCHECK(t >= 0 && t < p.N, p.status)) {
+                    const int tok = p.tokens[t];
+                    const float q = p.logp[t];
+                    f = 1.f;
+                    if (!far) {
+                        const float s = expm1f(-q);
+                        const uint16_t s16 = round16<true>(s);
+                        const float sr = __uint_as_float(static_cast<uint32_t>(s16) << 16);
+                        f = -p.gco[t] * (sr > 0.f ? -expm1f(q) / sr : expf(q));
+                        if (d0 == 0 && tok >= 0 && tok < p.V)
+                            p.dS[static_cast<int64_t>(slot) * p.V_pad + tok] = s16 ^ 0x8000u;
+                    }
+                }
+                if (d0 == 0) p.rowf[slot] = f;
+            }
+            s_f[threadIdx.x] = f;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < kGTile * 8; i += blockDim.x) {
+            const int r = i >> 3, v = i & 7;
+            const uint4 x = reinterpret_cast<const uint4*>(p.hc)[static_cast<int64_t>(r0 + r) * vpr + (d0 >> 3) + v];
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            const float f = s_f[r];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 y = unpack16<true>(w[j]);
+                tile[r][4 * v + j] = static_cast<uint32_t>(round16<true>(f * y.x)) |
+                                     (static_cast<uint32_t>(round16<true>(f * y.y)) << 16);
+            }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < kGTile * 8; i += blockDim.x) {
+            const int k = i >> 3, v = i & 7;   // output row d0 + k, slots r0 + 8v .. r0 + 8v + 7
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t w0 = tile[8 * v + 2 * j][k >> 1], w1 = tile[8 * v + 2 * j + 1][k >> 1];
+                const uint32_t e0 = (k & 1) ? (w0 >> 16) : (w0 & 0xFFFFu);
+                const uint32_t e1 = (k & 1) ? (w1 >> 16) : (w1 & 0xFFFFu);
+                o[j] = e0 | (e1 << 16);
+            }
+            *reinterpret_cast<uint4*>(p.hct + static_cast<int64_t>(d0 + k) * p.R + r0 + 8 * v) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        __syncthreads();
+    }
+}
+
+cudaError_t launch_head_scale(const HeadChunkParams& p, float* oscale, int sm_count, cudaStream_t st) {
+    const int64_t tiles = static_cast<int64_t>(p.R / kGTile) * (p.d / kGTile);
+    const int blocks = static_cast<int>(tiles < sm_count * 8 ? tiles : sm_count * 8);
+    k_head_scale<<<blocks, 256, 0, st>>>(p, oscale);
+    return cudaGetLastError();
+}
+
 // ------------------------------------------------------------ dH join
 // One warp per row of a split dH tile: adds its K pieces in order, scales,
 // rounds and stores it.
@@ -624,7 +759,7 @@ __global__ void __launch_bounds__(256) k_dh_join(const HeadChunkParams p) {
     const int n_nt = (p.d + kBN - 1) / kBN;
     const int units = (n_c + 2 * kBM - 1) / (2 * kBM) * n_nt;
     const int rem = units - plan.x;
-    const float f = p.oscale[p.chunk];
+    const float scale = p.oscale[p.chunk] * dh_gain(p.V, plan.y);
     const int lane = threadIdx.x & 31;
     bool bad = false;
     for (int it = blockIdx.x * 8 + (threadIdx.x >> 5); it < rem * 2 * kBM; it += gridDim.x * 8) {
@@ -642,6 +777,7 @@ __global__ void __launch_bounds__(256) k_dh_join(const HeadChunkParams p) {
             acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w;
             acc[4] += b.x, acc[5] += b.y, acc[6] += b.z, acc[7] += b.w;
         }
+        const float f = p.rowf ? scale * p.rowf[slot] : scale;
         uint32_t o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

@@ -10,13 +10,18 @@
 //
 // Sums over K.  tcgen05.mma adds to its fp32 accumulator with rounding towards
 // zero: after d / 16 additions a logit of 11 was 4.6e-5 too small at d = 4096
-// (measured), a bias that stays in every log-prob, in ratios near 1 and in
-// sums of log-probs over a completion.  The two forward kernels therefore let
-// the tensor cores add only kPieceK = 256 products at a time and add the
-// pieces in registers, rounding to nearest: 16 times fewer biased additions on
-// numbers 16 times smaller.  Eight epilogue warps hold one 128 x 256
-// accumulator (128 registers a thread); a piece takes the tensor cores about
-// 2100 clocks and the epilogue about 500, so nothing waits for it.
+// (measured), always in one direction, so it stays in log-probs, in ratios
+// near 1 and in sums of log-probs over a completion.  Two remedies:
+//   - the tensor cores add only kPieceK products at a time, and the pieces
+//     are added in registers, rounding to nearest.  Eight epilogue warps
+//     hold one 128 x 256 accumulator (128 registers a thread).
+//   - each of n additions loses about half a unit in the last place of the
+//     partial sum, whose expected value grows linearly to the final one, so
+//     the loss is proportional to the sum: kAddLoss n.  Measured per addition:
+//     1.43e-8 of the sum for n = 64, 1.57e-8 for n = 256, within 8% on five kinds
+//     of inputs (half as much again with outlier columns).  The forward
+//     kernels multiply it back in with the scale of the logits; what is left of a
+//     logit of 10 is below 1e-6, and 4e-8 of an average one.
 #include <cfloat>
 
 #include "head_join.cuh"
@@ -37,7 +42,7 @@ constexpr int kLgSmem = kLgStages * kLgStageBytes + 1024 + 512;
 // units: (row-tile pair, vocabulary split), row-tile pairs fastest within
 // groups of kFwdGroup so that a W tile is shared in L2
 struct LgSched {
-    int n_units, ks, n_pc, n_mp, c0, n_c;
+    int n_units, ks, n_pc, n_mp, c0, n_c, S, nps;
 };
 
 __device__ __forceinline__ bool lg_setup(const LogitsParams& p, LgSched& sc) {
@@ -45,27 +50,35 @@ __device__ __forceinline__ bool lg_setup(const LogitsParams& p, LgSched& sc) {
     sc.c0 = p.cb[p.chunk];
     sc.n_c = p.cb[p.chunk + 1] - sc.c0;
     sc.n_mp = (sc.n_c + 2 * kBM - 1) / (2 * kBM);
-    sc.n_units = sc.n_mp * p.S;
+    sc.S = p.plan[p.chunk].x;
+    sc.nps = p.plan[p.chunk].y;
+    sc.n_units = sc.n_mp * sc.S;
     sc.ks = p.d / kBK;
     sc.n_pc = (sc.ks + kStagesPerPiece - 1) / kStagesPerPiece;
     return sc.n_units > 0;
 }
 
-__device__ __forceinline__ int lg_items(const LogitsParams& p, int split) {
-    return min(split * p.nps + p.nps, p.n_ntiles) - split * p.nps;
+__device__ __forceinline__ int lg_items(const LogitsParams& p, const LgSched& sc, int split) {
+    return min(split * sc.nps + sc.nps, p.n_ntiles) - split * sc.nps;
 }
 
-// One row's running statistics over the columns a thread sees: m = max of
-// z log2 e as rounded, s = sum 2^(z log2 e - m), u = sum z 2^(z log2 e - m).  In
-// base 2 the rounding of m cancels; e^(z - m) with m log2 e rounded would not.
+// One row's running statistics over the columns a thread sees: with m = max of
+// z log2 e - kUp as rounded, s = sum 2^(z log2 e - m) and u = sum z 2^(z log2 e - m).
+// In base 2 the rounding of m cancels; e^(z - m) with m log2 e rounded would not.
+// kUp lifts the exponentials to at most 2^14, so that fp16 keeps 11 bits of
+// those down to 2^-28 of the largest.
+constexpr float kUp = 14.f;
+
 struct RowStat {
     float m, s, u;
 };
 
-template <bool kBf16, bool kKeep, bool kEnt>
+template <bool kBf16, int kMode>
 __device__ __forceinline__ void lg_body(const LogitsParams& p, const CUtensorMap& mA, const CUtensorMap& mB) {
+    constexpr bool kKeep = kMode >= LG_KEEP_MAX, kEnt = kMode == LG_ENTROPY, kToken = kMode == LG_KEEP_TOKEN;
     extern __shared__ uint8_t smem_raw[];
     LgSched sc;
+    if (p.only_if && *p.only_if == 0) return;
     if (!lg_setup(p, sc)) return;
     const int cid = static_cast<int>(blockIdx.x) >> 1;
     const int n_pairs = static_cast<int>(gridDim.x) >> 1;
@@ -119,14 +132,21 @@ __device__ __forceinline__ void lg_body(const LogitsParams& p, const CUtensorMap
         int it = 0;
         for (int unit = cid; unit < sc.n_units; unit += n_pairs) {
             int mp, split;
-            decode_grouped(unit, sc.n_mp, p.S, kFwdGroup, &mp, &split);
-            const int n_items = lg_items(p, split);
+            decode_grouped(unit, sc.n_mp, sc.S, kFwdGroup, &mp, &split);
+            const int n_items = lg_items(p, sc, split);
             const int slot = (2 * mp + rank) * kBM + row;
             bool valid = slot < sc.n_c && GRPO_DCHECK(slot < p.R, status);
             const int t = valid ? p.rows[sc.c0 + slot] : 0;
             if (valid && !GRPO_DCHECK(t >= 0 && t < p.N, status)) valid = false;
             const int tok = valid ? p.tokens[t] : -1;
             RowStat e{kNoLogit2, 0.f, 0.f};
+            // LG_KEEP_TOKEN: the fixed base, and whether the row is stored (zeros up to the next multiple of 128)
+            bool stored = valid;
+            if (kToken) {
+                stored = p.E && slot < min(p.R, (sc.n_c + kBM - 1) / kBM * kBM);
+                const bool ok = valid && tok >= 0 && tok < p.V;
+                e.m = ok ? static_cast<float>(p.zt[t] * 1.4426950408889634074) : INFINITY;
+            }
             for (int item = 0; item < n_items; ++item) {
                 float a[128];
                 for (int pc = 0; pc < sc.n_pc; ++pc, ++it) {
@@ -144,11 +164,11 @@ __device__ __forceinline__ void lg_body(const LogitsParams& p, const CUtensorMap
                     __syncwarp();
                     if (lane == 0) {
                         if (leader) mbar_arrive(&sm.acc_empty[b]);
-                        else mbar_arrive_cluster(acc_empty0 + 8u * b);
+                        else mbar_arrive_peer(acc_empty0 + 8u * b);
                     }
                 }
-                const int n0 = (split * p.nps + item) * kBN + 128 * half;
-                uint16_t* erow = kKeep && valid ? p.E + static_cast<int64_t>(slot) * p.V_pad + n0 : nullptr;
+                const int n0 = (split * sc.nps + item) * kBN + 128 * half;
+                uint16_t* erow = kKeep && stored ? p.E + static_cast<int64_t>(slot) * p.V_pad + n0 : nullptr;
                 float mv[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -156,10 +176,6 @@ __device__ __forceinline__ void lg_body(const LogitsParams& p, const CUtensorMap
                     mv[c] = 0.f;
                     if (col0 >= p.V) continue;
                     float* v = a + 32 * c;
-                    if (p.zscale != 1.f) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] *= p.zscale;
-                    }
                     // columns past V and the row's own token do not count here
                     const int nvalid = p.V - col0;
                     if (nvalid < 32) {
@@ -172,15 +188,18 @@ __device__ __forceinline__ void lg_body(const LogitsParams& p, const CUtensorMap
                         for (int j = 0; j < 32; ++j)
                             if (tok == col0 + j) v[j] = kNoLogit;
                     }
-                    float cmax = v[0];
+                    float base = e.m;
+                    if (!kToken) {
+                        float cmax = v[0];
 #pragma unroll
-                    for (int j = 1; j < 32; ++j) cmax = fmaxf(cmax, v[j]);
-                    const float m_new = fmaxf(e.m, cmax * kLog2e);
+                        for (int j = 1; j < 32; ++j) cmax = fmaxf(cmax, v[j]);
+                        base = fmaxf(e.m, fmaf(cmax, p.zscale2, -kUp));
+                    }
                     float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        const float x0 = fast_exp2(fmaf(v[j], kLog2e, -m_new));
-                        const float x1 = fast_exp2(fmaf(v[j + 1], kLog2e, -m_new));
+                        const float x0 = fast_exp2(fmaf(v[j], p.zscale2, -base));
+                        const float x1 = fast_exp2(fmaf(v[j + 1], p.zscale2, -base));
                         s0 += x0;
                         s1 += x1;
                         if (kEnt) {
@@ -190,30 +209,35 @@ __device__ __forceinline__ void lg_body(const LogitsParams& p, const CUtensorMap
                         v[j] = x0;
                         v[j + 1] = x1;
                     }
-                    const float f = fast_exp2(e.m - m_new);
-                    e.s = fmaf(e.s, f, s0 + s1);
-                    if (kEnt) e.u = fmaf(e.u, f, u0 + u1);
-                    e.m = m_new;
-                    mv[c] = m_new;
-                    if (kKeep && valid && GRPO_DCHECK(col0 + 32 <= p.V_pad, status)) {
+                    if (kToken) {
+                        e.s += s0 + s1;
+                    } else {
+                        const float f = fast_exp2(e.m - base);
+                        e.s = fmaf(e.s, f, s0 + s1);
+                        if (kEnt) e.u = fmaf(e.u, f, u0 + u1);
+                        e.m = base;
+                        mv[c] = base;
+                    }
+                    if (kKeep && stored && GRPO_DCHECK(col0 + 32 <= p.V_pad, status)) {
                         // 64 bytes of one row as two whole 32-byte sectors
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const float* w = v + 16 * h;
-                            st_global_v8(erow + 32 * c + 16 * h, pack2(w[0], w[1], true), pack2(w[2], w[3], true),
-                                         pack2(w[4], w[5], true), pack2(w[6], w[7], true), pack2(w[8], w[9], true),
-                                         pack2(w[10], w[11], true), pack2(w[12], w[13], true),
-                                         pack2(w[14], w[15], true));
+                            st_global_v8(erow + 32 * c + 16 * h, pack2(w[0], w[1], kToken), pack2(w[2], w[3], kToken),
+                                         pack2(w[4], w[5], kToken), pack2(w[6], w[7], kToken), pack2(w[8], w[9], kToken),
+                                         pack2(w[10], w[11], kToken), pack2(w[12], w[13], kToken),
+                                         pack2(w[14], w[15], kToken));
                         }
                     }
                 }
                 // nc32 is a multiple of 8 and n0 of 128: 16-byte aligned
-                if (kKeep && valid && GRPO_DCHECK((n0 >> 5) + 4 <= p.nc32, status))
+                if (kMode == LG_KEEP_MAX && valid && GRPO_DCHECK((n0 >> 5) + 4 <= p.nc32, status))
                     *reinterpret_cast<float4*>(p.mx + static_cast<int64_t>(slot) * p.nc32 + (n0 >> 5)) =
                         make_float4(mv[0], mv[1], mv[2], mv[3]);
             }
-            if (valid && GRPO_DCHECK(split >= 0 && split < p.S, status))
-                p.part[static_cast<int64_t>(slot) * (2 * p.S) + 2 * split + half] = make_float4(e.m, e.s, e.u, 0.f);
+            if (kEnt) e.u *= p.zscale;   // sum of z, not of the accumulator
+            if (valid && GRPO_DCHECK(split >= 0 && split < sc.S, status))
+                p.part[static_cast<int64_t>(slot) * (2 * sc.S) + 2 * split + half] = make_float4(e.m, e.s, e.u, 0.f);
         }
     epi_done:;
     } else {
@@ -225,11 +249,11 @@ __device__ __forceinline__ void lg_body(const LogitsParams& p, const CUtensorMap
                 uint32_t ph = 0;
                 for (int unit = cid; unit < sc.n_units; unit += n_pairs) {
                     int mp, split;
-                    decode_grouped(unit, sc.n_mp, p.S, kFwdGroup, &mp, &split);
+                    decode_grouped(unit, sc.n_mp, sc.S, kFwdGroup, &mp, &split);
                     const int m0 = (2 * mp + rank) * kBM;
-                    const int n_items = lg_items(p, split);
+                    const int n_items = lg_items(p, sc, split);
                     for (int item = 0; item < n_items; ++item) {
-                        const int n0 = (split * p.nps + item) * kBN + rank * 128;
+                        const int n0 = (split * sc.nps + item) * kBN + rank * 128;
                         for (int k = 0; k < sc.ks; ++k) {
                             if (!mbar_wait(&sm.empty[s], ph ^ 1u, sm.abort_flag, status)) goto producer_done;
                             uint8_t* st = sm.stages + s * kLgStageBytes;
@@ -256,8 +280,8 @@ __device__ __forceinline__ void lg_body(const LogitsParams& p, const CUtensorMap
                 int it = 0;
                 for (int unit = cid; unit < sc.n_units; unit += n_pairs) {
                     int mp, split;
-                    decode_grouped(unit, sc.n_mp, p.S, kFwdGroup, &mp, &split);
-                    const int n_items = lg_items(p, split);
+                    decode_grouped(unit, sc.n_mp, sc.S, kFwdGroup, &mp, &split);
+                    const int n_items = lg_items(p, sc, split);
                     for (int item = 0; item < n_items; ++item)
                         for (int k0 = 0; k0 < sc.ks; k0 += kStagesPerPiece, ++it) {
                             const int b = it & 1;
@@ -328,11 +352,11 @@ __device__ __forceinline__ void lg_body(const LogitsParams& p, const CUtensorMap
     }
 }
 
-template <bool kBf16, bool kKeep, bool kEnt>
+template <bool kBf16, int kMode>
 __global__ void __launch_bounds__(kHeadThreads, 1)
     head_logits_kernel(const __grid_constant__ LogitsParams p, const __grid_constant__ CUtensorMap mA,
                        const __grid_constant__ CUtensorMap mB) {
-    lg_body<kBf16, kKeep, kEnt>(p, mA, mB);
+    lg_body<kBf16, kMode>(p, mA, mB);
 }
 
 template <class K>
@@ -510,9 +534,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int vr = tile * kFewVocab + 32 * quarter + lane;
 #pragma unroll
             for (int n = 0; n < kNC; ++n) {
-                const float z = vr < p.V && vr != s_tok[n] ? a[n] * p.zscale : kNoLogit;
-                const float mn = fmaxf(m[n], z * kLog2e);
-                const float f = fast_exp2(m[n] - mn), x = fast_exp2(fmaf(z, kLog2e, -mn));
+                const float z = vr < p.V && vr != s_tok[n] ? a[n] : kNoLogit;
+                const float mn = fmaxf(m[n], z * p.zscale2);
+                const float f = fast_exp2(m[n] - mn), x = fast_exp2(fmaf(z, p.zscale2, -mn));
                 s[n] = fmaf(s[n], f, x);
                 u[n] = fmaf(u[n], f, x * z);
                 m[n] = mn;
@@ -534,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 s_part[quarter][n][0] = mw;
                 s_part[quarter][n][1] = sw;
-                s_part[quarter][n][2] = uw;
+                s_part[quarter][n][2] = uw * p.zscale;
             }
         }
     epi_done:;
@@ -661,6 +685,8 @@ struct HeadDhT : DhPairT {
         }
         const int t = valid ? p.rows[sc.c0 + slot] : 0;
         if (valid && !GRPO_DCHECK(t >= 0 && t < p.N, p.status)) valid = false;
+        const float scale = sc.winv * dh_gain(p.V, 1);
+        const float f = p.rowf && valid ? scale * p.rowf[slot] : scale;
         uint16_t* out = p.dH + static_cast<int64_t>(t) * p.d;
         bool bad = false;
 #pragma unroll 1
@@ -672,8 +698,8 @@ struct HeadDhT : DhPairT {
             uint32_t pk[16];
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
-                v[j] *= sc.winv;
-                v[j + 1] *= sc.winv;
+                v[j] *= f;
+                v[j + 1] *= f;
                 pk[j / 2] = pack2(v[j], v[j + 1], kBf16);
                 bad |= !kBf16 ? half2_nonfinite(pk[j / 2]) : !(isfinite(v[j]) && isfinite(v[j + 1]));
             }
@@ -768,15 +794,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 cudaError_t launch_head_logits(const LogitsParams& p, const CUtensorMap& mH, const CUtensorMap& mW, int n_sm, bool bf16,
-                               bool keep, bool entropy, cudaStream_t st) {
-    if (keep)
-        return bf16 ? launch_logits(head_logits_kernel<true, true, false>, p, mH, mW, n_sm, st)
-                    : launch_logits(head_logits_kernel<false, true, false>, p, mH, mW, n_sm, st);
-    if (entropy)
-        return bf16 ? launch_logits(head_logits_kernel<true, false, true>, p, mH, mW, n_sm, st)
-                    : launch_logits(head_logits_kernel<false, false, true>, p, mH, mW, n_sm, st);
-    return bf16 ? launch_logits(head_logits_kernel<true, false, false>, p, mH, mW, n_sm, st)
-                : launch_logits(head_logits_kernel<false, false, false>, p, mH, mW, n_sm, st);
+                               int mode, cudaStream_t st) {
+    switch (mode) {
+        case LG_KEEP_TOKEN: return launch_logits(head_logits_kernel<true, LG_KEEP_TOKEN>, p, mH, mW, n_sm, st);
+        case LG_KEEP_MAX:
+            return bf16 ? launch_logits(head_logits_kernel<true, LG_KEEP_MAX>, p, mH, mW, n_sm, st)
+                        : launch_logits(head_logits_kernel<false, LG_KEEP_MAX>, p, mH, mW, n_sm, st);
+        case LG_ENTROPY:
+            return bf16 ? launch_logits(head_logits_kernel<true, LG_ENTROPY>, p, mH, mW, n_sm, st)
+                        : launch_logits(head_logits_kernel<false, LG_ENTROPY>, p, mH, mW, n_sm, st);
+        default:
+            return bf16 ? launch_logits(head_logits_kernel<true, LG_STATS>, p, mH, mW, n_sm, st)
+                        : launch_logits(head_logits_kernel<false, LG_STATS>, p, mH, mW, n_sm, st);
+    }
 }
 
 cudaError_t launch_head_dh(const HeadChunkParams& p, const CUtensorMap& mDS, const CUtensorMap& mWmn, int n_sm, bool bf16,

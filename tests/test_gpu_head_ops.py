@@ -434,3 +434,65 @@ def test_the_binding_refuses_what_the_c_interface_cannot_see():
                dict(out=q.double()), dict(W=torch.empty(64, 100, dtype=torch.bfloat16, device="cuda").t())):
         with pytest.raises(ValueError):
             call(**kw)
+
+
+def far_case(n_groups, G, L, V, chunk_rows, n_far, seed, **kw):
+    """Large enough for dlogits relative to the token's logit (rows x V >= 2^24); n_far rows where another token is
+    about 100 nats above the given one, which that form cannot hold."""
+    c = Case(n_groups, G, L, 64, V, "bf16", "ragged", seed=seed, chunk_rows=chunk_rows, **kw)
+    rows = c.P.rows[:: max(1, len(c.P.rows) // max(1, n_far))][:n_far]
+    W = c.W.float().cpu()
+    for t in rows:
+        o = (int(c.tok[t]) + 17) % V
+        c.h[t] = (100.0 * W[o] / float(W[o] @ W[o]) - 20.0 * W[int(c.tok[t])]).to(torch.bfloat16).cuda()
+    c.P.h = c.h.double().cpu().numpy()
+    return c
+
+
+@pytest.mark.parametrize("n_far", [0, 1, 40])
+@pytest.mark.parametrize("chunk_rows", [0, 128])
+def test_relative_dlogits_clip(n_far, chunk_rows):
+    c = far_case(1, 2, 125, 70001 if chunk_rows == 0 else 131080, chunk_rows, n_far, 20)
+    adv = np.array([1.5, -0.75], np.float32)
+    old, ref = c.old_ref()
+    t = lambda x: torch.from_numpy(x).cuda()  # noqa: E731
+    opts = rg.clip_opts(clip_high=0.28)
+    loss, st, dH, dW = c.clip(t(adv), t(old), t(ref), opts)
+    rl, rs, g, lp = R.clip_loss(c.P, adv, clean(old, c.P.mask), clean(ref, c.P.mask), c.beta, 0.2, 0.28, False)
+    assert n_far == 0 or rs[:, 0].min() < -80
+    qb = R.logp_bound(c.P)
+    assert np.all(np.abs(host(st)[:, 0] - rs[:, 0]) <= qb * c.P.mask)
+    assert abs(float(loss) - rl) <= (1.5 * rs[:, 1].max() + c.beta * 6) * qb.max() + 2e-6
+    check_grads(c, dH, dW, g, lp)
+    l2, s2 = c.clip(t(adv), t(old), t(ref), opts, bwd=False)
+    assert torch.equal(l2, loss) and torch.equal(s2, st)
+
+
+@pytest.mark.parametrize("n_far", [0, 3])
+@pytest.mark.parametrize("chunk_rows", [0, 128, 256])
+def test_relative_dlogits_pair(n_far, chunk_rows):
+    c = far_case(2, 2, 90, 131080, chunk_rows, n_far, 21, beta=0.1)
+    _, ref = c.old_ref()
+    loss, q, st, dH, dW = c.pair(torch.from_numpy(ref).cuda(), rg.pair_opts())
+    rl, rs, g, lp = R.pair_loss(c.P, clean(ref, c.P.mask), c.beta)
+    check_logp(c, q, None)
+    S_err = 90 * R.logp_bound(c.P).max()
+    assert abs(float(loss) - rl) <= 2 * c.beta * S_err + 1e-6
+    rH, rW, aH, aW = R.gradients(c.P, g, lp)
+    rel = 2 * c.beta * S_err   # d log |sigmoid(-m)| / dm is at most 1
+    assert np.all(np.abs(host(dH) - rH) <= R.grad_bound(rH, (1 + rel) * aH, "bf16", "bf16", 1e-4 + rel, 1.0))
+    assert np.all(np.abs(host(dW) - rW) <= R.grad_bound(rW, (1 + rel) * aW, "bf16", "bf16", 1e-4 + rel, 1.0))
+    l2, q2, s2 = c.pair(torch.from_numpy(ref).cuda(), rg.pair_opts(), bwd=False)
+    assert torch.equal(l2, loss) and torch.equal(q2, q) and torch.equal(s2, st)
+
+
+def test_relative_dlogits_of_given_gradients_and_bad_tokens():
+    c = far_case(1, 1, 250, 70001, 0, 2, 22)
+    dq = torch.randn(250, generator=torch.Generator().manual_seed(1))
+    dH, dW = c.logp_bwd(dq.cuda(), 8.0, True)
+    check_grads(c, dH, dW, clean(dq.numpy(), c.P.mask), R.logp_entropy(c.P)[2], 8.0, True)
+    c = far_case(1, 1, 250, 70001, 0, 0, 23)
+    c.tok = c.tok.clone()
+    c.tok[3], c.tok[4] = 70001, -5
+    dH, dW = c.logp_bwd(dq.cuda())
+    assert int(c.status) == 2 and int(c.inf) == 0 and not dH[3:5].any() and bool(torch.isfinite(dW.float()).all())

@@ -86,7 +86,10 @@ def test_head_operator_workspaces(lib):
     w = rg.grpo_policy_workspace_bytes
     long = rg.make_shape(1, 8, 20000, d, V)
     assert w(long, "clip") - w(long, "clip", True) == 4 * V * d
-    assert w(long, "clip", True) < 2 * 2 * long.N * V // 40
+    R = 9728                                                            # 76 tiles of 128 rows by default
+    assert R * V * 2 < w(long, "clip", True) < R * V * 2 * 5 // 4 < 2 * 2 * long.N * V // 25
+    small = rg.make_shape(1, 8, 20000, d, V, chunk_rows=1000)           # rounded up to 8 tiles
+    assert 1024 * V * 2 < w(small, "clip", True) < 1024 * V * 2 * 2
     assert w(long, "logp") < 1 << 28
     one = rg.make_shape(1, 2, 1000, d, V)
     assert w(one, "clip") == w(one, "clip", True)                       # one chunk: no fp32 sum
