@@ -307,39 +307,42 @@ def grpo_selftest_wait_timeout(status, waited_ns, stream=None):
 # tensor of the stated type and number of elements (the C interface sees only
 # its pointer).  Integers pass as raw pointers, unchecked.
 
-def _arg(x, name, dtypes, numel):
+_types_of = None   # type name -> tuple of torch types, set at the first check
+
+
+def _types():
+    global _types_of
+    if _types_of is None:
+        import torch
+        _types_of = {"f32": (torch.float32,), "i32": (torch.int32,), "mask": (torch.uint8, torch.bool),
+                     BF16: (torch.bfloat16,), FP16: (torch.float16,)}
+    return _types_of
+
+
+def _arg(x, name, types, numel):
     if x is None or isinstance(x, int):
-        return _ptr(x)
-    if not x.is_cuda:
-        raise ValueError(f"{name}: a CUDA tensor is wanted")
-    if str(x.dtype).replace("torch.", "") not in dtypes:
-        raise ValueError(f"{name}: type {x.dtype}, wanted {' or '.join(dtypes)}")
-    if x.numel() != numel:
-        raise ValueError(f"{name}: {x.numel()} elements, wanted {numel}")
-    if not x.is_contiguous():
-        raise ValueError(f"{name}: a contiguous tensor is wanted")
-    return _ptr(x)
-
-
-_F32, _I32 = ("float32",), ("int32",)
-
-
-def _head_type(shape):
-    return {BF16: ("bfloat16",), FP16: ("float16",)}.get(shape.dtype, ())
+        return x
+    if x.dtype in types and x.numel() == numel and x.is_cuda and x.is_contiguous():
+        return x.data_ptr()
+    raise ValueError(f"{name}: a contiguous CUDA tensor of {numel} elements of type {' or '.join(map(str, types))} is "
+                     f"wanted, not {x.dtype}, shape {tuple(x.shape)}, strides {x.stride()}, on {x.device}")
 
 
 def _inputs(h, W, tokens, mask, shape):
-    t = _head_type(shape)
-    if not t:
+    """(the four pointers), rows, type tables"""
+    ty = _types()
+    t = ty.get(shape.dtype)
+    if t is None:
         raise GrpoError(5, "dtype check")
-    return (_arg(h, "h", t, shape.N * shape.d), _arg(W, "W", t, shape.V * shape.d), _arg(tokens, "tokens", _I32, shape.N),
-            _arg(mask, "mask", ("uint8", "bool"), shape.N))
+    N, d = shape.N, shape.d
+    return (_arg(h, "h", t, N * d), _arg(W, "W", t, shape.V * d), _arg(tokens, "tokens", ty["i32"], N),
+            _arg(mask, "mask", ty["mask"], N)), N, ty
 
 
-def _grads(dH, dW, found_inf, shape, dw_f32):
-    t = _head_type(shape)
-    return (_arg(dH, "dH", t, shape.N * shape.d), _arg(dW, "dW", _F32 if dw_f32 else t, shape.V * shape.d),
-            _arg(found_inf, "found_inf", _I32, 1))
+def _grads(dH, dW, found_inf, shape, dw_f32, ty):
+    t, d = ty[shape.dtype], shape.d
+    return (_arg(dH, "dH", t, shape.N * d), _arg(dW, "dW", ty["f32"] if dw_f32 else t, shape.V * d),
+            _arg(found_inf, "found_inf", ty["i32"], 1))
 
 
 def _workspace(ws):
@@ -371,61 +374,69 @@ def grpo_policy_workspace_bytes(shape: GrpoShape, op, dw_f32=False) -> int:
 
 def grpo_logprobs(h, W, tokens, mask, shape, temperature, workspace, logp_out, entropy_out, status, stream=None):
     """q (and the entropy, unless None) of every row's token; mask None counts every row."""
-    N = shape.N
-    _check(load().grpo_logprobs(*_inputs(h, W, tokens, mask, shape), ctypes.byref(shape), float(temperature),
-                                *_workspace(workspace), _arg(logp_out, "logp_out", _F32, N),
-                                _arg(entropy_out, "entropy_out", _F32, N), _arg(status, "status", _I32, 1),
-                                _stream(stream)), "grpo_logprobs")
+    x, N, ty = _inputs(h, W, tokens, mask, shape)
+    f, i = ty["f32"], ty["i32"]
+    _check(load().grpo_logprobs(*x, ctypes.byref(shape), temperature, *_workspace(workspace),
+                                _arg(logp_out, "logp_out", f, N), _arg(entropy_out, "entropy_out", f, N),
+                                _arg(status, "status", i, 1), _stream(stream)), "grpo_logprobs")
 
 
 def grpo_logprobs_bwd(h, W, tokens, mask, dlogp, shape, temperature, loss_scale, workspace, dH, dW, found_inf, status,
                       dw_f32=False, stream=None):
     """Gradients of sum dlogp q."""
-    g = _grads(dH, dW, found_inf, shape, dw_f32)
-    _check(load().grpo_logprobs_bwd(*_inputs(h, W, tokens, mask, shape), _arg(dlogp, "dlogp", _F32, shape.N),
-                                    ctypes.byref(shape), float(temperature), float(loss_scale), int(bool(dw_f32)),
-                                    *_workspace(workspace), *g, _arg(status, "status", _I32, 1), _stream(stream)),
-           "grpo_logprobs_bwd")
+    x, N, ty = _inputs(h, W, tokens, mask, shape)
+    g = _grads(dH, dW, found_inf, shape, dw_f32, ty)
+    _check(load().grpo_logprobs_bwd(*x, _arg(dlogp, "dlogp", ty["f32"], N), ctypes.byref(shape), temperature, loss_scale,
+                                    int(bool(dw_f32)), *_workspace(workspace), *g, _arg(status, "status", ty["i32"], 1),
+                                    _stream(stream)), "grpo_logprobs_bwd")
 
 
-def _clip_inputs(h, W, tokens, mask, adv, logp_old, logp_ref, shape):
-    return (*_inputs(h, W, tokens, mask, shape), _arg(adv, "adv", _F32, shape.n_groups * shape.G),
-            _arg(logp_old, "logp_old", _F32, shape.N), _arg(logp_ref, "logp_ref", _F32, shape.N))
+def _clip_args(h, W, tokens, mask, adv, logp_old, logp_ref, shape):
+    x, N, ty = _inputs(h, W, tokens, mask, shape)
+    f = ty["f32"]
+    return (*x, _arg(adv, "adv", f, shape.n_groups * shape.G), _arg(logp_old, "logp_old", f, N),
+            _arg(logp_ref, "logp_ref", f, N), ctypes.byref(shape)), N, ty
 
 
 def grpo_clip_loss_fwd(h, W, tokens, mask, adv, logp_old, logp_ref, shape, opts, workspace, loss_out, row_stats, status,
                        stream=None):
-    _check(load().grpo_clip_loss_fwd(*_clip_inputs(h, W, tokens, mask, adv, logp_old, logp_ref, shape),
-                                     ctypes.byref(shape), ctypes.byref(opts), *_workspace(workspace),
-                                     _arg(loss_out, "loss_out", _F32, 1), _arg(row_stats, "row_stats", _F32, 3 * shape.N),
-                                     _arg(status, "status", _I32, 1), _stream(stream)), "grpo_clip_loss_fwd")
+    x, N, ty = _clip_args(h, W, tokens, mask, adv, logp_old, logp_ref, shape)
+    f, i = ty["f32"], ty["i32"]
+    _check(load().grpo_clip_loss_fwd(*x, ctypes.byref(opts), *_workspace(workspace), _arg(loss_out, "loss_out", f, 1),
+                                     _arg(row_stats, "row_stats", f, 3 * N), _arg(status, "status", i, 1),
+                                     _stream(stream)), "grpo_clip_loss_fwd")
 
 
 def grpo_clip_loss_fwd_bwd(h, W, tokens, mask, adv, logp_old, logp_ref, shape, opts, loss_scale, workspace, loss_out, dH,
                            dW, found_inf, row_stats, status, stream=None):
-    g = _grads(dH, dW, found_inf, shape, opts.dw_f32)
-    _check(load().grpo_clip_loss_fwd_bwd(*_clip_inputs(h, W, tokens, mask, adv, logp_old, logp_ref, shape),
-                                         ctypes.byref(shape), ctypes.byref(opts), float(loss_scale),
-                                         *_workspace(workspace), _arg(loss_out, "loss_out", _F32, 1), *g,
-                                         _arg(row_stats, "row_stats", _F32, 3 * shape.N),
-                                         _arg(status, "status", _I32, 1), _stream(stream)), "grpo_clip_loss_fwd_bwd")
+    x, N, ty = _clip_args(h, W, tokens, mask, adv, logp_old, logp_ref, shape)
+    f, i = ty["f32"], ty["i32"]
+    g = _grads(dH, dW, found_inf, shape, opts.dw_f32, ty)
+    _check(load().grpo_clip_loss_fwd_bwd(*x, ctypes.byref(opts), loss_scale, *_workspace(workspace),
+                                         _arg(loss_out, "loss_out", f, 1), *g, _arg(row_stats, "row_stats", f, 3 * N),
+                                         _arg(status, "status", i, 1), _stream(stream)), "grpo_clip_loss_fwd_bwd")
+
+
+def _pair_args(h, W, tokens, mask, logp_ref, shape):
+    x, N, ty = _inputs(h, W, tokens, mask, shape)
+    return (*x, _arg(logp_ref, "logp_ref", ty["f32"], N), ctypes.byref(shape)), N, ty
 
 
 def grpo_pair_loss_fwd(h, W, tokens, mask, logp_ref, shape, opts, workspace, loss_out, logp_out, pair_stats, status,
                        stream=None):
-    _check(load().grpo_pair_loss_fwd(*_inputs(h, W, tokens, mask, shape), _arg(logp_ref, "logp_ref", _F32, shape.N),
-                                     ctypes.byref(shape), ctypes.byref(opts), *_workspace(workspace),
-                                     _arg(loss_out, "loss_out", _F32, 1), _arg(logp_out, "logp_out", _F32, shape.N),
-                                     _arg(pair_stats, "pair_stats", _F32, 4 * shape.n_groups),
-                                     _arg(status, "status", _I32, 1), _stream(stream)), "grpo_pair_loss_fwd")
+    x, N, ty = _pair_args(h, W, tokens, mask, logp_ref, shape)
+    f, i = ty["f32"], ty["i32"]
+    _check(load().grpo_pair_loss_fwd(*x, ctypes.byref(opts), *_workspace(workspace), _arg(loss_out, "loss_out", f, 1),
+                                     _arg(logp_out, "logp_out", f, N), _arg(pair_stats, "pair_stats", f, 4 * shape.n_groups),
+                                     _arg(status, "status", i, 1), _stream(stream)), "grpo_pair_loss_fwd")
 
 
 def grpo_pair_loss_fwd_bwd(h, W, tokens, mask, logp_ref, shape, opts, loss_scale, workspace, loss_out, dH, dW, found_inf,
                            logp_out, pair_stats, status, stream=None):
-    g = _grads(dH, dW, found_inf, shape, opts.dw_f32)
-    _check(load().grpo_pair_loss_fwd_bwd(*_inputs(h, W, tokens, mask, shape), _arg(logp_ref, "logp_ref", _F32, shape.N),
-                                         ctypes.byref(shape), ctypes.byref(opts), float(loss_scale),
-                                         *_workspace(workspace), _arg(loss_out, "loss_out", _F32, 1), *g,
-                                         _arg(logp_out, "logp_out", _F32, shape.N),
-                                         _arg(pair_stats, "pair_stats", _F32, 4 * shape.n_groups),
-                                         _arg(status, "status", _I32, 1), _stream(stream)), "grpo_pair_loss_fwd_bwd")
+    x, N, ty = _pair_args(h, W, tokens, mask, logp_ref, shape)
+    f, i = ty["f32"], ty["i32"]
+    g = _grads(dH, dW, found_inf, shape, opts.dw_f32, ty)
+    _check(load().grpo_pair_loss_fwd_bwd(*x, ctypes.byref(opts), loss_scale, *_workspace(workspace),
+                                         _arg(loss_out, "loss_out", f, 1), *g, _arg(logp_out, "logp_out", f, N),
+                                         _arg(pair_stats, "pair_stats", f, 4 * shape.n_groups),
+                                         _arg(status, "status", i, 1), _stream(stream)), "grpo_pair_loss_fwd_bwd")

@@ -170,6 +170,13 @@ struct PairParams {
     int* status;
 };
 
+struct LossParams {
+    const float* ell;        // weighted objective per valid row, or nullptr
+    const double* pair_ell;  // per pair, or nullptr
+    int n_pairs;
+    float* loss;             // nullptr: nothing to do
+};
+
 // ChunkParams of the head operators' GEMMs
 struct HeadChunkParams : ChunkParams {
     float* dw_acc;          // fp32 dW (the caller's, or the workspace's when dw16 is given and there are several chunks)
@@ -202,11 +209,10 @@ cudaError_t launch_head_dlogits(const HeadChunkParams& p, float* oscale, bool bf
 cudaError_t launch_head_scale(const HeadChunkParams& p, float* oscale, int sm_count, cudaStream_t st);
 cudaError_t launch_head_dh(const HeadChunkParams& p, const CUtensorMap& mDS, const CUtensorMap& mWmn, int n_sm, bool bf16,
                            cudaStream_t st);
-cudaError_t launch_head_dh_join(const HeadChunkParams& p, bool bf16, int sm_count, cudaStream_t st);
+cudaError_t launch_head_dh_join(const HeadChunkParams& p, const LossParams& l, bool bf16, int sm_count, cudaStream_t st);
 cudaError_t launch_head_dw(const HeadChunkParams& p, const CUtensorMap& mDSmn, const CUtensorMap& mHct, int n_sm, bool bf16,
                            cudaStream_t st);
-cudaError_t launch_row_loss(const float* ell, const int* counts, float* loss, cudaStream_t st);
-cudaError_t launch_pair_loss(const double* ell, int n_pairs, const int* counts, float* loss, cudaStream_t st);
+cudaError_t launch_loss(const LossParams& l, const int* counts, cudaStream_t st);
 cudaError_t launch_few_prep(const FewParams& p, const uint16_t* h, const uint16_t* W, bool bf16, double* zt, cudaStream_t st);
 cudaError_t launch_few(const FewParams& p, const CUtensorMap& mH, const CUtensorMap& mW, int grid, bool bf16, int nc,
                        cudaStream_t st);

@@ -405,6 +405,18 @@ struct HeadRun {
         return GRPO_OK;
     }
 
+    LossParams loss() const {
+        LossParams l = {};
+        l.loss = c.loss;
+        if (c.mode == HEAD_PAIR) {
+            l.pair_ell = at<double>(L.pair_ell);
+            l.n_pairs = c.shape->n_groups;
+        } else {
+            l.ell = at<float>(L.ell);
+        }
+        return l;
+    }
+
     int gradients(int chunk, int gmax_chunk) {
         const grpo_shape& s = *c.shape;
         HeadChunkParams p = {};
@@ -443,7 +455,8 @@ struct HeadRun {
         HEAD_LAUNCH(GRPO_PROF_DLOGITS, launch_head_dlogits(p, at<float>(L.oscale), bf16, dev.sm_count, st));
         if (L.relative) HEAD_LAUNCH(GRPO_PROF_DLOGITS, launch_head_scale(p, at<float>(L.oscale), dev.sm_count, st));
         HEAD_LAUNCH(GRPO_PROF_DH, launch_head_dh(p, mDS_k, mW_mn, dev.sm_count, bf16, st));
-        HEAD_LAUNCH(GRPO_PROF_DH, launch_head_dh_join(p, bf16, dev.sm_count, st));
+        const LossParams l = chunk + 1 == L.max_chunks ? loss() : LossParams{};   // all rows are merged by then
+        HEAD_LAUNCH(GRPO_PROF_DH, launch_head_dh_join(p, l, bf16, dev.sm_count, st));
         HEAD_LAUNCH(GRPO_PROF_DW, launch_head_dw(p, mDS_mn, mHct, dev.sm_count, bf16, st));
         return GRPO_OK;
     }
@@ -484,11 +497,7 @@ struct HeadRun {
             if (rel) HEAD_STEP(logits(i, LG_KEEP_MAX, true, at<int>(L.far) + i));
             HEAD_STEP(gradients(i, 0));
         }
-        if (c.mode == HEAD_CLIP)
-            HEAD_LAUNCH(GRPO_PROF_MERGE, launch_row_loss(at<float>(L.ell), at<int>(L.counts), c.loss, st));
-        if (c.mode == HEAD_PAIR)
-            HEAD_LAUNCH(GRPO_PROF_MERGE,
-                        launch_pair_loss(at<double>(L.pair_ell), c.shape->n_groups, at<int>(L.counts), c.loss, st));
+        if (c.loss && !c.backward) HEAD_LAUNCH(GRPO_PROF_MERGE, launch_loss(loss(), at<int>(L.counts), st));
         return GRPO_OK;
     }
 };

@@ -5,9 +5,12 @@
 namespace grpo {
 
 // A row's partials (m, s, u) joined with its given token, whose column the
-// logits kernels left out.  With M = max m and everything relative to 2^M,
-//   lse = ln 2 (M + log2 s),   q = z_tok - lse,   H = -sum p log p = lse - u / s.
-// The last additions are in fp64: q is a difference of two numbers of about 10.
+// logits kernels left out.  With M = max m, everything relative to 2^M, and
+// x = s 2^M / e^z_tok (the other tokens' weight against the given one's),
+//   q = -log(1 + x),   lse = z_tok - q,   H = -sum p log p = lse - E[z].
+// log1p keeps q's relative precision however near the token's probability is
+// to 1.  The differences of numbers of about 10 are in fp64, the functions in
+// fp32 (fp64 ones cost microseconds).
 struct RowSum {
     double lse, q;
     float ent;
@@ -19,11 +22,10 @@ __device__ __forceinline__ RowSum join_row(const float4* part, int S2, int lane,
     for (int k = lane; k < S2; k += 32) m = fmaxf(m, __ldcg(part + k).x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    m = fmaxf(m, static_cast<float>(zt * kLog2eD));
     float s = 0.f, u = 0.f;
     for (int k = lane; k < S2; k += 32) {
         const float4 ps = __ldcg(part + k);
-        const float f = exp2f(ps.x - m);   // 0 for a part that held the token's column alone
+        const float f = exp2f(ps.x - m);
         s = fmaf(ps.y, f, s);
         u = fmaf(ps.z, f, u);
     }
@@ -32,12 +34,23 @@ __device__ __forceinline__ RowSum join_row(const float4* part, int S2, int lane,
         s += __shfl_xor_sync(0xffffffffu, s, o);
         u += __shfl_xor_sync(0xffffffffu, u, o);
     }
-    const double et = exp2(zt * kLog2eD - static_cast<double>(m));
-    const double sd = static_cast<double>(s) + et;
     RowSum r;
-    r.lse = (static_cast<double>(m) + log2(sd)) * kLn2D;
-    r.q = zt - r.lse;
-    const float ent = static_cast<float>(r.lse - (static_cast<double>(u) + et * zt) / sd);
+    float mean;   // E[z]
+    const double dm = static_cast<double>(m) - zt * kLog2eD;
+    if (dm < 80.0) {
+        const float f = exp2f(static_cast<float>(dm));   // 0 when there is no other token: m is about -2^100
+        const float x = s * f;
+        r.q = -static_cast<double>(log1pf(x));
+        r.lse = zt - r.q;
+        mean = (fmaf(u, f, static_cast<float>(zt))) / (1.f + x);
+    } else {   // p below 2^-80: the given token adds nothing
+        int ex;
+        const float mant = frexpf(s, &ex);
+        r.lse = (static_cast<double>(m) + ex + static_cast<double>(log2f(mant))) * kLn2D;
+        r.q = zt - r.lse;
+        mean = u / s;
+    }
+    const float ent = static_cast<float>(r.lse - static_cast<double>(mean));
     r.ent = ent < 0.f ? 0.f : ent;
     return r;
 }
@@ -53,7 +66,7 @@ __device__ __forceinline__ RowSum join_row_relative(const float4* part, int S2, 
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     const double base = static_cast<double>(__ldcg(part).x);
     RowSum r;
-    r.q = -log1p(static_cast<double>(s) * exp2(base - zt * 1.4426950408889634074));
+    r.q = -static_cast<double>(log1pf(s * exp2f(static_cast<float>(base - zt * 1.4426950408889634074))));
     r.lse = zt - r.q;
     r.ent = 0.f;
     return r;

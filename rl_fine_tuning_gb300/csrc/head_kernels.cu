@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 
 #include "head_join.cuh"
+#include "ptx.cuh"
 
 namespace grpo {
 
@@ -383,6 +384,7 @@ cudaError_t launch_head_gather(const GatherParams& p, bool bf16, int sm_count, c
 template <bool kBf16>
 __global__ void __launch_bounds__(32) k_few_prep(const FewParams p, const uint4* __restrict__ h,
                                                  const uint4* __restrict__ W, double* __restrict__ zt) {
+    chain_next();
     const int n = blockIdx.x, lane = threadIdx.x, vpr = p.d / 8;
     if (n == 0 && lane == 0) {
         *p.status = 0;
@@ -525,9 +527,10 @@ __global__ void __launch_bounds__(256) k_pair_coef(const PairParams p) {
                 ell = x * x;
                 dm = 2.0 * x / beta;
             } else {
-                const double up = log1p(exp(-fabs(m))) + (m < 0.0 ? -m : 0.0);   // -log sigmoid(m)
+                const float mf = static_cast<float>(m);
+                const double up = log1pf(expf(-fabsf(mf))) + (m < 0.0 ? -m : 0.0);   // -log sigmoid(m)
                 ell = up + e * m;                                                  // -log sigmoid(-m) = up + m
-                dm = e - 1.0 / (1.0 + exp(m));
+                dm = e - 1.f / (1.f + expf(mf));
             }
             if (m != m) ell = dm = m;   // a NaN stays one
         }
@@ -560,33 +563,30 @@ cudaError_t launch_pair_coef(const PairParams& p, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-// ------------------------------------------------------------ loss sums
-__global__ void __launch_bounds__(1024) k_row_loss(const float* __restrict__ ell, const int* __restrict__ counts,
-                                                   float* __restrict__ loss) {
-    __shared__ double sh[1024];
-    const int nv = counts[C_NVALID];
+// ------------------------------------------------------------ loss
+// Sums the rows' (or pairs') weighted objectives in fp64 in a fixed order, one
+// block of 256.  With a backward it is block 0 of the last dH join, else a kernel.
+__device__ __forceinline__ void write_loss(const LossParams& l, const int* counts) {
+    __shared__ double sh[256];
+    if (!l.loss) return;
     double acc = 0.0;
-    for (int i = threadIdx.x; i < nv; i += 1024) acc += static_cast<double>(ell[i]);
+    if (l.pair_ell) {
+        for (int i = threadIdx.x; i < l.n_pairs; i += 256) acc += l.pair_ell[i];
+    } else {
+        const int nv = counts[C_NVALID];
+        for (int i = threadIdx.x; i < nv; i += 256) acc += static_cast<double>(l.ell[i]);
+    }
     acc = block_sum(acc, sh);
-    if (threadIdx.x == 0) *loss = static_cast<float>(acc);
+    if (threadIdx.x == 0) {
+        const int n = l.pair_ell ? counts[C_NACT] : 1;   // rows carry their weight in the mean already
+        *l.loss = n > 0 ? static_cast<float>(acc / n) : 0.f;
+    }
 }
 
-cudaError_t launch_row_loss(const float* ell, const int* counts, float* loss, cudaStream_t st) {
-    k_row_loss<<<1, 1024, 0, st>>>(ell, counts, loss);
-    return cudaGetLastError();
-}
+__global__ void __launch_bounds__(256) k_loss(const LossParams l, const int* __restrict__ counts) { write_loss(l, counts); }
 
-__global__ void __launch_bounds__(1024) k_pair_loss(const double* __restrict__ ell, int n_pairs,
-                                                    const int* __restrict__ counts, float* __restrict__ loss) {
-    __shared__ double sh[1024];
-    double acc = 0.0;
-    for (int i = threadIdx.x; i < n_pairs; i += 1024) acc += ell[i];
-    acc = block_sum(acc, sh);
-    if (threadIdx.x == 0) *loss = counts[C_NACT] > 0 ? static_cast<float>(acc / counts[C_NACT]) : 0.f;
-}
-
-cudaError_t launch_pair_loss(const double* ell, int n_pairs, const int* counts, float* loss, cudaStream_t st) {
-    k_pair_loss<<<1, 1024, 0, st>>>(ell, n_pairs, counts, loss);
+cudaError_t launch_loss(const LossParams& l, const int* counts, cudaStream_t st) {
+    k_loss<<<1, 256, 0, st>>>(l, counts);
     return cudaGetLastError();
 }
 
@@ -751,7 +751,8 @@ cudaError_t launch_head_scale(const HeadChunkParams& p, float* oscale, int sm_co
 // One warp per row of a split dH tile: adds its K pieces in order, scales,
 // rounds and stores it.
 template <bool kBf16>
-__global__ void __launch_bounds__(256) k_dh_join(const HeadChunkParams p) {
+__global__ void __launch_bounds__(256) k_dh_join(const HeadChunkParams p, const LossParams l) {
+    if (blockIdx.x == 0) write_loss(l, p.counts);
     const int2 cbn = chunk_bounds(p.counts, p.cb, p.chunk);
     const int c0 = cbn.x, n_c = cbn.y;
     if (n_c == 0) return;
@@ -790,9 +791,9 @@ __global__ void __launch_bounds__(256) k_dh_join(const HeadChunkParams p) {
     if (bad) atomicOr(p.found_inf, 1);
 }
 
-cudaError_t launch_head_dh_join(const HeadChunkParams& p, bool bf16, int sm_count, cudaStream_t st) {
-    if (bf16) k_dh_join<true><<<sm_count * 4, 256, 0, st>>>(p);
-    else k_dh_join<false><<<sm_count * 4, 256, 0, st>>>(p);
+cudaError_t launch_head_dh_join(const HeadChunkParams& p, const LossParams& l, bool bf16, int sm_count, cudaStream_t st) {
+    if (bf16) k_dh_join<true><<<sm_count * 4, 256, 0, st>>>(p, l);
+    else k_dh_join<false><<<sm_count * 4, 256, 0, st>>>(p, l);
     return cudaGetLastError();
 }
 

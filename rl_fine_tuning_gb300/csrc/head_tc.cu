@@ -22,6 +22,7 @@
 //     of inputs (half as much again with outlier columns).  The forward
 //     kernels multiply it back in with the scale of the logits; what is left of a
 //     logit of 10 is below 1e-6, and 4e-8 of an average one.
+#include <atomic>
 #include <cfloat>
 
 #include "head_join.cuh"
@@ -359,10 +360,20 @@ __global__ void __launch_bounds__(kHeadThreads, 1)
     lg_body<kBf16, kMode>(p, mA, mB);
 }
 
-template <class K>
-cudaError_t launch_logits(K kern, const LogitsParams& p, const CUtensorMap& a, const CUtensorMap& b, int n_sm,
-                          cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLgSmem);
+// Shared memory limit and the number of clusters of two that fit on the device at
+// once, set and asked once per kernel and device: both calls cost the host as
+// much as a launch does.
+constexpr int kDevices = 64;
+
+template <auto kKern>
+cudaError_t pairs_fit(int threads, int smem, int n_sm, int* clusters) {
+    static std::atomic<int> known[kDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kDevices && (*clusters = known[dev].load(std::memory_order_acquire)) > 0) return cudaSuccess;
+    const void* fn = reinterpret_cast<const void*>(kKern);
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -370,19 +381,40 @@ cudaError_t launch_logits(K kern, const LogitsParams& p, const CUtensorMap& a, c
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    cfg.blockDim = dim3(kHeadThreads);
-    cfg.dynamicSmemBytes = kLgSmem;
+    cfg.gridDim = dim3(n_sm / 2 * 2);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    *clusters = n_sm / 2;
+    int active = 0;
+    if (cudaOccupancyMaxActiveClusters(&active, fn, &cfg) == cudaSuccess && active > 0 && active < *clusters)
+        *clusters = active;
+    if (*clusters < 1) return cudaErrorInvalidConfiguration;
+    if (dev < kDevices) known[dev].store(*clusters, std::memory_order_release);
+    return cudaSuccess;
+}
+
+// Persistent launch of a kernel on SM pairs: one CTA per SM, capped by how many
+// clusters fit on the device at once, so that every CTA runs concurrently.
+template <auto kKern, class... A>
+cudaError_t launch_pairs(int threads, int smem, int n_sm, cudaStream_t st, const A&... args) {
+    int clusters = 0;
+    const cudaError_t e = pairs_fit<kKern>(threads, smem, n_sm, &clusters);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(clusters * 2);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int clusters = n_sm / 2;
-    cfg.gridDim = dim3(clusters * 2);
-    int active = 0;
-    if (cudaOccupancyMaxActiveClusters(&active, kern, &cfg) == cudaSuccess && active > 0 && active < clusters)
-        clusters = active;
-    if (clusters < 1) return cudaErrorInvalidConfiguration;
-    cfg.gridDim = dim3(clusters * 2);
-    return cudaLaunchKernelEx(&cfg, kern, p, a, b);
+    return cudaLaunchKernelEx(&cfg, kKern, args...);
 }
 
 // ====================================================================== few rows
@@ -577,6 +609,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 2 * kNC);
     }
+    // W, h and the tokens are the caller's and were there before k_few_prep began;
+    // its own results (zt, the counter) are needed from here on
+    chain_wait();
     // this CTA's partial of each row
     const int n_cta = static_cast<int>(gridDim.x);
     if (static_cast<int>(threadIdx.x) < min(kNC, p.N)) {
@@ -796,38 +831,57 @@ __global__ void __launch_bounds__(kThreads, 1)
 cudaError_t launch_head_logits(const LogitsParams& p, const CUtensorMap& mH, const CUtensorMap& mW, int n_sm, bool bf16,
                                int mode, cudaStream_t st) {
     switch (mode) {
-        case LG_KEEP_TOKEN: return launch_logits(head_logits_kernel<true, LG_KEEP_TOKEN>, p, mH, mW, n_sm, st);
+        case LG_KEEP_TOKEN: return launch_pairs<head_logits_kernel<true, LG_KEEP_TOKEN>>(kHeadThreads, kLgSmem, n_sm, st, p, mH, mW);
         case LG_KEEP_MAX:
-            return bf16 ? launch_logits(head_logits_kernel<true, LG_KEEP_MAX>, p, mH, mW, n_sm, st)
-                        : launch_logits(head_logits_kernel<false, LG_KEEP_MAX>, p, mH, mW, n_sm, st);
+            return bf16 ? launch_pairs<head_logits_kernel<true, LG_KEEP_MAX>>(kHeadThreads, kLgSmem, n_sm, st, p, mH, mW)
+                        : launch_pairs<head_logits_kernel<false, LG_KEEP_MAX>>(kHeadThreads, kLgSmem, n_sm, st, p, mH, mW);
         case LG_ENTROPY:
-            return bf16 ? launch_logits(head_logits_kernel<true, LG_ENTROPY>, p, mH, mW, n_sm, st)
-                        : launch_logits(head_logits_kernel<false, LG_ENTROPY>, p, mH, mW, n_sm, st);
+            return bf16 ? launch_pairs<head_logits_kernel<true, LG_ENTROPY>>(kHeadThreads, kLgSmem, n_sm, st, p, mH, mW)
+                        : launch_pairs<head_logits_kernel<false, LG_ENTROPY>>(kHeadThreads, kLgSmem, n_sm, st, p, mH, mW);
         default:
-            return bf16 ? launch_logits(head_logits_kernel<true, LG_STATS>, p, mH, mW, n_sm, st)
-                        : launch_logits(head_logits_kernel<false, LG_STATS>, p, mH, mW, n_sm, st);
+            return bf16 ? launch_pairs<head_logits_kernel<true, LG_STATS>>(kHeadThreads, kLgSmem, n_sm, st, p, mH, mW)
+                        : launch_pairs<head_logits_kernel<false, LG_STATS>>(kHeadThreads, kLgSmem, n_sm, st, p, mH, mW);
     }
 }
 
 cudaError_t launch_head_dh(const HeadChunkParams& p, const CUtensorMap& mDS, const CUtensorMap& mWmn, int n_sm, bool bf16,
                            cudaStream_t st) {
-    return bf16 ? launch_tc<HeadDhT, 2>(head_dh_kernel<true>, p, mDS, mDS, mWmn, n_sm, st)
-                : launch_tc<HeadDhT, 2>(head_dh_kernel<false>, p, mDS, mDS, mWmn, n_sm, st);
+    return bf16 ? launch_pairs<head_dh_kernel<true>>(kThreads, smem_bytes<HeadDhT>(), n_sm, st, p, mDS, mDS, mWmn)
+                : launch_pairs<head_dh_kernel<false>>(kThreads, smem_bytes<HeadDhT>(), n_sm, st, p, mDS, mDS, mWmn);
 }
 
 cudaError_t launch_head_dw(const HeadChunkParams& p, const CUtensorMap& mDSmn, const CUtensorMap& mHct, int n_sm, bool bf16,
                            cudaStream_t st) {
-    return bf16 ? launch_tc<HeadDwT, 2>(head_dw_kernel<true>, p, mDSmn, mDSmn, mHct, n_sm, st)
-                : launch_tc<HeadDwT, 2>(head_dw_kernel<false>, p, mDSmn, mDSmn, mHct, n_sm, st);
+    return bf16 ? launch_pairs<head_dw_kernel<true>>(kThreads, smem_bytes<HeadDwT>(), n_sm, st, p, mDSmn, mDSmn, mHct)
+                : launch_pairs<head_dw_kernel<false>>(kThreads, smem_bytes<HeadDwT>(), n_sm, st, p, mDSmn, mDSmn, mHct);
 }
 
 template <bool kBf16, int kNC>
 static cudaError_t launch_few_t(const FewParams& p, const CUtensorMap& mH, const CUtensorMap& mW, int grid, cudaStream_t st) {
-    auto kern = head_few_kernel<kBf16, kNC>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, FewShape<kNC>::kSmem);
+    static std::atomic<int> known[kDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    kern<<<grid, kThreads, FewShape<kNC>::kSmem, st>>>(p, mH, mW);
-    return cudaGetLastError();
+    if (dev >= kDevices || !known[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(head_few_kernel<kBf16, kNC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 FewShape<kNC>::kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < kDevices) known[dev].store(1, std::memory_order_release);
+    }
+    // starts while k_few_prep runs (see chain_wait in the kernel): 2 us of 88 at 8 rows of a 152K vocabulary.
+    // The chunked operators' kernels are not chained this way: their waiting blocks cost more
+    // than the launches they hide (88 us instead of 53 for the smallest clipped-loss step).
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = FewShape<kNC>::kSmem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, head_few_kernel<kBf16, kNC>, p, mH, mW);
 }
 
 cudaError_t launch_few(const FewParams& p, const CUtensorMap& mH, const CUtensorMap& mW, int grid, bool bf16, int nc,

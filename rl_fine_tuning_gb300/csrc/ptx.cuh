@@ -347,6 +347,12 @@ __device__ __forceinline__ void umma_pair_commit(uint64_t* bar) {
                  : "memory");
 }
 
+// ---------------------------------------------------------------- dependent launches
+// chain_next: the next kernel in the stream, if launched as dependent, may start.
+// chain_wait, in that kernel: the predecessor has ended and its writes are there.
+__device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- registers per warpgroup
 // Executed by all four warps of a warpgroup.  The shares of a block's
 // warpgroups together stay within what the block was launched with.
