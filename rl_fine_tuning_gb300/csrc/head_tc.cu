@@ -36,7 +36,7 @@ constexpr int kStagesPerPiece = kPieceK / kBK;
 
 // ====================================================================== logits of a chunk
 
-constexpr int kLgStages = 6;
+constexpr int kLgStages = 7;
 constexpr int kLgStageBytes = 16384 + 16384;   // A (128 rows x 64), B half (128 vocabulary rows x 64)
 constexpr int kLgSmem = kLgStages * kLgStageBytes + 1024 + 512;
 
@@ -647,6 +647,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// Watches stored values for one that is not finite: 0 x is NaN for those alone, so
+// a sum of them tells with one instruction per (packed pair of) value.
+template <bool kBf16>
+struct Finite {
+    __nv_bfloat162 b = __floats2bfloat162_rn(0.f, 0.f);
+    __half2 h = __floats2half2_rn(0.f, 0.f);
+    float f = 0.f;
+    __device__ __forceinline__ void see(uint32_t pk) {
+        if (kBf16) b = __hfma2(reinterpret_cast<const __nv_bfloat162&>(pk), __floats2bfloat162_rn(0.f, 0.f), b);
+        else h = __hfma2(reinterpret_cast<const __half2&>(pk), __floats2half2_rn(0.f, 0.f), h);
+    }
+    __device__ __forceinline__ void see_f32(float x) { f = fmaf(x, 0.f, f); }
+    __device__ __forceinline__ bool bad() const {
+        const float2 t = kBf16 ? __bfloat1622float2(b) : __half22float2(h);
+        return !(t.x == 0.f && t.y == 0.f && f == 0.f);
+    }
+};
+
 // ====================================================================== dH, last wave split
 struct HeadDhT : DhPairT {
     using Params = HeadChunkParams;
@@ -723,7 +741,7 @@ struct HeadDhT : DhPairT {
         const float scale = sc.winv * dh_gain(p.V, 1);
         const float f = p.rowf && valid ? scale * p.rowf[slot] : scale;
         uint16_t* out = p.dH + static_cast<int64_t>(t) * p.d;
-        bool bad = false;
+        Finite<kBf16> fin;
 #pragma unroll 1
         for (int c = 0; c < kBN / 32; ++c) {
             const int col0 = n0 + c * 32;
@@ -733,10 +751,8 @@ struct HeadDhT : DhPairT {
             uint32_t pk[16];
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
-                v[j] *= f;
-                v[j + 1] *= f;
-                pk[j / 2] = pack2(v[j], v[j + 1], kBf16);
-                bad |= !kBf16 ? half2_nonfinite(pk[j / 2]) : !(isfinite(v[j]) && isfinite(v[j + 1]));
+                pk[j / 2] = pack2(v[j] * f, v[j + 1] * f, kBf16);
+                fin.see(pk[j / 2]);
             }
             if (valid) {
 #pragma unroll
@@ -745,7 +761,7 @@ struct HeadDhT : DhPairT {
                                  pk[8 * h + 4], pk[8 * h + 5], pk[8 * h + 6], pk[8 * h + 7]);
             }
         }
-        if (bad && valid) atomicOr(p.found_inf, 1);
+        if (valid && fin.bad()) atomicOr(p.found_inf, 1);
     }
     __device__ static void epi_end(const Params&, const Sched&, int, Epi&) {}
 };
@@ -753,11 +769,16 @@ struct HeadDhT : DhPairT {
 // ====================================================================== dW
 // DwPairT with the operators' output: chunks add up in fp32 (dw_acc), and with
 // dw16 the last chunk (often the only one) rounds the sum to the type of W.
+// With few rows a unit's MMAs are short (16 K-stages for 1024 rows, about 8200
+// clocks), so eight warps share the epilogue: four took longer than that.
 struct HeadDwT : DwPairT {
+    static constexpr int kEpiWarps = 8;
     using Params = HeadChunkParams;
     template <bool kBf16>
     __device__ static void epi_item(const Params& p, const Sched& sc, int unit, int, int rank, uint32_t tacc, Epi&) {
-        const int row = (threadIdx.x & 31) + 32 * ((threadIdx.x >> 5) & 3);
+        const int warp = threadIdx.x >> 5;
+        const int row = (threadIdx.x & 31) + 32 * (warp & 3);
+        const int half = (warp - 2) >> 2;
         const int v = vtile(sc, unit, rank) * kBM + row;
         const int n0 = dtile(sc, unit) * kBN;
         const bool valid = v < p.V;
@@ -765,9 +786,9 @@ struct HeadDwT : DwPairT {
         const bool first = p.chunk == 0;
         const bool last = p.dw16 && p.chunk + 1 == p.counts[C_NCHUNKS];
         const int64_t at = static_cast<int64_t>(valid ? v : 0) * p.d;
-        bool bad = false;
+        Finite<kBf16> fin;
 #pragma unroll 1
-        for (int c = 0; c < kBN / 32; ++c) {
+        for (int c = half * (kBN / 64); c < (half + 1) * (kBN / 64); ++c) {
             const int col0 = n0 + c * 32;
             if (col0 >= p.d) break;
             float x[32];
@@ -790,7 +811,7 @@ struct HeadDwT : DwPairT {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     pk[j] = pack2(x[2 * j], x[2 * j + 1], kBf16);
-                    bad |= !kBf16 ? half2_nonfinite(pk[j]) : !(isfinite(x[2 * j]) && isfinite(x[2 * j + 1]));
+                    fin.see(pk[j]);
                 }
                 uint16_t* out = p.dw16 + at + col0;
 #pragma unroll
@@ -799,7 +820,7 @@ struct HeadDwT : DwPairT {
                                  pk[8 * h + 5], pk[8 * h + 6], pk[8 * h + 7]);
             } else {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) bad |= !isfinite(x[j]);
+                for (int j = 0; j < 32; ++j) fin.see_f32(x[j]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     st_global_v8(acc + 8 * j, __float_as_uint(x[8 * j]), __float_as_uint(x[8 * j + 1]),
@@ -808,9 +829,10 @@ struct HeadDwT : DwPairT {
                                  __float_as_uint(x[8 * j + 6]), __float_as_uint(x[8 * j + 7]));
             }
         }
-        if (bad) atomicOr(p.found_inf, 1);
+        if (fin.bad()) atomicOr(p.found_inf, 1);
     }
 };
+constexpr int kDwThreads = 64 + 32 * HeadDwT::kEpiWarps;
 
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -820,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kDwThreads, 1)
     head_dw_kernel(const __grid_constant__ HeadChunkParams p, const __grid_constant__ CUtensorMap mA,
                    const __grid_constant__ CUtensorMap mA2, const __grid_constant__ CUtensorMap mB) {
     tc_pair_body<HeadDwT, kBf16>(p, mA, mA2, mB);
@@ -852,8 +874,8 @@ cudaError_t launch_head_dh(const HeadChunkParams& p, const CUtensorMap& mDS, con
 
 cudaError_t launch_head_dw(const HeadChunkParams& p, const CUtensorMap& mDSmn, const CUtensorMap& mHct, int n_sm, bool bf16,
                            cudaStream_t st) {
-    return bf16 ? launch_pairs<head_dw_kernel<true>>(kThreads, smem_bytes<HeadDwT>(), n_sm, st, p, mDSmn, mDSmn, mHct)
-                : launch_pairs<head_dw_kernel<false>>(kThreads, smem_bytes<HeadDwT>(), n_sm, st, p, mDSmn, mDSmn, mHct);
+    return bf16 ? launch_pairs<head_dw_kernel<true>>(kDwThreads, smem_bytes<HeadDwT>(), n_sm, st, p, mDSmn, mDSmn, mHct)
+                : launch_pairs<head_dw_kernel<false>>(kDwThreads, smem_bytes<HeadDwT>(), n_sm, st, p, mDSmn, mDSmn, mHct);
 }
 
 template <bool kBf16, int kNC>

@@ -363,6 +363,18 @@ struct WideAcc {
     static constexpr bool value = get<T>(nullptr);
 };
 
+// Epilogue warps of the pair engine: four (one accumulator row per thread), or
+// eight for a traits class with kEpiWarps = 8, whose second four take the upper
+// half of the columns.
+template <class T>
+struct EpiWarps {
+    template <class U>
+    static constexpr int get(decltype(U::kEpiWarps)*) { return U::kEpiWarps; }
+    template <class U>
+    static constexpr int get(...) { return 4; }
+    static constexpr int value = get<T>(nullptr);
+};
+
 template <class T>
 __device__ __forceinline__ int acc_buf(int it) {
     return WideAcc<T>::value ? 0 : (it & 1);
@@ -398,7 +410,7 @@ __device__ __forceinline__ void tc_pair_body(const typename T::Params& p, const 
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm.acc_full[b], 1);    // the leader's commit, multicast
-            mbar_init(&sm.acc_empty[b], 8);   // leader: the epilogue warps of both CTAs
+            mbar_init(&sm.acc_empty[b], 2 * EpiWarps<T>::value);   // leader: the epilogue warps of both CTAs
         }
         mbar_init(sm.drain, 1);
         *sm.abort_flag = 0;
