@@ -179,6 +179,7 @@ struct LossParams {
 
 // ChunkParams of the head operators' GEMMs
 struct HeadChunkParams : ChunkParams {
+    CUtensorMap mDw16;      // dw16 in boxes of 32 rows x 64
     float* dw_acc;          // fp32 dW (the caller's, or the workspace's when dw16 is given and there are several chunks)
     uint16_t* dw16;         // 16-bit dW, nullable
     float* dh_part;         // [slots][2][128 x 256] fp32

@@ -14,7 +14,7 @@ constexpr int64_t kPairChunkRowsMax = 19456;   // default chunks grow to hold on
 
 // bf16 chunks of at least this many logits use relative dlogits (k_head_scale)
 // instead of a pass over the dlogits; below, the pass is the shorter way
-constexpr int64_t kRelativeMin = 1 << 24;
+constexpr int64_t kRelativeMin = 1 << 22;
 
 struct HeadLayout {
     size_t counts, off, cb, pb, dh_plan, lg_plan, gmax, far, oscale, rowf, rows, zt, lse, gco, ell, q, pair_ell, hc, part, mx, ds, hct, dh_part,
@@ -227,7 +227,7 @@ struct HeadRun {
     cudaStream_t st;
     char* w;
     bool bf16;
-    CUtensorMap mW_k, mH_k, mW_mn, mHct, mDS_k, mDS_mn;
+    CUtensorMap mW_k, mH_k, mW_mn, mHct, mDS_k, mDS_mn, mDw16;
 
     template <class T>
     T* at(size_t off) const { return reinterpret_cast<T*>(w + off); }
@@ -240,7 +240,8 @@ struct HeadRun {
         if (c.backward && (!make_map(&mW_mn, c.W, bf16, s.d, s.V, s.d, 64, kBK) ||
                            !make_map(&mHct, at<void>(L.hct), bf16, L.R, s.d, L.R, kBK, 128) ||
                            !make_map(&mDS_k, at<void>(L.ds), bf16, s.V, L.R, L.V_pad, kBK, kBM) ||
-                           !make_map(&mDS_mn, at<void>(L.ds), bf16, s.V, L.R, L.V_pad, 64, kBK)))
+                           !make_map(&mDS_mn, at<void>(L.ds), bf16, s.V, L.R, L.V_pad, 64, kBK) ||
+                           (!c.dw_f32 && !make_map(&mDw16, c.dW, bf16, s.d, s.V, s.d, 64, 32))))
             return GRPO_ERR_LAUNCH;
         return GRPO_OK;
     }
@@ -440,6 +441,7 @@ struct HeadRun {
         p.dH = static_cast<uint16_t*>(c.dH);
         p.found_inf = c.found_inf;
         p.status = c.status;
+        p.mDw16 = mDw16;
         p.dw_acc = c.dw_f32 ? static_cast<float*>(c.dW) : at<float>(L.dw_acc);
         p.dw16 = c.dw_f32 ? nullptr : static_cast<uint16_t*>(c.dW);
         p.dh_part = at<float>(L.dh_part);
@@ -511,7 +513,7 @@ int head_call(const HeadCall& c, grpo_stream_t stream) {
     if (rc != GRPO_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (c.mode == HEAD_LOGP && L.N <= kFewRows) return run_few(c, L, dev, st);
-    HeadRun run{c, L, dev, st, static_cast<char*>(c.ws), c.shape->dtype == GRPO_BF16, {}, {}, {}, {}, {}, {}};
+    HeadRun run{c, L, dev, st, static_cast<char*>(c.ws), c.shape->dtype == GRPO_BF16, {}, {}, {}, {}, {}, {}, {}};
     return run.run();
 }
 

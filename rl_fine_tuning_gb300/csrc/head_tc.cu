@@ -141,10 +141,10 @@ __device__ __forceinline__ void lg_body(const LogitsParams& p, const CUtensorMap
             if (valid && !GRPO_DCHECK(t >= 0 && t < p.N, status)) valid = false;
             const int tok = valid ? p.tokens[t] : -1;
             RowStat e{kNoLogit2, 0.f, 0.f};
-            // LG_KEEP_TOKEN: the fixed base, and whether the row is stored (zeros up to the next multiple of 128)
-            bool stored = valid;
+            // rows past the chunk's last, up to the next multiple of 128: zeros with LG_KEEP_TOKEN (their
+            // compact rows are zeros; with LG_KEEP_MAX the dlogits pass writes them)
+            const bool stored = kToken ? p.E && slot < min(p.R, (sc.n_c + kBM - 1) / kBM * kBM) : valid;
             if (kToken) {
-                stored = p.E && slot < min(p.R, (sc.n_c + kBM - 1) / kBM * kBM);
                 const bool ok = valid && tok >= 0 && tok < p.V;
                 e.m = ok ? static_cast<float>(p.zt[t] * 1.4426950408889634074) : INFINITY;
             }
@@ -169,7 +169,6 @@ __device__ __forceinline__ void lg_body(const LogitsParams& p, const CUtensorMap
                     }
                 }
                 const int n0 = (split * sc.nps + item) * kBN + 128 * half;
-                uint16_t* erow = kKeep && stored ? p.E + static_cast<int64_t>(slot) * p.V_pad + n0 : nullptr;
                 float mv[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -220,11 +219,13 @@ __device__ __forceinline__ void lg_body(const LogitsParams& p, const CUtensorMap
                         mv[c] = base;
                     }
                     if (kKeep && stored && GRPO_DCHECK(col0 + 32 <= p.V_pad, status)) {
-                        // 64 bytes of one row as two whole 32-byte sectors
+                        // 64 bytes of one row as two whole 32-byte sectors.  (Boxes through shared memory
+                        // and TMA stores need a K-stage's room: 5% slower.)
+                        uint16_t* e16 = p.E + static_cast<int64_t>(slot) * p.V_pad + col0;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const float* w = v + 16 * h;
-                            st_global_v8(erow + 32 * c + 16 * h, pack2(w[0], w[1], kToken), pack2(w[2], w[3], kToken),
+                            st_global_v8(e16 + 16 * h, pack2(w[0], w[1], kToken), pack2(w[2], w[3], kToken),
                                          pack2(w[4], w[5], kToken), pack2(w[6], w[7], kToken), pack2(w[8], w[9], kToken),
                                          pack2(w[10], w[11], kToken), pack2(w[12], w[13], kToken),
                                          pack2(w[14], w[15], kToken));
@@ -766,14 +767,49 @@ struct HeadDhT : DhPairT {
     __device__ static void epi_end(const Params&, const Sched&, int, Epi&) {}
 };
 
+// dW's 16-bit tiles leave through shared memory, 32 rows of 64 columns (4 KB, in
+// the 128-byte swizzle) per epilogue warp, and a TMA store.  A thread owns a row,
+// so storing from registers means 32-byte pieces of 32 rows per instruction:
+// dW of one row of the 8B head took 352 us that way, 317 this way.
+constexpr int kOutBytes = 4096;
+
+// 32 columns of this lane's row, packed, as the left (half 0) or right half of the box
+__device__ __forceinline__ void out_stage(uint8_t* buf, int lane, int half, const uint32_t (&pk)[16]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(buf + lane * 128 + (((4 * half + j) ^ (lane & 7)) << 4)) =
+            make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+}
+
+// the box may be written again
+__device__ __forceinline__ void out_free(int lane) {
+    if (lane == 0) tma_store_wait_read();
+    __syncwarp();
+}
+
+__device__ __forceinline__ void out_send(const CUtensorMap* map, const uint8_t* buf, int lane, int x, int y) {
+    fence_async_proxy();
+    __syncwarp();
+    if (lane == 0) tma_store_2d(map, buf, x, y);
+}
+
 // ====================================================================== dW
 // DwPairT with the operators' output: chunks add up in fp32 (dw_acc), and with
 // dw16 the last chunk (often the only one) rounds the sum to the type of W.
 // With few rows a unit's MMAs are short (16 K-stages for 1024 rows, about 8200
 // clocks), so eight warps share the epilogue: four took longer than that.
 struct HeadDwT : DwPairT {
+    static constexpr int kStages = 6;
+    static constexpr int kOutOffset = kStages * kStageBytes + 1024;   // the output boxes, past the barriers
     static constexpr int kEpiWarps = 8;
     using Params = HeadChunkParams;
+    struct Sched : ChunkSched {
+        bool last;   // this chunk completes the 16-bit dW
+    };
+    __device__ static bool setup(const Params& p, Sched& sc) {
+        sc.last = p.dw16 && p.chunk + 1 == p.counts[C_NCHUNKS];
+        return DwPairT::setup(p, sc);
+    }
     template <bool kBf16>
     __device__ static void epi_item(const Params& p, const Sched& sc, int unit, int, int rank, uint32_t tacc, Epi&) {
         const int warp = threadIdx.x >> 5;
@@ -784,8 +820,10 @@ struct HeadDwT : DwPairT {
         const bool valid = v < p.V;
         if (!__any_sync(0xffffffffu, valid)) return;
         const bool first = p.chunk == 0;
-        const bool last = p.dw16 && p.chunk + 1 == p.counts[C_NCHUNKS];
         const int64_t at = static_cast<int64_t>(valid ? v : 0) * p.d;
+        extern __shared__ uint8_t smem_raw[];
+        const int lane = threadIdx.x & 31;
+        uint8_t* out = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u) + kOutOffset + (warp - 2) * kOutBytes;
         Finite<kBf16> fin;
 #pragma unroll 1
         for (int c = half * (kBN / 64); c < (half + 1) * (kBN / 64); ++c) {
@@ -793,11 +831,10 @@ struct HeadDwT : DwPairT {
             if (col0 >= p.d) break;
             float x[32];
             tmem_ld32(tacc + c * 32, x);
-            if (!valid) continue;
             float* acc = p.dw_acc + at + col0;
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] *= sc.winv;
-            if (!first) {
+            if (!first && valid) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float prev[8];
@@ -806,19 +843,18 @@ struct HeadDwT : DwPairT {
                     for (int i = 0; i < 8; ++i) x[8 * j + i] += prev[i];
                 }
             }
-            if (last) {
+            if (sc.last) {
                 uint32_t pk[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     pk[j] = pack2(x[2 * j], x[2 * j + 1], kBf16);
                     fin.see(pk[j]);
                 }
-                uint16_t* out = p.dw16 + at + col0;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    st_global_v8(out + 16 * h, pk[8 * h], pk[8 * h + 1], pk[8 * h + 2], pk[8 * h + 3], pk[8 * h + 4],
-                                 pk[8 * h + 5], pk[8 * h + 6], pk[8 * h + 7]);
-            } else {
+                // whole boxes of 64 columns (d is a multiple of 64); rows past V are not written
+                if ((c & 1) == 0) out_free(lane);
+                out_stage(out, lane, c & 1, pk);
+                if ((c & 1) == 1) out_send(&p.mDw16, out, lane, col0 - 32, v - lane);
+            } else if (valid) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) fin.see_f32(x[j]);
 #pragma unroll
@@ -829,10 +865,11 @@ struct HeadDwT : DwPairT {
                                  __float_as_uint(x[8 * j + 6]), __float_as_uint(x[8 * j + 7]));
             }
         }
-        if (fin.bad()) atomicOr(p.found_inf, 1);
+        if (valid && fin.bad()) atomicOr(p.found_inf, 1);
     }
 };
 constexpr int kDwThreads = 64 + 32 * HeadDwT::kEpiWarps;
+constexpr int kDwSmem = 1024 + HeadDwT::kOutOffset + HeadDwT::kEpiWarps * kOutBytes;
 
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -846,6 +883,7 @@ __global__ void __launch_bounds__(kDwThreads, 1)
     head_dw_kernel(const __grid_constant__ HeadChunkParams p, const __grid_constant__ CUtensorMap mA,
                    const __grid_constant__ CUtensorMap mA2, const __grid_constant__ CUtensorMap mB) {
     tc_pair_body<HeadDwT, kBf16>(p, mA, mA2, mB);
+    tma_store_wait_all();   // of the threads that sent output boxes
 }
 
 }  // namespace
@@ -874,8 +912,8 @@ cudaError_t launch_head_dh(const HeadChunkParams& p, const CUtensorMap& mDS, con
 
 cudaError_t launch_head_dw(const HeadChunkParams& p, const CUtensorMap& mDSmn, const CUtensorMap& mHct, int n_sm, bool bf16,
                            cudaStream_t st) {
-    return bf16 ? launch_pairs<head_dw_kernel<true>>(kDwThreads, smem_bytes<HeadDwT>(), n_sm, st, p, mDSmn, mDSmn, mHct)
-                : launch_pairs<head_dw_kernel<false>>(kDwThreads, smem_bytes<HeadDwT>(), n_sm, st, p, mDSmn, mDSmn, mHct);
+    return bf16 ? launch_pairs<head_dw_kernel<true>>(kDwThreads, kDwSmem, n_sm, st, p, mDSmn, mDSmn, mHct)
+                : launch_pairs<head_dw_kernel<false>>(kDwThreads, kDwSmem, n_sm, st, p, mDSmn, mDSmn, mHct);
 }
 
 template <bool kBf16, int kNC>
