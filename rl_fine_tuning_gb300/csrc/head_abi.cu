@@ -177,11 +177,10 @@ int head_validate(const HeadCall& c, HeadLayout* L) {
     } while (0)
 
 // logit = zscale * accumulator, with the correction of the tensor cores' rounding
-// (see head_tc.cu): a piece of n_i additions holds n_i / n of the sum and loses
-// kAddLoss n_i of that.
+// (see head_tc.cu) for pieces of d / 16 / (pieces) additions
 void logit_scale(const HeadCall& c, float* zscale, float* zscale2) {
-    const int d = c.shape->d, full = d / kPieceK * kPieceK, rest = d - full;
-    const double n_eff = (static_cast<double>(full) * kPieceK + static_cast<double>(rest) * rest) / d / 16.0;
+    const int d = c.shape->d, pieces = (d + kPieceK - 1) / kPieceK;
+    const double n_eff = d / 16.0 / pieces;
     const double z = (1.0 + kAddLoss * n_eff) / static_cast<double>(c.temperature);
     *zscale = static_cast<float>(z);
     *zscale2 = static_cast<float>(z * 1.4426950408889634074);

@@ -32,7 +32,13 @@ namespace grpo {
 
 namespace {
 
-constexpr int kStagesPerPiece = kPieceK / kBK;
+// K-stages per piece: the fewest pieces of at most kPieceK, all of one length but
+// for the last (a short piece leaves the epilogue too little time for the one
+// before it: d = 1536 as 768 + 768 takes 8% less than as 1024 + 512)
+__device__ __forceinline__ int piece_stages(int ks) {
+    const int n = (ks * kBK + kPieceK - 1) / kPieceK;
+    return (ks + n - 1) / n;
+}
 
 // ====================================================================== logits of a chunk
 
@@ -43,7 +49,7 @@ constexpr int kLgSmem = kLgStages * kLgStageBytes + 1024 + 512;
 // units: (row-tile pair, vocabulary split), row-tile pairs fastest within
 // groups of kFwdGroup so that a W tile is shared in L2
 struct LgSched {
-    int n_units, ks, n_pc, n_mp, c0, n_c, S, nps;
+    int n_units, ks, per, n_pc, n_mp, c0, n_c, S, nps;
 };
 
 __device__ __forceinline__ bool lg_setup(const LogitsParams& p, LgSched& sc) {
@@ -55,7 +61,8 @@ __device__ __forceinline__ bool lg_setup(const LogitsParams& p, LgSched& sc) {
     sc.nps = p.plan[p.chunk].y;
     sc.n_units = sc.n_mp * sc.S;
     sc.ks = p.d / kBK;
-    sc.n_pc = (sc.ks + kStagesPerPiece - 1) / kStagesPerPiece;
+    sc.per = piece_stages(sc.ks);
+    sc.n_pc = (sc.ks + sc.per - 1) / sc.per;
     return sc.n_units > 0;
 }
 
@@ -285,12 +292,12 @@ __device__ __forceinline__ void lg_body(const LogitsParams& p, const CUtensorMap
                     decode_grouped(unit, sc.n_mp, sc.S, kFwdGroup, &mp, &split);
                     const int n_items = lg_items(p, sc, split);
                     for (int item = 0; item < n_items; ++item)
-                        for (int k0 = 0; k0 < sc.ks; k0 += kStagesPerPiece, ++it) {
+                        for (int k0 = 0; k0 < sc.ks; k0 += sc.per, ++it) {
                             const int b = it & 1;
                             if (!mbar_wait(&sm.acc_empty[b], ((it >> 1) & 1u) ^ 1u, sm.abort_flag, status)) goto mma_done;
                             tc_fence_after();
                             const uint32_t acc = tmem + b * 256;
-                            const int k1 = min(k0 + kStagesPerPiece, sc.ks);
+                            const int k1 = min(k0 + sc.per, sc.ks);
                             for (int k = k0; k < k1; ++k) {
                                 if (!mbar_wait(&sm.full[s], ph, sm.abort_flag, status)) goto mma_done;
                                 ++n_used;
@@ -445,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     int* status = p.status;
-    const int ks = p.d / kBK;
+    const int ks = p.d / kBK, per = piece_stages(ks);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < F::kStages; ++s) {
@@ -501,11 +508,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             int s = 0, n_used = 0, it = 0;
             uint32_t ph = 0;
             for (int tile = blockIdx.x; tile < p.n_tiles; tile += gridDim.x)
-                for (int k0 = 0; k0 < ks; k0 += kStagesPerPiece, ++it) {
+                for (int k0 = 0; k0 < ks; k0 += per, ++it) {
                     const int b = it & 1;
                     if (!mbar_wait(&sm.acc_empty[b], ((it >> 1) & 1u) ^ 1u, sm.abort_flag, status)) goto mma_done;
                     tc_fence_after();
-                    const int k1 = min(k0 + kStagesPerPiece, ks);
+                    const int k1 = min(k0 + per, ks);
                     for (int k = k0; k < k1; ++k) {
                         if (!mbar_wait(&sm.full[s], ph, sm.abort_flag, status)) goto mma_done;
                         ++n_used;
@@ -549,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int it = 0;
         for (int tile = blockIdx.x; tile < p.n_tiles; tile += gridDim.x) {
             float a[kNC];
-            for (int k0 = 0; k0 < ks; k0 += kStagesPerPiece, ++it) {
+            for (int k0 = 0; k0 < ks; k0 += per, ++it) {
                 const int b = it & 1;
                 if (!mbar_wait(&sm.acc_full[b], (it >> 1) & 1u, sm.abort_flag, status)) goto epi_done;
                 tc_fence_after();
