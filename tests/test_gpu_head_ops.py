@@ -496,3 +496,89 @@ def test_relative_dlogits_of_given_gradients_and_bad_tokens():
     c.tok[3], c.tok[4] = 70001, -5
     dH, dW = c.logp_bwd(dq.cuda())
     assert int(c.status) == 2 and int(c.inf) == 0 and not dH[3:5].any() and bool(torch.isfinite(dW.float()).all())
+
+
+def test_example_runs_the_operators_together():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "off_policy_steps.py")
+    spec = importlib.util.spec_from_file_location("off_policy_steps", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    out = m.main(["--d", "128", "--V", "1000", "--L", "40", "--steps", "3"])
+    assert out["clip"]["losses"][-1] < out["clip"]["losses"][0]
+    assert out["pair"]["losses"][-1] < out["pair"]["losses"][0]
+    assert all(np.isfinite(x) and x < 0 for x in out["token"])
+
+
+def test_nan_in_rows_that_do_not_count_stays_there():
+    """Masked rows of h, the stored log-probs of masked rows and the advantage of an empty completion are never used."""
+    for rows in (4, 60):
+        c = Case(1, 3, rows // 2, 128, 300, "bf16", "all", seed=30)
+        c.P.mask[: rows // 2] = False                 # completion 0 is empty
+        c.P.mask[-1] = False
+        c.mask = torch.from_numpy(c.P.mask.astype(np.uint8)).cuda()
+        c.h[~torch.from_numpy(c.P.mask)] = float("nan")
+        old, ref = c.old_ref()
+        q, e = c.logp()
+        check_logp(c, q, e)
+        adv = torch.tensor([float("nan"), 1.0, -1.0], device="cuda")
+        loss, st, dH, dW = c.clip(adv, torch.from_numpy(old).cuda(), torch.from_numpy(ref).cuda(), rg.clip_opts())
+        assert int(c.inf) == 0 and bool(torch.isfinite(loss)) and bool(torch.isfinite(dW.float()).all())
+        assert not host(dH)[~c.P.mask].any()
+
+
+def test_nan_in_a_row_that_counts_is_reported():
+    c = Case(1, 1, 60, 128, 300, "bf16", "all", seed=31)
+    c.h[5] = float("nan")
+    q, _ = c.logp()
+    assert np.isnan(host(q)[5]) and np.isfinite(np.delete(host(q), 5)).all()
+    dq = torch.ones(60, device="cuda")
+    dH, _ = c.logp_bwd(dq)
+    assert int(c.inf) == 1 and int(c.status) == 0
+    assert bool(torch.isfinite(dH[torch.arange(60) != 5].float()).all())
+
+
+def test_offsets_past_32_bits():
+    """A chunk of 19456 rows x 131072 columns: 2.55e9 dlogits.  Sampled rows and columns against fp64 on the GPU."""
+    L, d, V = 9728, 64, 131072
+    g = torch.Generator(device="cuda").manual_seed(3)
+    N = 2 * L
+    W = (torch.randn(V, d, device="cuda", generator=g) * d ** -0.5).bfloat16()
+    tok = torch.randint(0, V, (N,), device="cuda", generator=g, dtype=torch.int32)
+    h = (torch.randn(N, d, device="cuda", generator=g) + 8 * W[tok.long()].float()).bfloat16()
+    mask = torch.ones(N, dtype=torch.uint8, device="cuda")
+    ref = torch.full((N,), -1.0, device="cuda")
+    shape = rg.make_shape(1, 2, L, d, V, beta=0.01)
+    ws = torch.full((rg.grpo_policy_workspace_bytes(shape, "pair"),), 255, dtype=torch.uint8, device="cuda")
+    dH, dW = torch.full_like(h, 7.0), torch.full_like(W, 7.0)
+    loss, q, st = torch.empty(1, device="cuda"), torch.empty(N, device="cuda"), torch.empty(1, 4, device="cuda")
+    status, inf = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
+    rg.grpo_pair_loss_fwd_bwd(h, W, tok, mask, ref, shape, rg.pair_opts(length_mean=True), 1024.0, ws, loss, dH, dW, inf, q, st,
+                              status)
+    torch.cuda.synchronize()
+    assert int(status) == 0 and int(inf) == 0
+    H, W64 = h.double(), W.double()
+    q64, p_cols, parts = torch.empty(N, dtype=torch.float64, device="cuda"), [], []
+    cols = torch.cat([torch.arange(32, device="cuda"), torch.arange(V - 32, V, device="cuda"), tok[-64:].long()])
+    rows = torch.cat([torch.arange(64, device="cuda"), torch.arange(N - 64, N, device="cuda")])
+    for r in torch.arange(N, device="cuda").split(512):
+        z = H[r] @ W64.t()
+        lp = z - torch.logsumexp(z, 1, keepdim=True)
+        q64[r] = lp.gather(1, tok[r].long()[:, None])[:, 0]
+        p_cols.append(lp[:, cols].exp())
+        parts.append(lp[(r[:, None] == rows[None]).any(1)].exp())
+    assert float((q.double() - q64).abs().max()) < 1e-5
+    S = (q64 - ref.double()).reshape(2, L).mean(1)
+    m = 0.01 * (S[0] - S[1])
+    c = 0.01 * -torch.sigmoid(-m) / L * 1024.0
+    gq = torch.cat([c.expand(L), -c.expand(L)])
+    one = (tok.long()[:, None] == cols[None]).double()
+    rW = ((one - torch.cat(p_cols)) * gq[:, None]).t() @ H
+    P = torch.cat(parts)
+    P = -P
+    P[torch.arange(128, device="cuda"), tok[rows].long()] += 1
+    rH = (P * gq[rows][:, None]) @ W64
+    for got, want in ((dW[cols].double(), rW), (dH[rows].double(), rH)):
+        assert float((got - want).norm() / want.norm()) < 3 * 2 ** -8
+        assert float((got - want).abs().max() / want.abs().max()) < 4 * 2 ** -8
