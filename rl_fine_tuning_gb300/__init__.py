@@ -156,10 +156,17 @@ def _nbytes(x) -> int:
     return x.numel() * x.element_size()
 
 
+_raw_stream = None   # torch's current stream as a number, without a Stream object (3 us less a call)
+
+
 def _stream(stream):
+    global _raw_stream
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        if _raw_stream is None:
+            import torch
+            get, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+            _raw_stream = (lambda: get(device())) if get else lambda: torch.cuda.current_stream().cuda_stream
+        return ctypes.c_void_p(_raw_stream())
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)

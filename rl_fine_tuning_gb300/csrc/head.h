@@ -46,7 +46,9 @@ struct PlanParams {
     int by_pair;            // chunks of whole pairs of completions
     int pairs_of_g2;        // completions 2i and 2i + 1 are a pair: count pairs, not completions, with a valid row
     int max_chunks;
-    int n_nt, ks, n_pairs, slots_max;   // dH: 256-wide d tiles, K-stages, SM pairs, partial tiles (0: no backward)
+    int n_nt, ks, n_pairs, slots_max;   // dH: 256-wide d tiles, K-stages, SM pairs, partial tiles
+    int backward;
+    int n_w;                // dW units in dH's launch (0: dW has its own)
     int* counts;
     int* off;               // [n_seq + 1] valid rows before completion i
     int* cb;                // [max_chunks + 1] first valid row of chunk c
@@ -58,6 +60,7 @@ struct PlanParams {
     int* far;               // [max_chunks], zeroed
     int* rows;              // [N] valid rows, ascending
     int* found_inf;         // nullable, zeroed
+    float* loss;            // nullable, zeroed: what it is when no row counts
     int* status;            // zeroed
 };
 
@@ -179,7 +182,8 @@ struct LossParams {
 
 // ChunkParams of the head operators' GEMMs
 struct HeadChunkParams : ChunkParams {
-    CUtensorMap mDw16;      // dw16 in boxes of 32 rows x 64
+    CUtensorMap mHct;       // hct, dW's B operand
+    LossParams loss;        // written with the last chunk that has rows
     float* dw_acc;          // fp32 dW (the caller's, or the workspace's when dw16 is given and there are several chunks)
     uint16_t* dw16;         // 16-bit dW, nullable
     float* dh_part;         // [slots][2][128 x 256] fp32
@@ -207,12 +211,15 @@ cudaError_t launch_head_logits(const LogitsParams& p, const CUtensorMap& mH, con
 cudaError_t launch_head_merge(const HeadMergeParams& p, cudaStream_t st);
 cudaError_t launch_pair_coef(const PairParams& p, cudaStream_t st);
 cudaError_t launch_head_dlogits(const HeadChunkParams& p, float* oscale, bool bf16, int sm_count, cudaStream_t st);
+cudaError_t launch_merge_dlogits(const HeadMergeParams& m, const HeadChunkParams& p, float* oscale, int sm_count,
+                                 cudaStream_t st);
 cudaError_t launch_head_scale(const HeadChunkParams& p, float* oscale, int sm_count, cudaStream_t st);
+cudaError_t launch_head_grads(const HeadChunkParams& p, const CUtensorMap& mDS, const CUtensorMap& mDSmn,
+                              const CUtensorMap& mWmn, int n_sm, bool bf16, cudaStream_t st);
 cudaError_t launch_head_dh(const HeadChunkParams& p, const CUtensorMap& mDS, const CUtensorMap& mWmn, int n_sm, bool bf16,
                            cudaStream_t st);
-cudaError_t launch_head_dh_join(const HeadChunkParams& p, const LossParams& l, bool bf16, int sm_count, cudaStream_t st);
-cudaError_t launch_head_dw(const HeadChunkParams& p, const CUtensorMap& mDSmn, const CUtensorMap& mHct, int n_sm, bool bf16,
-                           cudaStream_t st);
+cudaError_t launch_head_dw(const HeadChunkParams& p, const CUtensorMap& mDSmn, int n_sm, bool bf16, cudaStream_t st);
+cudaError_t launch_head_dh_join(const HeadChunkParams& p, bool bf16, int sm_count, cudaStream_t st);
 cudaError_t launch_loss(const LossParams& l, const int* counts, cudaStream_t st);
 cudaError_t launch_few_prep(const FewParams& p, const uint16_t* h, const uint16_t* W, bool bf16, double* zt, cudaStream_t st);
 cudaError_t launch_few(const FewParams& p, const CUtensorMap& mH, const CUtensorMap& mW, int grid, bool bf16, int nc,

@@ -13,14 +13,22 @@ namespace {
 constexpr int64_t kPairChunkRowsMax = 19456;   // default chunks grow to hold one whole pair up to this (152 tiles of 128)
 
 // bf16 chunks of at least this many logits use relative dlogits (k_head_scale)
-// instead of a pass over the dlogits; below, the pass is the shorter way
+// instead of a pass over the dlogits.  The pass against the relative way, for a
+// whole backward call at d = 1024: 60 against 62 us for 1M logits, 78 against 79 for
+// 4M, 165 against 152 for 8M (128 rows), 326 against 286 for 64M.
 constexpr int64_t kRelativeMin = 1 << 22;
+
+// Chunks of at most this much work per gradient (rows x V x d) compute dH and dW
+// in one launch; above, each has a kernel of its own, whose inner loops know
+// their operands.  One launch against two, for a whole backward call: 39 against
+// 44 us at 3e7, 112 against 118 at 1.6e10, 188 against 188 at 2e10, 435 against 420 at 5e10.
+constexpr double kOneLaunchMax = 2e10;
 
 struct HeadLayout {
     size_t counts, off, cb, pb, dh_plan, lg_plan, gmax, far, oscale, rowf, rows, zt, lse, gco, ell, q, pair_ell, hc, part, mx, ds, hct, dh_part,
         dw_acc, total;
     int64_t N;
-    int n_seq, R, max_chunks, S, n_ntiles, V_pad, nc32, slots, by_pair, relative;
+    int n_seq, R, max_chunks, S, n_ntiles, n_vt, V_pad, nc32, slots, by_pair, relative, one_launch;
 };
 
 bool head_shape_ok(const grpo_shape& s, int op) {
@@ -63,13 +71,17 @@ bool head_layout(const grpo_shape& s, int op, int dw_f32, HeadLayout* o) {
     }
     o->relative = has_backward(op) && s.dtype == GRPO_BF16 && static_cast<int64_t>(o->R) * s.V >= kRelativeMin;
     o->n_ntiles = (s.V + kBN - 1) / kBN;
+    o->n_vt = (s.V + kBM - 1) / kBM;
+    o->one_launch = has_backward(op) && static_cast<double>(o->R) * s.V * s.d <= kOneLaunchMax;
     // splits: at most kHeadSplitsMax, and at least what 64 tiles a split give
     const int least = (o->n_ntiles + 63) / 64;
     o->S = o->n_ntiles < kHeadSplitsMax ? o->n_ntiles : least > kHeadSplitsMax ? least : kHeadSplitsMax;
     o->V_pad = (s.V + 63) / 64 * 64;
     o->nc32 = ((s.V + 31) / 32 + 7) / 8 * 8;
     const int64_t units = static_cast<int64_t>((o->R + 2 * kBM - 1) / (2 * kBM)) * ((s.d + kBN - 1) / kBN);
-    const int64_t pieces = units * ((s.V + kBK - 1) / kBK);
+    // up to 32 K-stages (V = 2048) a unit is not worth splitting: no partial tiles, and no launch to join them
+    const int ks = (s.V + kBK - 1) / kBK;
+    const int64_t pieces = ks > 32 ? units * ks : 0;
     o->slots = static_cast<int>(pieces < kDhSlotsMax ? pieces : kDhSlotsMax);
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -226,7 +238,7 @@ struct HeadRun {
     cudaStream_t st;
     char* w;
     bool bf16;
-    CUtensorMap mW_k, mH_k, mW_mn, mHct, mDS_k, mDS_mn, mDw16;
+    CUtensorMap mW_k, mH_k, mW_mn, mHct, mDS_k, mDS_mn;
 
     template <class T>
     T* at(size_t off) const { return reinterpret_cast<T*>(w + off); }
@@ -239,8 +251,7 @@ struct HeadRun {
         if (c.backward && (!make_map(&mW_mn, c.W, bf16, s.d, s.V, s.d, 64, kBK) ||
                            !make_map(&mHct, at<void>(L.hct), bf16, L.R, s.d, L.R, kBK, 128) ||
                            !make_map(&mDS_k, at<void>(L.ds), bf16, s.V, L.R, L.V_pad, kBK, kBM) ||
-                           !make_map(&mDS_mn, at<void>(L.ds), bf16, s.V, L.R, L.V_pad, 64, kBK) ||
-                           (!c.dw_f32 && !make_map(&mDw16, c.dW, bf16, s.d, s.V, s.d, 64, 32))))
+                           !make_map(&mDS_mn, at<void>(L.ds), bf16, s.V, L.R, L.V_pad, 64, kBK)))
             return GRPO_ERR_LAUNCH;
         return GRPO_OK;
     }
@@ -258,7 +269,10 @@ struct HeadRun {
         p.n_nt = (s.d + kBN - 1) / kBN;
         p.ks = (s.V + kBK - 1) / kBK;
         p.n_pairs = dev.sm_count / 2;
-        p.slots_max = c.backward ? L.slots : 0;
+        p.slots_max = L.slots;
+        p.backward = c.backward;
+        p.n_w = L.one_launch ? (L.n_vt + 1) / 2 * p.n_nt : 0;
+        p.loss = c.loss;
         p.counts = at<int>(L.counts);
         p.off = at<int>(L.off);
         p.cb = at<int>(L.cb);
@@ -337,13 +351,9 @@ struct HeadRun {
         return GRPO_OK;
     }
 
-    // far: the chunk's word of the far list (set when a row's q is below kLeastQ)
-    int merge(int chunk, bool relative, const int* only_if, bool set_far) {
+    HeadMergeParams merge_params(int chunk) const {
         const grpo_shape& s = *c.shape;
         HeadMergeParams p = {};
-        p.relative = relative;
-        p.only_if = only_if;
-        p.far = set_far ? at<int>(L.far) : nullptr;
         p.part = at<float4>(L.part);
         p.plan = at<int2>(L.lg_plan);
         p.counts = at<int>(L.counts);
@@ -375,6 +385,15 @@ struct HeadRun {
         p.R = L.R;
         p.N = L.N;
         p.status = c.status;
+        return p;
+    }
+
+    // set_far: note the chunk when a row's q is below kLeastQ
+    int merge(int chunk, bool relative, const int* only_if, bool set_far) {
+        HeadMergeParams p = merge_params(chunk);
+        p.relative = relative;
+        p.only_if = only_if;
+        p.far = set_far ? at<int>(L.far) : nullptr;
         HEAD_LAUNCH(GRPO_PROF_MERGE, launch_head_merge(p, st));
         return GRPO_OK;
     }
@@ -417,7 +436,8 @@ struct HeadRun {
         return l;
     }
 
-    int gradients(int chunk, int gmax_chunk) {
+    // fused: the merge is part of it
+    int gradients(int chunk, int gmax_chunk, bool fused = false) {
         const grpo_shape& s = *c.shape;
         HeadChunkParams p = {};
         p.counts = at<int>(L.counts);
@@ -440,7 +460,8 @@ struct HeadRun {
         p.dH = static_cast<uint16_t*>(c.dH);
         p.found_inf = c.found_inf;
         p.status = c.status;
-        p.mDw16 = mDw16;
+        p.mHct = mHct;
+        p.loss = loss();
         p.dw_acc = c.dw_f32 ? static_cast<float*>(c.dW) : at<float>(L.dw_acc);
         p.dw16 = c.dw_f32 ? nullptr : static_cast<uint16_t*>(c.dW);
         p.dh_part = at<float>(L.dh_part);
@@ -453,12 +474,13 @@ struct HeadRun {
         p.hc = at<uint16_t>(L.hc);
         p.rowf = L.relative ? at<float>(L.rowf) : nullptr;
         p.far = L.relative ? at<int>(L.far) : nullptr;
-        HEAD_LAUNCH(GRPO_PROF_DLOGITS, launch_head_dlogits(p, at<float>(L.oscale), bf16, dev.sm_count, st));
+        if (fused) HEAD_LAUNCH(GRPO_PROF_DLOGITS, launch_merge_dlogits(merge_params(chunk), p, at<float>(L.oscale), dev.sm_count, st));
+        else HEAD_LAUNCH(GRPO_PROF_DLOGITS, launch_head_dlogits(p, at<float>(L.oscale), bf16, dev.sm_count, st));
         if (L.relative) HEAD_LAUNCH(GRPO_PROF_DLOGITS, launch_head_scale(p, at<float>(L.oscale), dev.sm_count, st));
-        HEAD_LAUNCH(GRPO_PROF_DH, launch_head_dh(p, mDS_k, mW_mn, dev.sm_count, bf16, st));
-        const LossParams l = chunk + 1 == L.max_chunks ? loss() : LossParams{};   // all rows are merged by then
-        HEAD_LAUNCH(GRPO_PROF_DH, launch_head_dh_join(p, l, bf16, dev.sm_count, st));
-        HEAD_LAUNCH(GRPO_PROF_DW, launch_head_dw(p, mDS_mn, mHct, dev.sm_count, bf16, st));
+        if (L.one_launch) HEAD_LAUNCH(GRPO_PROF_DH, launch_head_grads(p, mDS_k, mDS_mn, mW_mn, dev.sm_count, bf16, st));
+        else HEAD_LAUNCH(GRPO_PROF_DH, launch_head_dh(p, mDS_k, mW_mn, dev.sm_count, bf16, st));
+        if (L.slots > 0) HEAD_LAUNCH(GRPO_PROF_DH, launch_head_dh_join(p, bf16, dev.sm_count, st));
+        if (!L.one_launch) HEAD_LAUNCH(GRPO_PROF_DW, launch_head_dw(p, mDS_mn, dev.sm_count, bf16, st));
         return GRPO_OK;
     }
 
@@ -482,6 +504,10 @@ struct HeadRun {
             const int* far = at<int>(L.far) + i;
             HEAD_STEP(gather(i, grad && !rel, i == 0));
             HEAD_STEP(logits(i, grad ? keep : stats, grad));
+            if (grad && bf16 && !rel && c.mode != HEAD_PAIR) {
+                HEAD_STEP(gradients(i, i, true));
+                continue;
+            }
             HEAD_STEP(merge(i, rel, nullptr, rel));
             if (rel) {   // only for a chunk with a far row
                 HEAD_STEP(logits(i, grad ? LG_KEEP_MAX : LG_STATS, grad, far));
@@ -512,7 +538,7 @@ int head_call(const HeadCall& c, grpo_stream_t stream) {
     if (rc != GRPO_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (c.mode == HEAD_LOGP && L.N <= kFewRows) return run_few(c, L, dev, st);
-    HeadRun run{c, L, dev, st, static_cast<char*>(c.ws), c.shape->dtype == GRPO_BF16, {}, {}, {}, {}, {}, {}, {}};
+    HeadRun run{c, L, dev, st, static_cast<char*>(c.ws), c.shape->dtype == GRPO_BF16, {}, {}, {}, {}, {}, {}};
     return run.run();
 }
 

@@ -72,4 +72,24 @@ __device__ __forceinline__ RowSum join_row_relative(const float4* part, int S2, 
     return r;
 }
 
+// The loss from the rows' (or pairs') weighted objectives, by one warp: fp64 sums in
+// a fixed order.
+__device__ __forceinline__ void write_loss(const LossParams& l, const int* counts, int lane) {
+    if (!l.loss) return;
+    double acc = 0.0;
+    if (l.pair_ell) {
+        for (int i = lane; i < l.n_pairs; i += 32) acc += __ldcg(l.pair_ell + i);
+    } else {
+        const int nv = counts[C_NVALID];
+#pragma unroll 8
+        for (int i = lane; i < nv; i += 32) acc += static_cast<double>(__ldcg(l.ell + i));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (lane == 0) {
+        const int n = l.pair_ell ? counts[C_NACT] : 1;   // rows carry their weight in the mean already
+        *l.loss = n > 0 ? static_cast<float>(acc / n) : 0.f;
+    }
+}
+
 }  // namespace grpo

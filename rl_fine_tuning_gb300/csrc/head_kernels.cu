@@ -13,7 +13,6 @@ namespace grpo {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
 constexpr int kPlanItems = 16;
 
 // exclusive sum over the block; *total gets the block's sum
@@ -119,7 +118,7 @@ __device__ __forceinline__ double token_logit(const uint4* a, const uint4* b, in
 }  // namespace
 
 // ------------------------------------------------------------ plan
-// One block walks the mask in segments of 16,384 rows and writes the valid
+// One block walks the mask in segments of 16 rows a thread and writes the valid
 // rows in order, the number of valid rows before each completion, the chunk
 // bounds and, for each chunk, how the logits' and dH's units are split.
 //
@@ -133,11 +132,12 @@ __device__ __forceinline__ double token_logit(const uint4* a, const uint4* b, in
 // logits twice.
 //
 // dH split: dH's units (256 x 256 tiles, each a sum over the whole vocabulary)
-// run in waves of one per SM pair.  The units of the full waves run whole; the
-// rest is cut into K pieces so that the last wave is shared by all SM pairs,
-// and k_dh_join adds the pieces.  The cost model counts K-stages per SM pair:
-// 12 for a unit's fill and epilogue, 0.3 for each partial tile's trip through
-// memory.
+// run in rounds of one per SM pair.  The units of the last round are cut into
+// K pieces, which k_dh_join adds, so that all SM pairs share it; with dW's units
+// in the same launch (head_grads_kernel) those share it first.  The cost model counts
+// K-stages per SM pair: 12 and 4 for a dH and a dW unit's own cost, 0.3 for each
+// partial tile's trip through memory.
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) k_plan(const PlanParams p) {
     __shared__ int s_warp[32];
     __shared__ int s_act;
@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(const PlanParams p) {
     if (tid == 0) {
         *p.status = 0;
         if (p.found_inf) *p.found_inf = 0;
+        if (p.loss) *p.loss = 0.f;
         s_act = 0;
     }
     const bool vec = p.mask && (reinterpret_cast<uintptr_t>(p.mask) & 15u) == 0;
@@ -245,9 +246,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(const PlanParams p) {
         }
         best = warp_best(best_cost, best);
         if (lane == 0) p.lg_plan[c] = make_int2((p.n_ntiles + best - 1) / best, best);
-        if (p.slots_max <= 0) continue;
+        if (!p.backward) continue;
         const int units = row_pairs * p.n_nt;
         const int full = units / p.n_pairs * p.n_pairs, rem = units - full;
+        const int ks_w = (p.cb[c + 1] - p.cb[c] + kBK - 1) / kBK;
         best_cost = 3e38f;
         best = 1;
 #pragma unroll
@@ -256,8 +258,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(const PlanParams p) {
             if (rem == 0 || s > p.ks || (s > 1 && rem * s > p.slots_max)) continue;
             const int kper = (p.ks + s - 1) / s;
             if ((s - 1) * kper >= p.ks) continue;   // the last piece would be empty
-            const float waves = static_cast<float>((rem * s + p.n_pairs - 1) / p.n_pairs);
-            const float cost = waves * (kper + 12) + (s > 1 ? 0.3f * rem * s : 0.f);
+            const float whole = static_cast<float>(full / p.n_pairs) * (p.ks + 12);
+            const float last = static_cast<float>((rem * s + p.n_pairs - 1) / p.n_pairs) * (kper + 12);
+            const float all = whole + (static_cast<float>(rem * s) * (kper + 12) + static_cast<float>(p.n_w) * (ks_w + 4)) / p.n_pairs;
+            const float cost = fmaxf(whole + last, all) + (s > 1 ? 0.3f * rem * s : 0.f);
             if (cost < best_cost) {
                 best_cost = cost;
                 best = s;
@@ -269,7 +273,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(const PlanParams p) {
 }
 
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t st) {
-    k_plan<<<1, kPlanThreads, 0, st>>>(p);
+    // few rows: fewer warps to synchronise
+    if (p.N <= 256 * kPlanItems) k_plan<256><<<1, 256, 0, st>>>(p);
+    else k_plan<1024><<<1, 1024, 0, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -412,10 +418,69 @@ cudaError_t launch_few_prep(const FewParams& p, const uint16_t* h, const uint16_
 // row's weight in the mean and 1 / temperature included; ell carries the weight too.
 constexpr int kHeadMergeThreads = 256;
 
+// One row's merge by one warp; lane 0 writes and returns what its dlogits need.
+struct RowGrad {
+    float g, lse, q;
+    int tok;   // -1: nothing (a bad token id, reported here)
+};
+
+__device__ __forceinline__ RowGrad merge_row(const HeadMergeParams& p, int slot, int c0, int lane) {
+    RowGrad out{0.f, 0.f, 0.f, -1};
+    const int S2 = 2 * p.plan[p.chunk].x;
+    const int t = p.rows[c0 + slot];
+    if (!GRPO_DCHECK(t >= 0 && t < p.N, p.status)) return out;
+    const int tok = p.tokens[t];
+    const bool ok = tok >= 0 && tok < p.V;
+    RowSum r{0.0, 0.0, 0.f};
+    if (ok) r = p.relative ? join_row_relative(p.part + static_cast<int64_t>(slot) * S2, S2, lane, p.zt[t])
+                           : join_row(p.part + static_cast<int64_t>(slot) * S2, S2, lane, p.zt[t]);
+    if (lane != 0) return out;
+    if (!ok) atomicCAS(p.status, 0, GRPO_ERR_SHAPE);
+    const float q = static_cast<float>(r.q);
+    if (p.far && !(q >= kLeastQ)) atomicOr(p.far + p.chunk, 1);
+    float g = 0.f, ell = 0.f, ratio = 0.f, pen = 0.f;
+    if (ok && p.mode == HEAD_GRAD) g = p.dlogp[t];
+    if (ok && p.mode == HEAD_CLIP) {
+        const int i = t / p.L;
+        const float A = p.adv[i];
+        ratio = expf(static_cast<float>(r.q - p.logp_old[t]));
+        const bool cut = A >= 0.f ? ratio > p.clip_hi : ratio < p.clip_lo;
+        ell = -A * (cut ? (A >= 0.f ? p.clip_hi : p.clip_lo) : ratio);
+        g = cut ? 0.f : -A * ratio;
+        if (p.logp_ref) {
+            const float x = static_cast<float>(p.logp_ref[t] - r.q);
+            const float em1 = expm1f(x);
+            pen = em1 - x;
+            ell = fmaf(p.beta, pen, ell);
+            g = fmaf(-p.beta, em1, g);
+        }
+        const float w = p.loss_mode == GRPO_SEQUENCE_MEAN
+                            ? 1.f / (static_cast<float>(p.off[i + 1] - p.off[i]) * p.counts[C_NACT])
+                            : 1.f / p.counts[C_NVALID];
+        ell *= w;
+        g *= w;
+    }
+    g *= p.inv_t;
+    p.lse[t] = static_cast<float>(r.lse);
+    if (p.logp) p.logp[t] = q;
+    if (p.entropy) p.entropy[t] = r.ent;
+    if (p.stats) {
+        p.stats[3 * static_cast<int64_t>(t)] = q;
+        p.stats[3 * static_cast<int64_t>(t) + 1] = ratio;
+        p.stats[3 * static_cast<int64_t>(t) + 2] = pen;
+    }
+    if (p.mode == HEAD_GRAD || p.mode == HEAD_CLIP) p.gco[t] = g;
+    if (p.ell) p.ell[c0 + slot] = ell;
+    out.g = g;
+    out.lse = static_cast<float>(r.lse);
+    out.q = q;
+    out.tok = ok ? tok : -1;
+    return out;
+}
+
 __global__ void __launch_bounds__(kHeadMergeThreads) k_head_merge(const HeadMergeParams p) {
     __shared__ unsigned s_max;
-    if (p.chunk >= p.counts[C_NCHUNKS] || (p.only_if && *p.only_if == 0)) return;
-    const int S2 = 2 * p.plan[p.chunk].x;
+    if (p.only_if && *p.only_if == 0) return;
     const int2 cbn = chunk_bounds(p.counts, p.cb, p.chunk);
     const int c0 = cbn.x, n_c = cbn.y;
     const int lane = threadIdx.x & 31;
@@ -424,61 +489,8 @@ __global__ void __launch_bounds__(kHeadMergeThreads) k_head_merge(const HeadMerg
     if (threadIdx.x == 0) s_max = 0u;
     __syncthreads();
     if (slot < n_c && GRPO_DCHECK(slot < p.R, p.status)) {
-        const int t = p.rows[c0 + slot];
-        if (GRPO_DCHECK(t >= 0 && t < p.N, p.status)) {
-            const int tok = p.tokens[t];
-            const bool ok = tok >= 0 && tok < p.V;
-            RowSum r{0.0, 0.0, 0.f};
-            if (ok) r = p.relative ? join_row_relative(p.part + static_cast<int64_t>(slot) * S2, S2, lane, p.zt[t])
-                                   : join_row(p.part + static_cast<int64_t>(slot) * S2, S2, lane, p.zt[t]);
-            if (lane == 0) {
-                if (!ok) atomicCAS(p.status, 0, GRPO_ERR_SHAPE);
-                const float q = static_cast<float>(r.q);
-                if (p.far && !(q >= kLeastQ)) atomicOr(p.far + p.chunk, 1);
-                float g = 0.f, ell = 0.f, ratio = 0.f, pen = 0.f;
-                if (ok && p.mode == HEAD_GRAD) g = p.dlogp[t];
-                if (ok && p.mode == HEAD_CLIP) {
-                    const int i = t / p.L;
-                    const float A = p.adv[i];
-                    ratio = expf(static_cast<float>(r.q - p.logp_old[t]));
-                    if (A >= 0.f) {
-                        const bool cut = ratio > p.clip_hi;
-                        ell = -A * (cut ? p.clip_hi : ratio);
-                        g = cut ? 0.f : -A * ratio;
-                    } else {
-                        const bool cut = ratio < p.clip_lo;
-                        ell = -A * (cut ? p.clip_lo : ratio);
-                        g = cut ? 0.f : -A * ratio;
-                    }
-                    if (p.logp_ref) {
-                        const float x = static_cast<float>(p.logp_ref[t] - r.q);
-                        const float em1 = expm1f(x);
-                        pen = em1 - x;
-                        ell = fmaf(p.beta, pen, ell);
-                        g = fmaf(-p.beta, em1, g);
-                    }
-                    const float w = p.loss_mode == GRPO_SEQUENCE_MEAN
-                                        ? 1.f / (static_cast<float>(p.off[i + 1] - p.off[i]) * p.counts[C_NACT])
-                                        : 1.f / p.counts[C_NVALID];
-                    ell *= w;
-                    g *= w;
-                }
-                g *= p.inv_t;
-                p.lse[t] = static_cast<float>(r.lse);
-                if (p.logp) p.logp[t] = q;
-                if (p.entropy) p.entropy[t] = r.ent;
-                if (p.stats) {
-                    p.stats[3 * static_cast<int64_t>(t)] = q;
-                    p.stats[3 * static_cast<int64_t>(t) + 1] = ratio;
-                    p.stats[3 * static_cast<int64_t>(t) + 2] = pen;
-                }
-                if (p.mode == HEAD_GRAD || p.mode == HEAD_CLIP) {
-                    p.gco[t] = g;
-                    if (p.gmax) atomicMax(&s_max, __float_as_uint(fabsf(g)));
-                }
-                if (p.ell) p.ell[c0 + slot] = ell;
-            }
-        }
+        const RowGrad r = merge_row(p, slot, c0, lane);
+        if (p.gmax && lane == 0) atomicMax(&s_max, __float_as_uint(fabsf(r.g)));
     }
     if (!p.gmax) return;
     __syncthreads();
@@ -564,29 +576,13 @@ cudaError_t launch_pair_coef(const PairParams& p, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------ loss
-// Sums the rows' (or pairs') weighted objectives in fp64 in a fixed order, one
-// block of 256.  With a backward it is block 0 of the last dH join, else a kernel.
-__device__ __forceinline__ void write_loss(const LossParams& l, const int* counts) {
-    __shared__ double sh[256];
-    if (!l.loss) return;
-    double acc = 0.0;
-    if (l.pair_ell) {
-        for (int i = threadIdx.x; i < l.n_pairs; i += 256) acc += l.pair_ell[i];
-    } else {
-        const int nv = counts[C_NVALID];
-        for (int i = threadIdx.x; i < nv; i += 256) acc += static_cast<double>(l.ell[i]);
-    }
-    acc = block_sum(acc, sh);
-    if (threadIdx.x == 0) {
-        const int n = l.pair_ell ? counts[C_NACT] : 1;   // rows carry their weight in the mean already
-        *l.loss = n > 0 ? static_cast<float>(acc / n) : 0.f;
-    }
+// Without a backward; with one, head_grads_kernel does the same.
+__global__ void __launch_bounds__(32) k_loss(const LossParams l, const int* __restrict__ counts) {
+    write_loss(l, counts, threadIdx.x);
 }
 
-__global__ void __launch_bounds__(256) k_loss(const LossParams l, const int* __restrict__ counts) { write_loss(l, counts); }
-
 cudaError_t launch_loss(const LossParams& l, const int* counts, cudaStream_t st) {
-    k_loss<<<1, 256, 0, st>>>(l, counts);
+    k_loss<<<1, 32, 0, st>>>(l, counts);
     return cudaGetLastError();
 }
 
@@ -598,6 +594,44 @@ cudaError_t launch_loss(const LossParams& l, const int* counts, cudaStream_t st)
 // spare: there g is divided by the power of two above the chunk's largest |g|
 // and multiplied by 2^14, and the GEMMs' epilogues undo it (oscale), whatever
 // the caller's loss scale is.  Reads and writes the chunk once: bound by HBM.
+// One row by one block; true if a value is not finite.
+template <bool kBf16>
+__device__ __forceinline__ bool dlogits_row(const HeadChunkParams& p, int slot, int tok, float lse, float q, float coef) {
+    uint4* row = reinterpret_cast<uint4*>(p.dS + static_cast<int64_t>(slot) * p.V_pad);
+    const int nvec = p.V_pad / 8;
+    const float lse2 = lse * 1.4426950408889634f;
+    const float dtok = -coef * expm1f(q);   // g (1 - p_tok)
+    const float* mrow = p.mx + static_cast<int64_t>(slot) * p.nc32;
+    bool bad = false;
+    for (int i = threadIdx.x; i < nvec; i += kTransformThreads) {
+        const int v0 = i * 8;
+        const float c = coef * exp2f(mrow[v0 >> 5] - lse2);
+        const uint4 u = row[i];
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int va = v0 + 2 * j, vb = va + 1;
+            const float2 e = unpack16<false>(w[j]);
+            float d0 = -c * e.x, d1 = -c * e.y;
+            if (va == tok) d0 = dtok;
+            if (vb == tok) d1 = dtok;
+            if (va >= p.V) d0 = 0.f;
+            if (vb >= p.V) d1 = 0.f;
+            const uint16_t h0 = round16<kBf16>(d0), h1 = round16<kBf16>(d1);
+            bad |= nonfinite16<kBf16>(h0) || nonfinite16<kBf16>(h1);
+            o[j] = static_cast<uint32_t>(h0) | (static_cast<uint32_t>(h1) << 16);
+        }
+        row[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    return bad;
+}
+
+__device__ __forceinline__ void zero_row(const HeadChunkParams& p, int slot) {
+    uint4* row = reinterpret_cast<uint4*>(p.dS + static_cast<int64_t>(slot) * p.V_pad);
+    for (int i = threadIdx.x; i < p.V_pad / 8; i += kTransformThreads) row[i] = make_uint4(0, 0, 0, 0);
+}
+
 template <bool kBf16>
 __global__ void __launch_bounds__(kTransformThreads) k_head_dlogits(const HeadChunkParams p, float* oscale) {
     const int2 cbn = chunk_bounds(p.counts, p.cb, p.chunk);
@@ -611,44 +645,55 @@ __global__ void __launch_bounds__(kTransformThreads) k_head_dlogits(const HeadCh
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) oscale[p.chunk] = p.loss_scale / up;
     const int n_fill = min(p.R, (n_c + kBM - 1) / kBM * kBM);
-    const int nvec = p.V_pad / 8;
     bool bad = false;
     for (int slot = blockIdx.x; slot < n_fill; slot += gridDim.x) {
-        uint4* row = reinterpret_cast<uint4*>(p.dS + static_cast<int64_t>(slot) * p.V_pad);
         if (slot >= n_c) {
-            for (int i = threadIdx.x; i < nvec; i += kTransformThreads) row[i] = make_uint4(0, 0, 0, 0);
+            zero_row(p, slot);
             continue;
         }
         const int t = p.rows[c0 + slot];
         if (!GRPO_DCHECK(t >= 0 && t < p.N, p.status)) continue;
         const int tok = p.tokens[t];
-        const float lse2 = p.lse[t] * 1.4426950408889634f;
         const float coef = tok >= 0 && tok < p.V ? up * p.gco[t] : 0.f;
-        const float dtok = -coef * expm1f(p.logp[t]);   // g (1 - p_tok)
-        const float* mrow = p.mx + static_cast<int64_t>(slot) * p.nc32;
-        for (int i = threadIdx.x; i < nvec; i += kTransformThreads) {
-            const int v0 = i * 8;
-            const float c = coef * exp2f(mrow[v0 >> 5] - lse2);
-            const uint4 u = row[i];
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int va = v0 + 2 * j, vb = va + 1;
-                const float2 e = unpack16<false>(w[j]);
-                float d0 = -c * e.x, d1 = -c * e.y;
-                if (va == tok) d0 = dtok;
-                if (vb == tok) d1 = dtok;
-                if (va >= p.V) d0 = 0.f;
-                if (vb >= p.V) d1 = 0.f;
-                const uint16_t h0 = round16<kBf16>(d0), h1 = round16<kBf16>(d1);
-                bad |= nonfinite16<kBf16>(h0) || nonfinite16<kBf16>(h1);
-                o[j] = static_cast<uint32_t>(h0) | (static_cast<uint32_t>(h1) << 16);
-            }
-            row[i] = make_uint4(o[0], o[1], o[2], o[3]);
-        }
+        bad |= dlogits_row<kBf16>(p, slot, tok, p.lse[t], p.logp[t], coef);
     }
     if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(p.found_inf, 1);
+}
+
+// Merge and dlogits of a bf16 chunk in one launch, one block per row: for chunks
+// so small that the launches are what counts, where no step lies between the two
+// (the preference loss sums over rows first; fp16 needs the chunk's largest g).
+__global__ void __launch_bounds__(kTransformThreads) k_merge_dlogits(const HeadMergeParams m, const HeadChunkParams p,
+                                                                     float* oscale) {
+    __shared__ RowGrad s_row;
+    const int2 cbn = chunk_bounds(p.counts, p.cb, p.chunk);
+    const int c0 = cbn.x, n_c = cbn.y;
+    if (n_c == 0) return;
+    if (blockIdx.x == 0 && threadIdx.x == 0) oscale[p.chunk] = p.loss_scale;
+    const int n_fill = min(p.R, (n_c + kBM - 1) / kBM * kBM);
+    bool bad = false;
+    for (int slot = blockIdx.x; slot < n_fill; slot += gridDim.x) {
+        if (slot >= n_c) {
+            zero_row(p, slot);
+            continue;
+        }
+        if (threadIdx.x < 32) {
+            const RowGrad r = merge_row(m, slot, c0, threadIdx.x);
+            if (threadIdx.x == 0) s_row = r;
+        }
+        __syncthreads();
+        const RowGrad r = s_row;
+        bad |= dlogits_row<true>(p, slot, r.tok, r.lse, r.q, r.tok >= 0 ? r.g : 0.f);
+        __syncthreads();   // s_row is read
+    }
+    if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(p.found_inf, 1);
+}
+
+cudaError_t launch_merge_dlogits(const HeadMergeParams& m, const HeadChunkParams& p, float* oscale, int sm_count,
+                                 cudaStream_t st) {
+    const int blocks = p.R < sm_count * 8 ? p.R : sm_count * 8;
+    k_merge_dlogits<<<blocks, kTransformThreads, 0, st>>>(m, p, oscale);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_head_dlogits(const HeadChunkParams& p, float* oscale, bool bf16, int sm_count, cudaStream_t st) {
@@ -751,8 +796,7 @@ cudaError_t launch_head_scale(const HeadChunkParams& p, float* oscale, int sm_co
 // One warp per row of a split dH tile: adds its K pieces in order, scales,
 // rounds and stores it.
 template <bool kBf16>
-__global__ void __launch_bounds__(256) k_dh_join(const HeadChunkParams p, const LossParams l) {
-    if (blockIdx.x == 0) write_loss(l, p.counts);
+__global__ void __launch_bounds__(256) k_dh_join(const HeadChunkParams p) {
     const int2 cbn = chunk_bounds(p.counts, p.cb, p.chunk);
     const int c0 = cbn.x, n_c = cbn.y;
     if (n_c == 0) return;
@@ -791,9 +835,9 @@ __global__ void __launch_bounds__(256) k_dh_join(const HeadChunkParams p, const 
     if (bad) atomicOr(p.found_inf, 1);
 }
 
-cudaError_t launch_head_dh_join(const HeadChunkParams& p, const LossParams& l, bool bf16, int sm_count, cudaStream_t st) {
-    if (bf16) k_dh_join<true><<<sm_count * 4, 256, 0, st>>>(p, l);
-    else k_dh_join<false><<<sm_count * 4, 256, 0, st>>>(p, l);
+cudaError_t launch_head_dh_join(const HeadChunkParams& p, bool bf16, int sm_count, cudaStream_t st) {
+    if (bf16) k_dh_join<true><<<sm_count * 4, 256, 0, st>>>(p);
+    else k_dh_join<false><<<sm_count * 4, 256, 0, st>>>(p);
     return cudaGetLastError();
 }
 

@@ -5,8 +5,9 @@
 //       written.  With a backward it keeps exp(z - running max).
 //   head_few_kernel     the same for at most 32 rows, W as the M operand, so
 //       that W streams through the SMs once: bound by HBM.
-//   head_dh_kernel      dH = dlogits . W, its last wave split over K
+//   head_dh_kernel      dH = dlogits . W
 //   head_dw_kernel      dW = dlogits^T . h, written in the type of W or in fp32
+//   head_grads_kernel   both, for small chunks
 //
 // Sums over K.  tcgen05.mma adds to its fp32 accumulator with rounding towards
 // zero: after d / 16 additions a logit of 11 was 4.6e-5 too small at d = 4096
@@ -673,9 +674,26 @@ struct Finite {
     }
 };
 
-// ====================================================================== dH, last wave split
+// ====================================================================== gradients
+// dH's units are 256 x 256 tiles, sums over the vocabulary, some cut into K pieces;
+// dW's are 256 x 256 tiles, sums over the chunk's rows.
+//
+// Eight epilogue warps, the second four for the upper half of the columns: a dW
+// unit of 1000 rows has 8200 clocks of MMAs, and four warps took longer than that.
+// A thread stores 32-byte pieces of its own row; boxes through shared memory and
+// TMA stores were 10% faster for dW of a few rows, but they need a K-stage's room,
+// which costs as much elsewhere.
+
+// the loss, once all rows are merged (with the last chunk that has rows)
+__device__ __forceinline__ void idle_loss(const HeadChunkParams& p, int lane) {
+    if (blockIdx.x < 2 && p.chunk + 1 == p.counts[C_NCHUNKS]) write_loss(p.loss, p.counts, lane);
+}
+
 struct HeadDhT : DhPairT {
+    static constexpr int kEpiWarps = 8;
+    static constexpr bool kIdle = true;
     using Params = HeadChunkParams;
+    __device__ static void idle(const Params& p, int lane) { idle_loss(p, lane); }
     struct Sched : ChunkSched {
         int n_full, pieces, rem, kper;
     };
@@ -708,17 +726,20 @@ struct HeadDhT : DhPairT {
         const int2 u = piece(sc, unit);
         return Coord{mtile(sc, u.x, rank) * kBM, dtile(sc, u.x) * kBN, u.y < 0 ? 0 : u.y * sc.kper};
     }
-    __device__ static uint32_t tx_bytes(const Params& p, const Sched&, const Coord& c) {
-        return 2 * 16384 + 8192 * min(4, (p.d - c.n0) / 64);
+    __device__ static uint32_t tx_bytes(const Params& p, const Sched& sc, const Coord& c) {
+        return DhPairT::tx_bytes(p, sc, DhPairT::Coord{c.m0, c.n0});
     }
     __device__ static void load(const Params& p, const Sched& sc, const Coord& c, int k, uint8_t* st, uint32_t bar,
                                 const CUtensorMap* mA, const CUtensorMap* mA2, const CUtensorMap* mB, int rank) {
         DhPairT::load(p, sc, DhPairT::Coord{c.m0, c.n0}, c.k0 + k, st, bar, mA, mA2, mB, rank);
     }
     __device__ static void epi_begin(const Params&, const Sched&, int, int, int, Epi&) {}
+    __device__ static void epi_end(const Params&, const Sched&, int, Epi&) {}
     template <bool kBf16>
     __device__ static void epi_item(const Params& p, const Sched& sc, int unit, int, int rank, uint32_t tacc, Epi&) {
-        const int row = (threadIdx.x & 31) + 32 * ((threadIdx.x >> 5) & 3);
+        const int warp = threadIdx.x >> 5;
+        const int row = (threadIdx.x & 31) + 32 * (warp & 3);
+        const int c0 = ((warp - 2) >> 2) * (kBN / 64), c1 = c0 + kBN / 64;   // 32-column groups of this warp
         const int2 u = piece(sc, unit);
         const int slot = mtile(sc, u.x, rank) * kBM + row;
         const int n0 = dtile(sc, u.x) * kBN;
@@ -729,7 +750,7 @@ struct HeadDhT : DhPairT {
             const int64_t tile = static_cast<int64_t>(u.y) * sc.rem + (u.x - sc.n_full);
             float* out = p.dh_part + ((tile * 2 + rank) * kBM + row) * kBN;
 #pragma unroll 1
-            for (int c = 0; c < kBN / 32; ++c) {
+            for (int c = c0; c < c1; ++c) {
                 if (n0 + c * 32 >= p.d) break;
                 float v[32];
                 tmem_ld32(tacc + c * 32, v);
@@ -751,7 +772,7 @@ struct HeadDhT : DhPairT {
         uint16_t* out = p.dH + static_cast<int64_t>(t) * p.d;
         Finite<kBf16> fin;
 #pragma unroll 1
-        for (int c = 0; c < kBN / 32; ++c) {
+        for (int c = c0; c < c1; ++c) {
             const int col0 = n0 + c * 32;
             if (col0 >= p.d) break;
             float v[32];
@@ -771,43 +792,11 @@ struct HeadDhT : DhPairT {
         }
         if (valid && fin.bad()) atomicOr(p.found_inf, 1);
     }
-    __device__ static void epi_end(const Params&, const Sched&, int, Epi&) {}
 };
 
-// dW's 16-bit tiles leave through shared memory, 32 rows of 64 columns (4 KB, in
-// the 128-byte swizzle) per epilogue warp, and a TMA store.  A thread owns a row,
-// so storing from registers means 32-byte pieces of 32 rows per instruction:
-// dW of one row of the 8B head took 352 us that way, 317 this way.
-constexpr int kOutBytes = 4096;
-
-// 32 columns of this lane's row, packed, as the left (half 0) or right half of the box
-__device__ __forceinline__ void out_stage(uint8_t* buf, int lane, int half, const uint32_t (&pk)[16]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint4*>(buf + lane * 128 + (((4 * half + j) ^ (lane & 7)) << 4)) =
-            make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
-}
-
-// the box may be written again
-__device__ __forceinline__ void out_free(int lane) {
-    if (lane == 0) tma_store_wait_read();
-    __syncwarp();
-}
-
-__device__ __forceinline__ void out_send(const CUtensorMap* map, const uint8_t* buf, int lane, int x, int y) {
-    fence_async_proxy();
-    __syncwarp();
-    if (lane == 0) tma_store_2d(map, buf, x, y);
-}
-
-// ====================================================================== dW
 // DwPairT with the operators' output: chunks add up in fp32 (dw_acc), and with
 // dw16 the last chunk (often the only one) rounds the sum to the type of W.
-// With few rows a unit's MMAs are short (16 K-stages for 1024 rows, about 8200
-// clocks), so eight warps share the epilogue: four took longer than that.
 struct HeadDwT : DwPairT {
-    static constexpr int kStages = 6;
-    static constexpr int kOutOffset = kStages * kStageBytes + 1024;   // the output boxes, past the barriers
     static constexpr int kEpiWarps = 8;
     using Params = HeadChunkParams;
     struct Sched : ChunkSched {
@@ -817,31 +806,31 @@ struct HeadDwT : DwPairT {
         sc.last = p.dw16 && p.chunk + 1 == p.counts[C_NCHUNKS];
         return DwPairT::setup(p, sc);
     }
+    __device__ static void epi_begin(const Params&, const Sched&, int, int, int, Epi&) {}
+    __device__ static void epi_end(const Params&, const Sched&, int, Epi&) {}
     template <bool kBf16>
     __device__ static void epi_item(const Params& p, const Sched& sc, int unit, int, int rank, uint32_t tacc, Epi&) {
         const int warp = threadIdx.x >> 5;
         const int row = (threadIdx.x & 31) + 32 * (warp & 3);
-        const int half = (warp - 2) >> 2;
+        const int c0 = ((warp - 2) >> 2) * (kBN / 64), c1 = c0 + kBN / 64;   // 32-column groups of this warp
         const int v = vtile(sc, unit, rank) * kBM + row;
         const int n0 = dtile(sc, unit) * kBN;
         const bool valid = v < p.V;
         if (!__any_sync(0xffffffffu, valid)) return;
         const bool first = p.chunk == 0;
         const int64_t at = static_cast<int64_t>(valid ? v : 0) * p.d;
-        extern __shared__ uint8_t smem_raw[];
-        const int lane = threadIdx.x & 31;
-        uint8_t* out = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u) + kOutOffset + (warp - 2) * kOutBytes;
         Finite<kBf16> fin;
 #pragma unroll 1
-        for (int c = half * (kBN / 64); c < (half + 1) * (kBN / 64); ++c) {
+        for (int c = c0; c < c1; ++c) {
             const int col0 = n0 + c * 32;
             if (col0 >= p.d) break;
             float x[32];
             tmem_ld32(tacc + c * 32, x);
+            if (!valid) continue;
             float* acc = p.dw_acc + at + col0;
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] *= sc.winv;
-            if (!first && valid) {
+            if (!first) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float prev[8];
@@ -857,11 +846,12 @@ struct HeadDwT : DwPairT {
                     pk[j] = pack2(x[2 * j], x[2 * j + 1], kBf16);
                     fin.see(pk[j]);
                 }
-                // whole boxes of 64 columns (d is a multiple of 64); rows past V are not written
-                if ((c & 1) == 0) out_free(lane);
-                out_stage(out, lane, c & 1, pk);
-                if ((c & 1) == 1) out_send(&p.mDw16, out, lane, col0 - 32, v - lane);
-            } else if (valid) {
+                uint16_t* out = p.dw16 + at + col0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    st_global_v8(out + 16 * h, pk[8 * h], pk[8 * h + 1], pk[8 * h + 2], pk[8 * h + 3], pk[8 * h + 4],
+                                 pk[8 * h + 5], pk[8 * h + 6], pk[8 * h + 7]);
+            } else {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) fin.see_f32(x[j]);
 #pragma unroll
@@ -875,22 +865,123 @@ struct HeadDwT : DwPairT {
         if (valid && fin.bad()) atomicOr(p.found_inf, 1);
     }
 };
-constexpr int kDwThreads = 64 + 32 * HeadDwT::kEpiWarps;
-constexpr int kDwSmem = 1024 + HeadDwT::kOutOffset + HeadDwT::kEpiWarps * kOutBytes;
+
+// Both in one launch, for small chunks: dH's units come first, one per SM pair at
+// a time; the pairs left over in dH's last round go on with dW's units, and all
+// share the rest of those.
+struct HeadGradsT {
+    static constexpr int kStages = 7;
+    static constexpr int kStageBytes = DhPairT::kStageBytes;
+    static constexpr int kEpiWarps = 8;
+    static constexpr bool kMixed = true, kIdle = true;
+    static_assert(DhPairT::kStageBytes == DwPairT::kStageBytes, "one ring for both");
+    using Params = HeadChunkParams;
+    // Pair c of np does dH units c, c + np, ...: `full` rounds, and pairs below `r`
+    // one more.  Meanwhile the others do `x` dW units each, as many as that round
+    // takes; then all pairs share the dW units that are left.
+    struct Sched {
+        HeadDhT::Sched h;
+        HeadDwT::Sched w;
+        int n_units, np, full, r, x;
+    };
+    struct Coord {
+        int w;                // 1: dW
+        int a, b, k0;         // dH: m0, n0, first K-stage; dW: v0, n0
+    };
+    struct Epi {
+        int unused;
+    };
+    __device__ static bool setup(const Params& p, Sched& sc) {
+        if (!HeadDhT::setup(p, sc.h) || !HeadDwT::setup(p, sc.w)) return false;
+        sc.np = static_cast<int>(gridDim.x) >> 1;
+        sc.full = sc.h.n_units / sc.np;
+        sc.r = sc.h.n_units - sc.full * sc.np;
+        // K-stages of the last round's units, and 12 and 4 for the units' own cost (as in k_plan)
+        const int kl = (sc.h.rem > 0 ? sc.h.kper : sc.h.ks) + 12;
+        sc.x = sc.r > 0 ? min(kl / (sc.w.ks + 4), sc.w.n_units / (sc.np - sc.r)) : 0;
+        const int rest = sc.w.n_units - (sc.np - sc.r) * sc.x;
+        const int rounds = sc.full + max(sc.r > 0 ? 1 : 0, sc.x) + (rest + sc.np - 1) / sc.np;
+        sc.n_units = rounds * sc.np;
+        return true;
+    }
+    // unit = round * np + pair -> (kind: 0 dH, 1 dW, -1 nothing; index of that kind's unit)
+    __device__ static int2 pick(const Sched& sc, int unit) {
+        int j = unit / sc.np;
+        const int c = unit - j * sc.np;
+        if (j < sc.full) return make_int2(0, unit);
+        j -= sc.full;
+        const int others = sc.np - sc.r;
+        if (c < sc.r) {
+            if (j == 0) return make_int2(0, sc.full * sc.np + c);
+            j -= 1;
+        } else {
+            if (j < sc.x) return make_int2(1, j * others + c - sc.r);
+            j -= sc.x;
+        }
+        const int w = others * sc.x + j * sc.np + c;
+        return w < sc.w.n_units ? make_int2(1, w) : make_int2(-1, 0);
+    }
+    __device__ static int items(const Params&, const Sched& sc, int unit) { return pick(sc, unit).x >= 0 ? 1 : 0; }
+    __device__ static int ksteps(const Params& p, const Sched& sc, int unit) {
+        const int2 u = pick(sc, unit);
+        return u.x == 1 ? sc.w.ks : u.x == 0 ? HeadDhT::ksteps(p, sc.h, u.y) : 0;
+    }
+    __device__ static Coord coord(const Params& p, const Sched& sc, int unit, int item, int rank) {
+        const int2 u = pick(sc, unit);
+        if (u.x == 1) {
+            const DwPairT::Coord c = DwPairT::coord(p, sc.w, u.y, item, rank);
+            return Coord{1, c.v0, c.n0, 0};
+        }
+        const HeadDhT::Coord c = HeadDhT::coord(p, sc.h, u.y, item, rank);
+        return Coord{0, c.m0, c.n0, c.k0};
+    }
+    __device__ static uint32_t tx_bytes(const Params& p, const Sched& sc, const Coord& c) {
+        return c.w ? DwPairT::tx_bytes(p, sc.w, DwPairT::Coord{c.a, c.b}) : HeadDhT::tx_bytes(p, sc.h, HeadDhT::Coord{c.a, c.b, 0});
+    }
+    __device__ static void load(const Params& p, const Sched& sc, const Coord& c, int k, uint8_t* st, uint32_t bar,
+                                const CUtensorMap* mA, const CUtensorMap* mA2, const CUtensorMap* mB, int rank) {
+        if (c.w) DwPairT::load(p, sc.w, DwPairT::Coord{c.a, c.b}, k, st, bar, mA2, mA2, &p.mHct, rank);
+        else HeadDhT::load(p, sc.h, HeadDhT::Coord{c.a, c.b, c.k0}, k, st, bar, mA, mA2, mB, rank);
+    }
+    __device__ static int kind(const Sched& sc, int unit) { return pick(sc, unit).x; }
+    template <bool kBf16>
+    __device__ static void mma_kind(int kind, uint32_t st, uint32_t acc, bool first) {
+        if (kind == 1) DwPairT::mma<kBf16>(st, acc, first);
+        else DhPairT::mma<kBf16>(st, acc, first);
+    }
+    __device__ static void idle(const Params& p, int lane) { idle_loss(p, lane); }
+    __device__ static void epi_begin(const Params&, const Sched&, int, int, int, Epi&) {}
+    __device__ static void epi_end(const Params&, const Sched&, int, Epi&) {}
+    template <bool kBf16>
+    __device__ static void epi_item(const Params& p, const Sched& sc, int unit, int item, int rank, uint32_t tacc, Epi&) {
+        const int2 u = pick(sc, unit);
+        HeadDhT::Epi eh;
+        HeadDwT::Epi ew;
+        if (u.x == 1) HeadDwT::epi_item<kBf16>(p, sc.w, u.y, item, rank, tacc, ew);
+        else HeadDhT::epi_item<kBf16>(p, sc.h, u.y, item, rank, tacc, eh);
+    }
+};
+constexpr int kGradThreads = 64 + 32 * HeadGradsT::kEpiWarps;
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kGradThreads, 1)
+    head_grads_kernel(const __grid_constant__ HeadChunkParams p, const __grid_constant__ CUtensorMap mA,
+                      const __grid_constant__ CUtensorMap mA2, const __grid_constant__ CUtensorMap mB) {
+    tc_pair_body<HeadGradsT, kBf16>(p, mA, mA2, mB);
+}
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kGradThreads, 1)
     head_dh_kernel(const __grid_constant__ HeadChunkParams p, const __grid_constant__ CUtensorMap mA,
                    const __grid_constant__ CUtensorMap mA2, const __grid_constant__ CUtensorMap mB) {
     tc_pair_body<HeadDhT, kBf16>(p, mA, mA2, mB);
 }
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kDwThreads, 1)
+__global__ void __launch_bounds__(kGradThreads, 1)
     head_dw_kernel(const __grid_constant__ HeadChunkParams p, const __grid_constant__ CUtensorMap mA,
                    const __grid_constant__ CUtensorMap mA2, const __grid_constant__ CUtensorMap mB) {
     tc_pair_body<HeadDwT, kBf16>(p, mA, mA2, mB);
-    tma_store_wait_all();   // of the threads that sent output boxes
 }
 
 }  // namespace
@@ -911,16 +1002,24 @@ cudaError_t launch_head_logits(const LogitsParams& p, const CUtensorMap& mH, con
     }
 }
 
-cudaError_t launch_head_dh(const HeadChunkParams& p, const CUtensorMap& mDS, const CUtensorMap& mWmn, int n_sm, bool bf16,
-                           cudaStream_t st) {
-    return bf16 ? launch_pairs<head_dh_kernel<true>>(kThreads, smem_bytes<HeadDhT>(), n_sm, st, p, mDS, mDS, mWmn)
-                : launch_pairs<head_dh_kernel<false>>(kThreads, smem_bytes<HeadDhT>(), n_sm, st, p, mDS, mDS, mWmn);
+cudaError_t launch_head_grads(const HeadChunkParams& p, const CUtensorMap& mDS, const CUtensorMap& mDSmn,
+                              const CUtensorMap& mWmn, int n_sm, bool bf16, cudaStream_t st) {
+    constexpr int smem = smem_bytes<HeadGradsT>();
+    return bf16 ? launch_pairs<head_grads_kernel<true>>(kGradThreads, smem, n_sm, st, p, mDS, mDSmn, mWmn)
+                : launch_pairs<head_grads_kernel<false>>(kGradThreads, smem, n_sm, st, p, mDS, mDSmn, mWmn);
 }
 
-cudaError_t launch_head_dw(const HeadChunkParams& p, const CUtensorMap& mDSmn, const CUtensorMap& mHct, int n_sm, bool bf16,
+cudaError_t launch_head_dh(const HeadChunkParams& p, const CUtensorMap& mDS, const CUtensorMap& mWmn, int n_sm, bool bf16,
                            cudaStream_t st) {
-    return bf16 ? launch_pairs<head_dw_kernel<true>>(kDwThreads, kDwSmem, n_sm, st, p, mDSmn, mDSmn, mHct)
-                : launch_pairs<head_dw_kernel<false>>(kDwThreads, kDwSmem, n_sm, st, p, mDSmn, mDSmn, mHct);
+    constexpr int smem = smem_bytes<HeadDhT>();
+    return bf16 ? launch_pairs<head_dh_kernel<true>>(kGradThreads, smem, n_sm, st, p, mDS, mDS, mWmn)
+                : launch_pairs<head_dh_kernel<false>>(kGradThreads, smem, n_sm, st, p, mDS, mDS, mWmn);
+}
+
+cudaError_t launch_head_dw(const HeadChunkParams& p, const CUtensorMap& mDSmn, int n_sm, bool bf16, cudaStream_t st) {
+    constexpr int smem = smem_bytes<HeadDwT>();
+    return bf16 ? launch_pairs<head_dw_kernel<true>>(kGradThreads, smem, n_sm, st, p, mDSmn, mDSmn, p.mHct)
+                : launch_pairs<head_dw_kernel<false>>(kGradThreads, smem, n_sm, st, p, mDSmn, mDSmn, p.mHct);
 }
 
 template <bool kBf16, int kNC>

@@ -375,6 +375,28 @@ struct EpiWarps {
     static constexpr int value = get<T>(nullptr);
 };
 
+// A traits class whose units are of several kinds has kMixed = true, kind(sc, unit)
+// and, in place of mma(), mma_kind(kind, ...).
+template <class T>
+struct Mixed {
+    template <class U>
+    static constexpr bool get(decltype(U::kMixed)*) { return U::kMixed; }
+    template <class U>
+    static constexpr bool get(...) { return false; }
+    static constexpr bool value = get<T>(nullptr);
+};
+
+// A traits class with kIdle = true has idle(), which runs in the peer CTA's MMA
+// warp: that one has nothing to issue.
+template <class T>
+struct Idle {
+    template <class U>
+    static constexpr bool get(decltype(U::kIdle)*) { return U::kIdle; }
+    template <class U>
+    static constexpr bool get(...) { return false; }
+    static constexpr bool value = get<T>(nullptr);
+};
+
 template <class T>
 __device__ __forceinline__ int acc_buf(int it) {
     return WideAcc<T>::value ? 0 : (it & 1);
@@ -469,6 +491,8 @@ __device__ __forceinline__ void tc_pair_body(const typename T::Params& p, const 
             for (int unit = cid; unit < sc.n_units; unit += n_pairs) {
                 const int n_items = T::items(p, sc, unit);
                 const int ks = T::ksteps(p, sc, unit);
+                [[maybe_unused]] int kind = 0;
+                if constexpr (Mixed<T>::value) kind = T::kind(sc, unit);
                 for (int item = 0; item < n_items; ++item, ++it) {
                     const int b = acc_buf<T>(it);
                     const uint32_t aph = acc_phase<T>(it);
@@ -479,7 +503,11 @@ __device__ __forceinline__ void tc_pair_body(const typename T::Params& p, const 
                         if (!mbar_wait(&sm.full[s], ph, sm.abort_flag, status)) goto mma_done;
                         ++n_used;
                         tc_fence_after();
-                        T::template mma<kBf16>(smem_u32(sm.stages + s * T::kStageBytes), acc, k == 0);
+                        const uint32_t stage = smem_u32(sm.stages + s * T::kStageBytes);
+                        if constexpr (Mixed<T>::value)
+                            T::template mma_kind<kBf16>(kind, stage, acc, k == 0);
+                        else
+                            T::template mma<kBf16>(stage, acc, k == 0);
                         umma_pair_commit_both(&sm.empty[s]);
                         if (++s == T::kStages) {
                             s = 0;
@@ -503,6 +531,8 @@ __device__ __forceinline__ void tc_pair_body(const typename T::Params& p, const 
                 }
             }
         }
+        if constexpr (Idle<T>::value)
+            if (!leader) T::idle(p, lane);
     } else {
         // ------------------------------------------------ epilogue (both CTAs, own rows)
         const int row = lane + 32 * (warp & 3);
