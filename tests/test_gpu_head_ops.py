@@ -411,8 +411,9 @@ def test_checked_build_finds_no_bad_index():
     rg._declare(lib)
     normal, rg._lib = rg.load(), lib
     try:
-        for cr, G, L in ((0, 2, 100), (128, 2, 100), (256, 2, 40)):
-            c = Case(3, G, L, 128, 500, "bf16", "ragged", seed=16, chunk_rows=cr, beta=0.1)
+        for cr, G, L, V, d in ((0, 2, 100, 500, 128), (128, 2, 100, 500, 128), (256, 2, 40, 500, 128),
+                               (0, 2, 100, 9000, 128), (128, 2, 100, 40000, 128), (0, 2, 1500, 2049, 1280)):
+            c = Case(3, G, L, d, V, "bf16", "ragged", seed=16, chunk_rows=cr, beta=0.1)
             old, ref = (torch.from_numpy(x).cuda() for x in c.old_ref())
             check_logp(c, *c.logp())
             c.clip(torch.randn(c.n, device="cuda"), old, ref, rg.clip_opts())
@@ -582,3 +583,44 @@ def test_offsets_past_32_bits():
     for got, want in ((dW[cols].double(), rW), (dH[rows].double(), rH)):
         assert float((got - want).norm() / want.norm()) < 3 * 2 ** -8
         assert float((got - want).abs().max() / want.abs().max()) < 4 * 2 ** -8
+
+
+@pytest.mark.parametrize("dt,N,d,V,share,cr,dw_f32", [
+    ("bf16", 8192, 1280, 2049, 0.03, 0, False),    # relative dlogits, dH and dW in launches of their own
+    ("fp16", 8192, 1280, 2049, 0.03, 0, True),     # the dlogits pass
+    ("bf16", 512, 5120, 8000, 0.1, 0, False),      # the dlogits pass in bf16
+    ("bf16", 8192, 1280, 4100, 0.55, 4096, False),  # two chunks: dW's sum in the workspace
+    ("fp16", 8192, 1280, 4100, 0.55, 4096, True),
+])
+def test_large_chunks(dt, N, d, V, share, cr, dw_f32):
+    """Chunks above the sizes where dH and dW share a launch; few of the rows count, and the reference holds those alone."""
+    g = torch.Generator().manual_seed(40)
+    rng = np.random.default_rng(40)
+    keep = np.flatnonzero(rng.random(N) < share)
+    W = (torch.randn(V, d, generator=g) * d ** -0.5).to(TORCH[dt])
+    tok = torch.randint(0, V, (N,), generator=g, dtype=torch.int32)
+    h = (torch.randn(N, d, generator=g) + 8 * W[tok.long()].float()).to(TORCH[dt])
+    mask = np.zeros(N, np.uint8)
+    mask[keep] = 1
+    dq = rng.normal(size=N).astype(np.float32)
+    P = R.Problem(1, 1, len(keep), h[keep].double().numpy(), W.double().numpy(), tok[keep].numpy(),
+                  np.ones(len(keep), bool))
+    shape = rg.make_shape(1, 1, N, d, V, CODE[dt], chunk_rows=cr)
+    hd, Wd, td, md, dqd = h.cuda(), W.cuda(), tok.cuda(), torch.from_numpy(mask).cuda(), torch.from_numpy(dq).cuda()
+    ws = torch.full((rg.grpo_policy_workspace_bytes(shape, "logp_grad", dw_f32),), 255, dtype=torch.uint8, device="cuda")
+    status, inf = (torch.full((1,), 9, dtype=torch.int32, device="cuda") for _ in range(2))
+    outs = []
+    for _ in range(2):
+        dH = torch.full_like(hd, 7.0)
+        dW = torch.full_like(Wd, 7.0, dtype=torch.float32 if dw_f32 else Wd.dtype)
+        rg.grpo_logprobs_bwd(hd, Wd, td, md, dqd, shape, 1.0, 32.0, ws, dH, dW, inf, status, dw_f32=dw_f32)
+        torch.cuda.synchronize()
+        outs.append((dH, dW))
+    assert int(status) == 0 and int(inf) == 0
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    lp = R.logp_entropy(P)[2]
+    rH, rW, aH, aW = R.gradients(P, dq[keep].astype(np.float64), lp)
+    qe = R.logp_bound(P).max()
+    eH, eW = np.abs(host(dH)[keep] - 32 * rH), np.abs(host(dW) - 32 * rW)
+    assert np.all(eH <= R.grad_bound(32 * rH, 32 * aH, dt, dt, qe, 32)) and not host(dH)[mask == 0].any()
+    assert np.all(eW <= R.grad_bound(32 * rW, 32 * aW, dt, "f32" if dw_f32 else dt, qe, 32))
