@@ -25,7 +25,8 @@ constexpr int kPieceK = 1024;       // K elements the tensor cores add up before
 constexpr int kHeadThreads = 384;   // a warpgroup with the producer and MMA warps, two of epilogue warps
 constexpr int kHeadSplitsMax = 512;    // vocabulary splits of the logits kernel
 constexpr int kHeadChunkTiles = 76;    // default rows per chunk, in tiles of 128
-constexpr int kDhSlotsMax = 304;    // 256 x 256 partial tiles of dH (4 per SM pair)
+constexpr int kDhSlotsMax = 304;      // 256 x 256 partial tiles of dH (4 per SM pair, 80 MB)
+constexpr int kDhWideSlotsMax = 256;  // 256 x 512 ones
 constexpr int kFewRows = 32;        // rows of the few-row kernel
 constexpr int kFewVocab = 128;      // vocabulary rows per tile of the few-row kernel
 // what stands for a logit that does not count (the given token's own, columns
@@ -46,7 +47,7 @@ struct PlanParams {
     int by_pair;            // chunks of whole pairs of completions
     int pairs_of_g2;        // completions 2i and 2i + 1 are a pair: count pairs, not completions, with a valid row
     int max_chunks;
-    int n_nt, ks, n_pairs, slots_max;   // dH: 256-wide d tiles, K-stages, SM pairs, partial tiles
+    int n_nt, ks, n_pairs, slots_max;   // dH: d tiles, K-stages, SM pairs, partial tiles
     int backward;
     int n_w;                // dW units in dH's launch (0: dW has its own)
     int* counts;
@@ -186,7 +187,8 @@ struct HeadChunkParams : ChunkParams {
     LossParams loss;        // written with the last chunk that has rows
     float* dw_acc;          // fp32 dW (the caller's, or the workspace's when dw16 is given and there are several chunks)
     uint16_t* dw16;         // 16-bit dW, nullable
-    float* dh_part;         // [slots][2][128 x 256] fp32
+    float* dh_part;         // [slots][256 x dh_cols] fp32
+    int dh_cols;            // columns of a dH unit: 256 or 512
     const int2* dh_plan;
     const float* logp;      // [N] q
     float* rowf;            // nullable: [R] factor of a dlogits row (relative dlogits)

@@ -28,7 +28,7 @@ struct HeadLayout {
     size_t counts, off, cb, pb, dh_plan, lg_plan, gmax, far, oscale, rowf, rows, zt, lse, gco, ell, q, pair_ell, hc, part, mx, ds, hct, dh_part,
         dw_acc, total;
     int64_t N;
-    int n_seq, R, max_chunks, S, n_ntiles, n_vt, V_pad, nc32, slots, by_pair, relative, one_launch;
+    int n_seq, R, max_chunks, S, n_ntiles, n_vt, V_pad, nc32, slots, by_pair, relative, one_launch, dh_cols;
 };
 
 bool head_shape_ok(const grpo_shape& s, int op) {
@@ -78,11 +78,17 @@ bool head_layout(const grpo_shape& s, int op, int dw_f32, HeadLayout* o) {
     o->S = o->n_ntiles < kHeadSplitsMax ? o->n_ntiles : least > kHeadSplitsMax ? least : kHeadSplitsMax;
     o->V_pad = (s.V + 63) / 64 * 64;
     o->nc32 = ((s.V + 31) / 32 + 7) / 8 * 8;
-    const int64_t units = static_cast<int64_t>((o->R + 2 * kBM - 1) / (2 * kBM)) * ((s.d + kBN - 1) / kBN);
+    // dH in units of 512 columns where d is whole units and a full chunk has two for every SM pair: 4.50
+    // against 4.74 ms for dH of 7.5K rows of the 8B head; with fewer units their raggedness costs more
+    // (d = 1536, 4.9K rows: 1.45 against 1.37 ms)
+    const int row_pairs = (o->R + 2 * kBM - 1) / (2 * kBM);
+    o->dh_cols = !o->one_launch && s.d % (2 * kBN) == 0 && row_pairs * (s.d / (2 * kBN)) >= 2 * 76 ? 2 * kBN : kBN;
+    const int64_t units = static_cast<int64_t>(row_pairs) * ((s.d + o->dh_cols - 1) / o->dh_cols);
     // up to 32 K-stages (V = 2048) a unit is not worth splitting: no partial tiles, and no launch to join them
     const int ks = (s.V + kBK - 1) / kBK;
     const int64_t pieces = ks > 32 ? units * ks : 0;
-    o->slots = static_cast<int>(pieces < kDhSlotsMax ? pieces : kDhSlotsMax);
+    const int most = o->dh_cols == kBN ? kDhSlotsMax : kDhWideSlotsMax;
+    o->slots = static_cast<int>(pieces < most ? pieces : most);
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -117,7 +123,7 @@ bool head_layout(const grpo_shape& s, int op, int dw_f32, HeadLayout* o) {
         o->mx = take(R * o->nc32 * 4);
         o->ds = take(R * o->V_pad * 2);
         o->hct = take(R * s.d * 2);
-        o->dh_part = take(static_cast<size_t>(o->slots) * 2 * kBM * kBN * 4);
+        o->dh_part = take(static_cast<size_t>(o->slots) * 2 * kBM * o->dh_cols * 4);
         if (!dw_f32 && o->max_chunks > 1) o->dw_acc = take(static_cast<size_t>(s.V) * s.d * 4);
     }
     o->total = off;
@@ -266,7 +272,7 @@ struct HeadRun {
         p.R = L.R;
         p.by_pair = L.by_pair;
         p.max_chunks = L.max_chunks;
-        p.n_nt = (s.d + kBN - 1) / kBN;
+        p.n_nt = (s.d + L.dh_cols - 1) / L.dh_cols;
         p.ks = (s.V + kBK - 1) / kBK;
         p.n_pairs = dev.sm_count / 2;
         p.slots_max = L.slots;
@@ -465,6 +471,7 @@ struct HeadRun {
         p.dw_acc = c.dw_f32 ? static_cast<float*>(c.dW) : at<float>(L.dw_acc);
         p.dw16 = c.dw_f32 ? nullptr : static_cast<uint16_t*>(c.dW);
         p.dh_part = at<float>(L.dh_part);
+        p.dh_cols = L.dh_cols;
         p.dh_plan = at<int2>(L.dh_plan);
         p.logp = c.logp ? c.logp : at<float>(L.q);
         p.gmax = at<unsigned>(L.gmax);

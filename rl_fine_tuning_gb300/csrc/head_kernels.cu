@@ -793,7 +793,7 @@ cudaError_t launch_head_scale(const HeadChunkParams& p, float* oscale, int sm_co
 }
 
 // ------------------------------------------------------------ dH join
-// One warp per row of a split dH tile: adds its K pieces in order, scales,
+// One warp per row (and 256 columns) of a split dH tile: adds its K pieces in order, scales,
 // rounds and stores it.
 template <bool kBf16>
 __global__ void __launch_bounds__(256) k_dh_join(const HeadChunkParams p) {
@@ -801,23 +801,25 @@ __global__ void __launch_bounds__(256) k_dh_join(const HeadChunkParams p) {
     const int c0 = cbn.x, n_c = cbn.y;
     if (n_c == 0) return;
     const int2 plan = p.dh_plan[p.chunk];
-    const int n_nt = (p.d + kBN - 1) / kBN;
+    const int cols = p.dh_cols, halves = cols / kBN;
+    const int n_nt = (p.d + cols - 1) / cols;
     const int units = (n_c + 2 * kBM - 1) / (2 * kBM) * n_nt;
     const int rem = units - plan.x;
     const float scale = p.oscale[p.chunk] * dh_gain(p.V, plan.y);
     const int lane = threadIdx.x & 31;
     bool bad = false;
-    for (int it = blockIdx.x * 8 + (threadIdx.x >> 5); it < rem * 2 * kBM; it += gridDim.x * 8) {
-        const int r = it / (2 * kBM), row = it - r * 2 * kBM;
+    for (int it = blockIdx.x * 8 + (threadIdx.x >> 5); it < rem * 2 * kBM * halves; it += gridDim.x * 8) {
+        const int r = it / (2 * kBM * halves), rest = it - r * 2 * kBM * halves;
+        const int row = rest / halves, col0 = (rest - row * halves) * kBN + 8 * lane;
         const int unit = plan.x + r;
         const int slot = unit / n_nt * 2 * kBM + row;
-        const int col = unit % n_nt * kBN + 8 * lane;
+        const int col = unit % n_nt * cols + col0;
         if (slot >= n_c || col >= p.d) continue;
         const int t = p.rows[c0 + slot];
         if (!GRPO_DCHECK(t >= 0 && t < p.N, p.status)) continue;
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        const float* src = p.dh_part + (static_cast<int64_t>(r) * 2 * kBM + row) * kBN + 8 * lane;
-        for (int s = 0; s < plan.y; ++s, src += static_cast<int64_t>(rem) * 2 * kBM * kBN) {
+        const float* src = p.dh_part + (static_cast<int64_t>(r) * 2 * kBM + row) * cols + col0;
+        for (int s = 0; s < plan.y; ++s, src += static_cast<int64_t>(rem) * 2 * kBM * cols) {
             const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
             acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w;
             acc[4] += b.x, acc[5] += b.y, acc[6] += b.z, acc[7] += b.w;

@@ -591,6 +591,8 @@ def test_offsets_past_32_bits():
     ("bf16", 512, 5120, 8000, 0.1, 0, False),      # the dlogits pass in bf16
     ("bf16", 8192, 1280, 4100, 0.55, 4096, False),  # two chunks: dW's sum in the workspace
     ("fp16", 8192, 1280, 4100, 0.55, 4096, True),
+    ("bf16", 8192, 2560, 2049, 0.03, 0, False),    # dH in units of 512 columns, all of them split
+    ("fp16", 8192, 2560, 2049, 0.6, 0, False),     # whole and split ones
 ])
 def test_large_chunks(dt, N, d, V, share, cr, dw_f32):
     """Chunks above the sizes where dH and dW share a launch; few of the rows count, and the reference holds those alone."""
