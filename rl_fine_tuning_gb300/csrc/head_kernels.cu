@@ -14,6 +14,7 @@ namespace grpo {
 namespace {
 
 constexpr int kPlanItems = 16;
+constexpr int kTilesPerSplit = 8;
 
 // exclusive sum over the block; *total gets the block's sum
 __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
@@ -124,7 +125,10 @@ __device__ __forceinline__ double token_logit(const uint4* a, const uint4* b, in
 //
 // Logits split: a unit is (256 rows, nps vocabulary tiles of 256); nps is the one
 // for which the units, one per SM pair at a time, take the fewest tile times,
-// with 0.002 of a tile time for each split's partials.
+// with 0.002 of a tile time for each split's partials.  At most kTilesPerSplit
+// tiles: with long units all row tiles of the chunk are in flight at once, and h
+// no longer stays in L2 (9728 rows, d = 4096, V = 32768: 64 tiles a unit read 3.9 GB
+// from memory and took 1.45 ms, 8 read 0.9 GB and took 1.35).
 //
 // Chunks hold R rows, or (by_pair) as many whole pairs of completions as fit R
 // rows: a pair's d loss / d q needs the sums over both completions, so a chunk
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(const PlanParams p) {
         for (int h = 0; h < 2; ++h) {
             const int k = lane + 1 + 32 * h;   // tiles per split
             const int s = (p.n_ntiles + k - 1) / k;
-            if (k > p.n_ntiles || s > p.s_max) continue;
+            if (k > p.n_ntiles || s > p.s_max || (k > kTilesPerSplit && p.n_ntiles <= kTilesPerSplit * p.s_max)) continue;
             const float cost = static_cast<float>((row_pairs * s + p.n_pairs - 1) / p.n_pairs) * k + 0.002f * s;
             if (cost < best_cost) {
                 best_cost = cost;
