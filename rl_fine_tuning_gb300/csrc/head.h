@@ -37,8 +37,11 @@ constexpr float kNoLogit2 = kNoLogit * 1.4426950408889634f;
 // Correction of the tensor cores' rounding towards zero: n additions make a sum
 // too small by kAddLoss n of itself (see head_tc.cu)
 constexpr double kAddLoss = 1.45e-8;
-// q below this (p = 2^-100) does not fit the relative dlogits (see k_head_scale)
-constexpr float kLeastQ = -69.3f;
+// A chunk with a row whose q is below this takes dlogits relative to the running
+// maximum instead of to the given token (see k_head_scale): bf16 would hold
+// p_v / p_tok up to e^88, but g p_tok h has to stay a normal number as well, and with
+// p_tok >= e^-40 it does for every |g h| above 3e-21.
+constexpr float kLeastQ = -40.f;
 
 struct PlanParams {
     const uint8_t* mask;    // nullptr: every row counts

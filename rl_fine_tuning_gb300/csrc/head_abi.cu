@@ -73,9 +73,11 @@ bool head_layout(const grpo_shape& s, int op, int dw_f32, HeadLayout* o) {
     o->n_ntiles = (s.V + kBN - 1) / kBN;
     o->n_vt = (s.V + kBM - 1) / kBM;
     o->one_launch = has_backward(op) && static_cast<double>(o->R) * s.V * s.d <= kOneLaunchMax;
-    // splits: at most kHeadSplitsMax, and at least what 64 tiles a split give
+    // splits: at most kHeadSplitsMax (half of that with many row tiles, whose units are many anyway), and at
+    // least what 64 tiles a split give
     const int least = (o->n_ntiles + 63) / 64;
-    o->S = o->n_ntiles < kHeadSplitsMax ? o->n_ntiles : least > kHeadSplitsMax ? least : kHeadSplitsMax;
+    const int splits = o->R > 16 * kBM ? kHeadSplitsMax / 2 : kHeadSplitsMax;
+    o->S = o->n_ntiles < splits ? o->n_ntiles : least > splits ? least : splits;
     o->V_pad = (s.V + 63) / 64 * 64;
     o->nc32 = ((s.V + 31) / 32 + 7) / 8 * 8;
     // dH in units of 512 columns where d is whole units and a full chunk has two for every SM pair: 4.50

@@ -716,8 +716,7 @@ cudaError_t launch_head_dlogits(const HeadChunkParams& p, float* oscale, bool bf
 // s = sum of A over the other columns, p_tok = 1 / (1 + s) and
 //   dS_v = g (onehot - p_v) = f A_v  with  f = -g p_tok  and  A_tok = -s.
 // f is a factor of the row: dH's epilogue applies it, and for dW, where rows are
-// summed, the rows of h carry it.  A is rounded once to bf16 (any exponent that
-// q >= kLeastQ leaves is in range), f h once more.  The row's largest entry is
+// summed, the rows of h carry it.  A is rounded once to bf16, f h once more.  The row's largest entry is
 // the token's: f is taken as -g (1 - p_tok) / A_tok with A_tok as rounded, so
 // that entry is exact and dH has one rounding less than with the pass.  On 4.9K
 // rows of a 152K vocabulary at d = 1536 this kernel and the empty fallback take

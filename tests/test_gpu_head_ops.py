@@ -626,3 +626,19 @@ def test_large_chunks(dt, N, d, V, share, cr, dw_f32):
     eH, eW = np.abs(host(dH)[keep] - 32 * rH), np.abs(host(dW) - 32 * rW)
     assert np.all(eH <= R.grad_bound(32 * rH, 32 * aH, dt, dt, qe, 32)) and not host(dH)[mask == 0].any()
     assert np.all(eW <= R.grad_bound(32 * rW, 32 * aW, dt, "f32" if dw_f32 else dt, qe, 32))
+
+
+@pytest.mark.parametrize("size", [1e-12, 1e6])
+def test_relative_dlogits_scale_with_their_input(size):
+    """Tokens down to q of about -38, and d loss / d q of any size: row factors and relative dlogits stay in bf16's range."""
+    c = far_case(1, 1, 250, 70001, 0, 0, 24)
+    W = c.W.float().cpu()
+    for n, t in enumerate(c.P.rows[::10]):
+        o = (int(c.tok[t]) + 29) % 70001
+        c.h[t] = ((5.0 + 1.4 * n) * W[o] / float(W[o] @ W[o])).to(torch.bfloat16).cuda()
+    c.P.h = c.h.double().cpu().numpy()
+    q, _, lp = R.logp_entropy(c.P)
+    assert -42 < q.min() < -30
+    dq = (size * c.rng.normal(size=250)).astype(np.float32)
+    dH, dW = c.logp_bwd(torch.from_numpy(dq).cuda(), 1.0 / size)
+    check_grads(c, dH, dW, clean(dq, c.P.mask), lp, 1.0 / size)
