@@ -28,6 +28,7 @@ constexpr int kHeadChunkTiles = 76;    // default rows per chunk, in tiles of 12
 constexpr int kDhSlotsMax = 304;      // 256 x 256 partial tiles of dH (4 per SM pair, 80 MB)
 constexpr int kDhWideSlotsMax = 256;  // 256 x 512 ones
 constexpr int kFewRows = 32;        // rows of the few-row kernel
+constexpr int kFewCtas = 256;          // most CTAs of the few-row kernel
 constexpr int kFewVocab = 128;      // vocabulary rows per tile of the few-row kernel
 // what stands for a logit that does not count (the given token's own, columns
 // past V): finite, so no inf - inf can form, far below every logit, and a

@@ -116,7 +116,7 @@ bool head_layout(const grpo_shape& s, int op, int dw_f32, HeadLayout* o) {
     o->pair_ell = take(op == GRPO_OP_PAIR ? static_cast<size_t>(s.n_groups) * 8 : 0);
     o->hc = take(R * s.d * 2);
     size_t part = R * 2 * o->S * 16;
-    const size_t few = static_cast<size_t>(kFewRows) * 256 * 16;   // the few-row kernel: one partial per row and CTA
+    const size_t few = static_cast<size_t>(kFewRows) * kFewCtas * 16;   // the few-row kernel: one partial per row and CTA
     if (op == GRPO_OP_LOGPROBS && part < few) part = few;
     o->part = take(part);
     o->rowf = o->mx = o->ds = o->hct = o->dh_part = o->dw_acc = off;
@@ -231,7 +231,7 @@ int run_few(const HeadCall& c, const HeadLayout& L, const DeviceInfo& dev, cudaS
     p.n_tiles = (s.V + kFewVocab - 1) / kFewVocab;
     p.status = c.status;
     int grid = p.n_tiles < dev.sm_count ? p.n_tiles : dev.sm_count;
-    if (grid > 256) grid = 256;   // the partials' room
+    if (grid > kFewCtas) grid = kFewCtas;
     HEAD_LAUNCH(GRPO_PROF_GATHER,
                 launch_few_prep(p, static_cast<const uint16_t*>(c.h), static_cast<const uint16_t*>(c.W), bf16,
                                 reinterpret_cast<double*>(w + L.zt), st));

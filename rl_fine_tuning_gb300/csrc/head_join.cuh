@@ -16,24 +16,20 @@ struct RowSum {
     float ent;
 };
 
-__device__ __forceinline__ RowSum join_row(const float4* part, int S2, int lane, double zt) {
-    constexpr double kLog2eD = 1.4426950408889634074, kLn2D = 0.69314718055994530942;
-    float m = kNoLogit2;
-    for (int k = lane; k < S2; k += 32) m = fmaxf(m, __ldcg(part + k).x);
+__device__ __forceinline__ float warp_max(float m) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float s = 0.f, u = 0.f;
-    for (int k = lane; k < S2; k += 32) {
-        const float4 ps = __ldcg(part + k);
-        const float f = exp2f(ps.x - m);
-        s = fmaf(ps.y, f, s);
-        u = fmaf(ps.z, f, u);
-    }
+    return m;
+}
+
+__device__ __forceinline__ float warp_sum(float s) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        u += __shfl_xor_sync(0xffffffffu, u, o);
-    }
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+__device__ __forceinline__ RowSum finish_row(float m, float s, float u, double zt) {
+    constexpr double kLog2eD = 1.4426950408889634074, kLn2D = 0.69314718055994530942;
     RowSum r;
     float mean;   // E[z]
     const double dm = static_cast<double>(m) - zt * kLog2eD;
@@ -53,6 +49,41 @@ __device__ __forceinline__ RowSum join_row(const float4* part, int S2, int lane,
     const float ent = static_cast<float>(r.lse - static_cast<double>(mean));
     r.ent = ent < 0.f ? 0.f : ent;
     return r;
+}
+
+__device__ __forceinline__ RowSum join_row(const float4* part, int S2, int lane, double zt) {
+    float m = kNoLogit2;
+    for (int k = lane; k < S2; k += 32) m = fmaxf(m, __ldcg(part + k).x);
+    m = warp_max(m);
+    float s = 0.f, u = 0.f;
+    for (int k = lane; k < S2; k += 32) {
+        const float4 ps = __ldcg(part + k);
+        const float f = exp2f(ps.x - m);
+        s = fmaf(ps.y, f, s);
+        u = fmaf(ps.z, f, u);
+    }
+    return finish_row(m, warp_sum(s), warp_sum(u), zt);
+}
+
+// The same for at most 32 kPer partials, read once: all loads in flight together
+template <int kPer>
+__device__ __forceinline__ RowSum join_row_once(const float4* part, int S2, int lane, double zt) {
+    float4 v[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+        v[j] = lane + 32 * j < S2 ? __ldcg(part + lane + 32 * j) : make_float4(kNoLogit2, 0.f, 0.f, 0.f);
+    float m = kNoLogit2;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) m = fmaxf(m, v[j].x);
+    m = warp_max(m);
+    float s = 0.f, u = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const float f = exp2f(v[j].x - m);
+        s = fmaf(v[j].y, f, s);
+        u = fmaf(v[j].z, f, u);
+    }
+    return finish_row(m, warp_sum(s), warp_sum(u), zt);
 }
 
 // The same from sums relative to the given token's logit, part.x the fp32 value

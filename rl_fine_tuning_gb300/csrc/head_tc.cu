@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool on = !p.mask || p.mask[n] != 0;
         const bool ok = tok >= 0 && tok < p.V;
         RowSum r{0.0, 0.0, 0.f};
-        if (on && ok) r = join_row(p.part + static_cast<int64_t>(n) * n_cta, n_cta, lane, p.zt[n]);
+        if (on && ok) r = join_row_once<kFewCtas / 32>(p.part + static_cast<int64_t>(n) * n_cta, n_cta, lane, p.zt[n]);
         if (lane == 0) {
             if (on && !ok) atomicCAS(status, 0, GRPO_ERR_SHAPE);
             p.logp[n] = static_cast<float>(r.q);
