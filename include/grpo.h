@@ -330,7 +330,14 @@ int grpo_loss_fwd_noalloc(const void* h_pol, const void* h_ref, const void* W, c
  *
  * shape->objective has to be GRPO_OBJ_GRPO for grpo_clip_loss_*; the others
  * ignore it, and all but grpo_clip_loss_* ignore loss_mode.  chunk_rows is the
- * rows per chunk, as for grpo_loss_fwd_bwd. */
+ * rows per chunk, as for grpo_loss_fwd_bwd.
+ *
+ * Data-parallel shards: a loss is a mean over what its call counts (rows or
+ * completions of the mask; pairs), so the batch's loss is the sum over shards of
+ * loss * c, and its gradients come with loss_scale times c, where
+ * c = the shard's count / the batch's (grpo_shard_counts; a shard without rows
+ * contributes 0 with any loss_scale).  grpo_logprobs_bwd is a sum over rows and
+ * needs no weight. */
 
 /* Operators, for grpo_policy_workspace_bytes. */
 enum { GRPO_OP_LOGPROBS = 0, GRPO_OP_LOGPROBS_BWD = 1, GRPO_OP_CLIP = 2, GRPO_OP_PAIR = 3 };

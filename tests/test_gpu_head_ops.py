@@ -332,6 +332,79 @@ def test_results_do_not_depend_on_the_workspace_or_the_stream():
         assert torch.equal(x, y) and torch.equal(x, z)
 
 
+def test_calls_on_two_streams_at_once():
+    """Two clipped steps and a few-row call in flight together, each with its own workspace: the bits of the calls alone."""
+    cs = [Case(2, 3, 120, 192, 600, "bf16", "ragged", seed=s, chunk_rows=256) for s in (13, 14)]
+    few = Case(1, 4, 1, 128, 400, "bf16", "all", seed=15)
+    opts = rg.clip_opts()
+    ins = [[torch.from_numpy(x).cuda() for x in c.old_ref()] + [torch.randn(6, device="cuda")] for c in cs]
+    outs = [[c.ws("clip"), c.f32(1), *c.grads(), c.f32(len(c.tok), 3)] for c in cs]
+    fws, fq = few.ws("logp"), few.f32(4)
+
+    def call(k):
+        c, (old, ref, adv), (ws, loss, dH, dW, st) = cs[k], ins[k], outs[k]
+        rg.grpo_clip_loss_fwd_bwd(c.h, c.W, c.tok, c.mask, adv, old, ref, c.shape, opts, 1.0, ws, loss, dH, dW, c.inf, st,
+                                  c.status)
+
+    def call_few():
+        rg.grpo_logprobs(few.h, few.W, few.tok, None, few.shape, 1.0, fws, fq, None, few.status)
+
+    want = []
+    for k in (0, 1):
+        call(k)
+        torch.cuda.synchronize()
+        want.append([x.clone() for x in outs[k][1:]])
+    call_few()
+    torch.cuda.synchronize()
+    want_q = fq.clone()
+    for x in (*outs[0], *outs[1], fws, fq):
+        x.zero_()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k]):
+                call(k)
+        with torch.cuda.stream(streams[2]):
+            call_few()
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        assert all(torch.equal(x, y) for x, y in zip(outs[k][1:], want[k]))
+        assert int(cs[k].status) == 0
+    assert torch.equal(fq, want_q) and int(few.status) == 0
+
+
+@pytest.mark.parametrize("loss_mode", [0, 1])
+def test_shards_add_up_to_the_batch(loss_mode):
+    """Prompt groups on two shards, loss and gradients weighted by the shard's share of what the mean counts."""
+    c = Case(4, 2, 60, 128, 400, "bf16", "ragged", seed=16, loss_mode=loss_mode)
+    old, ref = (torch.from_numpy(x).cuda() for x in c.old_ref())
+    adv = torch.randn(8, device="cuda")
+    opts = rg.clip_opts(clip_high=0.28, dw_f32=True)
+    loss, _, dH, dW = c.clip(adv, old, ref, opts)
+    counts = lambda m: (m.view(-1, 60).any(1) if loss_mode else m).ne(0).sum().item()  # noqa: E731
+    total, sum_loss, sum_dW, rows = counts(c.mask), 0.0, torch.zeros_like(dW), []
+    shape = rg.make_shape(2, 2, 60, 128, 400, CODE["bf16"], beta=c.beta, loss_mode=loss_mode)
+    ws = torch.full((rg.grpo_policy_workspace_bytes(shape, "clip", True),), 255, dtype=torch.uint8, device="cuda")
+    for r in (slice(0, 240), slice(240, 480)):
+        h, tok, mask = c.h[r].contiguous(), c.tok[r].contiguous(), c.mask[r].contiguous()
+        w = counts(mask) / total
+        part, gH, gW = c.f32(1), torch.empty_like(h), torch.empty_like(dW)
+        rg.grpo_clip_loss_fwd_bwd(h, c.W, tok, mask, adv[r.start // 60:r.stop // 60].contiguous(), old[r].contiguous(),
+                                  ref[r].contiguous(), shape, opts, w, ws, part, gH, gW, c.inf, None, c.status)
+        torch.cuda.synchronize()
+        assert int(c.status) == 0 and int(c.inf) == 0
+        sum_loss += w * part.item()
+        sum_dW += gW
+        rows.append(gH)
+    # loss: fp32 sums of terms of order 1, whose q differ by fp32 roundings of logits below 64 (4e-6 each); gradients: two
+    # 16-bit roundings on each side (dlogits and the output, or dlogits and the scaled row)
+    assert abs(sum_loss - loss.item()) <= 1e-5 * (1 + abs(loss.item()))
+    for got, want in ((torch.cat(rows).float(), dH.float()), (sum_dW, dW)):
+        assert (got - want).norm() <= 4 * 2 ** -8 * want.norm()
+
+
 def test_graph_replays_on_new_inputs():
     c = Case(2, 2, 90, 128, 400, "bf16", "ragged", seed=10, chunk_rows=128, beta=0.1)
     c2 = Case(2, 2, 90, 128, 400, "bf16", "holes", seed=11, chunk_rows=128, beta=0.1)
