@@ -598,9 +598,11 @@ cudaError_t launch_loss(const LossParams& l, const int* counts, cudaStream_t st)
 //   dS = g (onehot(tok) - E 2^(m - lse log2 e)),   m the base of the column's group of 32
 // rounded to the input type, which the two GEMMs need (E's rounding, 2^-12, is
 // small beside bf16's).  fp16 has no exponent range to
-// spare: there g is divided by the power of two above the chunk's largest |g|
-// and multiplied by 2^14, and the GEMMs' epilogues undo it (oscale), whatever
-// the caller's loss scale is.  Reads and writes the chunk once: bound by HBM.
+// spare: there g is multiplied by the power of two 2^e that takes the chunk's
+// largest |g| to 2^13 .. 2^14, and the GEMMs' epilogues undo it (oscale), whatever
+// the caller's loss scale is.  e reaches 162 (a saturated preference pair's g is
+// 1e-36, fp32 goes down to 2^-149), where 2^e is no fp32 number: ldexpf applies it.
+// Reads and writes the chunk once: bound by HBM.
 // One row by one block; true if a value is not finite.
 template <bool kBf16>
 __device__ __forceinline__ bool dlogits_row(const HeadChunkParams& p, int slot, int tok, float lse, float q, float coef) {
@@ -644,13 +646,12 @@ __global__ void __launch_bounds__(kTransformThreads) k_head_dlogits(const HeadCh
     const int2 cbn = chunk_bounds(p.counts, p.cb, p.chunk);
     const int c0 = cbn.x, n_c = cbn.y;
     if (n_c == 0 || (p.far && p.far[p.chunk] == 0)) return;
-    float up = 1.f;
+    int e = 0;
     if (!kBf16) {
         const float gm = __uint_as_float(p.gmax[p.gmax_chunk]);
-        const float G = gm > 0.f && gm < 1e38f ? ldexpf(1.f, ilogbf(gm) + 1) : 1.f;
-        up = 16384.f / G;
+        if (gm > 0.f && isfinite(gm)) e = 13 - ilogbf(gm);
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) oscale[p.chunk] = p.loss_scale / up;
+    if (blockIdx.x == 0 && threadIdx.x == 0) oscale[p.chunk] = kBf16 ? p.loss_scale : ldexpf(p.loss_scale, -e);
     const int n_fill = min(p.R, (n_c + kBM - 1) / kBM * kBM);
     bool bad = false;
     for (int slot = blockIdx.x; slot < n_fill; slot += gridDim.x) {
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(kTransformThreads) k_head_dlogits(const HeadCh
         const int t = p.rows[c0 + slot];
         if (!GRPO_DCHECK(t >= 0 && t < p.N, p.status)) continue;
         const int tok = p.tokens[t];
-        const float coef = tok >= 0 && tok < p.V ? up * p.gco[t] : 0.f;
+        const float coef = tok >= 0 && tok < p.V ? (kBf16 ? p.gco[t] : ldexpf(p.gco[t], e)) : 0.f;
         bad |= dlogits_row<kBf16>(p, slot, tok, p.lse[t], p.logp[t], coef);
     }
     if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(p.found_inf, 1);

@@ -1,0 +1,67 @@
+"""The head operators where they can go wrong, beyond their ordinary range."""
+import numpy as np
+import pytest
+
+import head_bounds as B
+import head_reference as R
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+import rl_fine_tuning_gb300 as rg  # noqa: E402
+from test_gpu_head_ops import Case, clean, host  # noqa: E402
+
+
+def check(c, dH, dW, g, lp, scale, dw_f32=False, relative=False):
+    assert int(c.status) == 0 and int(c.inf) == 0
+    q_err = R.logp_bound(c.P)[c.P.mask].max()
+    rH, bH, rW, bW = B.grad_bounds(c.P, g, lp, c.dtype, relative, "f32" if dw_f32 else c.dtype, q_err, scale)
+    eH, eW = np.abs(host(dH) - rH), np.abs(host(dW) - rW)
+    assert np.all(eH <= bH), ("dH", np.max(eH / bH))
+    assert np.all(eW <= bW), ("dW", np.max(eW / bW))
+    assert not host(dH)[~c.P.mask].any()
+    return rH, bH, rW, bW
+
+
+# ---------------------------------------------------------------- gradients near the end of fp32's range
+
+@pytest.mark.parametrize("dt,size", [("fp16", 1e-30), ("fp16", 1e-36), ("fp16", 2e-38), ("bf16", 1e-30)])
+def test_tiny_gradients_of_given_size(dt, size):
+    """d loss / d q near the smallest fp32 numbers, brought back by the loss scale: as exact as any other."""
+    c = Case(1, 2, 60, 128, 500, dt, "ragged", seed=40)
+    dq = (size * c.rng.normal(size=len(c.tok))).astype(np.float32)
+    scale = float(np.float32(0.25 / size))
+    dH, dW = c.logp_bwd(torch.from_numpy(dq).cuda(), scale, True)
+    rH, bH, rW, bW = check(c, dH, dW, clean(dq, c.P.mask), R.logp_entropy(c.P)[2], scale, True)
+    assert B.shows_loss(rH[c.P.rows], bH[c.P.rows])
+    dH, dW = c.logp_bwd(torch.from_numpy(dq).cuda(), 1.0)          # unscaled: far below fp16, no overflow on the way
+    assert int(c.inf) == 0 and (dt == "bf16" or not (dH.any() or dW.any()))
+
+
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("margin", [70.0, 78.0, 84.0, 88.0, 95.0])
+@pytest.mark.parametrize("cr", [0, 128])
+def test_saturated_pairs(dt, margin, cr):
+    """A preferred completion far ahead: sigmoid(-m) down to the end of fp32, gradients near 0 and finite."""
+    L = 80
+    c = Case(2, 2, L, 128, 300, dt, "all", seed=41, chunk_rows=cr, beta=1.0)
+    q = R.logp_entropy(c.P)[0]
+    sign = np.where(np.arange(4 * L) // L % 2 == 0, 1.0, -1.0)
+    ref = (q - sign * margin / (2 * L)).astype(np.float32)         # each completion's S is +- margin / 2
+    loss, _, st, dH, dW = c.pair(torch.from_numpy(ref).cuda(), rg.pair_opts(dw_f32=True))
+    assert int(c.status) == 0 and int(c.inf) == 0
+    rl, rs, g, lp = R.pair_loss(c.P, ref.astype(np.float64), c.beta)
+    # S: fp32 numbers of q, each off by logp_bound; d sigmoid(-m) / dm is at most itself
+    rel = 2 * L * R.logp_bound(c.P).max()
+    assert np.all(np.abs(host(st)[:, 2] - rs[:, 2]) <= rel + 1e-5)
+    assert abs(float(loss) - rl) <= (np.expm1(rel + 1e-5) + 1e-5) * rl + 1e-44
+    rH, rW, aH, aW = R.gradients(c.P, g, lp)
+    f = np.expm1(rel + 1e-5) + (2.0 ** -6 if dt == "bf16" else 2.0 ** -9)
+    # expf(m) is infinite from m = 88.7 on: 0 where sigmoid(-m) is below 3e-39.  bf16 dlogits carry no scale of their own:
+    # entries and products below the smallest normal number may become 0.
+    low = 3e-39 if dt == "fp16" else 2.0 ** -125
+    assert np.all(np.abs(host(dW) - rW) <= f * aW + low * (1 + np.abs(c.P.h)).sum(0))
+    assert np.all(np.abs(host(dH) - rH) <= f * aH + R.TINY[dt] + low * (1 + np.abs(c.P.W)).sum(0))
