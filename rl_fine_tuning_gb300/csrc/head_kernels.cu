@@ -662,7 +662,11 @@ __global__ void __launch_bounds__(kTransformThreads) k_head_dlogits(const HeadCh
         const int t = p.rows[c0 + slot];
         if (!GRPO_DCHECK(t >= 0 && t < p.N, p.status)) continue;
         const int tok = p.tokens[t];
-        const float coef = tok >= 0 && tok < p.V ? (kBf16 ? p.gco[t] : ldexpf(p.gco[t], e)) : 0.f;
+        if (tok < 0 || tok >= p.V) {   // no lse to go by: 0 times the exponentials of large logits would be NaN
+            zero_row(p, slot);
+            continue;
+        }
+        const float coef = kBf16 ? p.gco[t] : ldexpf(p.gco[t], e);
         bad |= dlogits_row<kBf16>(p, slot, tok, p.lse[t], p.logp[t], coef);
     }
     if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(p.found_inf, 1);
@@ -691,7 +695,8 @@ __global__ void __launch_bounds__(kTransformThreads) k_merge_dlogits(const HeadM
         }
         __syncthreads();
         const RowGrad r = s_row;
-        bad |= dlogits_row<true>(p, slot, r.tok, r.lse, r.q, r.tok >= 0 ? r.g : 0.f);
+        if (r.tok >= 0) bad |= dlogits_row<true>(p, slot, r.tok, r.lse, r.q, r.g);
+        else zero_row(p, slot);
         __syncthreads();   // s_row is read
     }
     if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(p.found_inf, 1);

@@ -65,3 +65,44 @@ def test_saturated_pairs(dt, margin, cr):
     low = 3e-39 if dt == "fp16" else 2.0 ** -125
     assert np.all(np.abs(host(dW) - rW) <= f * aW + low * (1 + np.abs(c.P.h)).sum(0))
     assert np.all(np.abs(host(dH) - rH) <= f * aH + R.TINY[dt] + low * (1 + np.abs(c.P.W)).sum(0))
+
+
+# ---------------------------------------------------------------- rows with a bad token
+
+def with_bad_tokens(c, rows):
+    """Tokens out of range in `rows` on the device; the reference problem keeps good ones."""
+    c.tok = c.tok.clone()
+    for i, t in enumerate(rows):
+        c.tok[t] = -1 if i % 2 else c.P.W.shape[0]
+    bad = np.zeros(len(c.P.tokens), bool)
+    bad[list(rows)] = True
+    return bad & c.P.mask
+
+
+@pytest.mark.parametrize("dt,V,cr,far", [("fp16", 300, 0, 0), ("bf16", 300, 0, 0), ("fp16", 300, 128, 0),
+                                         ("bf16", 70001, 0, 0), ("bf16", 70001, 0, 1)])
+def test_a_bad_token_beside_large_logits(dt, V, cr, far):
+    """Logits of 150 and more in the row with the bad token: it contributes nothing, and nothing overflows."""
+    c = Case(1, 2, 100, 64, V, dt, "all", seed=42, chunk_rows=cr)
+    t = 7
+    o = int(c.tok[t])
+    W = c.W[o].float()
+    c.h[t] = (160.0 * W / float(W @ W)).to(c.h.dtype)
+    if far:                # another row's token is improbable: the chunk takes its dlogits relative to the maximum
+        W = c.W[(int(c.tok[20]) + 9) % V].float()
+        c.h[20] = (70.0 * W / float(W @ W)).to(c.h.dtype)
+    c.P.h = host(c.h)
+    assert R.logits(c.P)[t].max() > 150 and (R.logp_entropy(c.P)[0].min() < -45) == bool(far)
+    bad = with_bad_tokens(c, [t])
+    dq = np.ones(200, np.float32)
+    dH, dW = c.logp_bwd(torch.from_numpy(dq).cuda(), 1.0, True)
+    assert int(c.status) == 2 and int(c.inf) == 0 and not dH[t].any()
+    g = np.where(bad, 0.0, 1.0)
+    q_err = np.delete(R.logp_bound(c.P), t).max()
+    rH, bH, rW, bW = B.grad_bounds(c.P, g, R.logp_entropy(c.P)[2], dt, V > 1000 and not far, "f32", q_err, 1.0)
+    assert np.all(np.abs(host(dH) - rH) <= bH) and np.all(np.abs(host(dW) - rW) <= bW)
+    if dt == "bf16":       # the same through the clipped loss
+        old = torch.from_numpy(R.logp_entropy(c.P)[0].astype(np.float32)).cuda()
+        loss, st, dH, dW = c.clip(torch.ones(2, device="cuda"), old, old, rg.clip_opts())
+        assert int(c.status) == 2 and int(c.inf) == 0 and not dH[t].any() and not st[t].any()
+        assert bool(torch.isfinite(dW.float()).all()) and bool(torch.isfinite(loss))
