@@ -314,7 +314,8 @@ int grpo_loss_fwd_noalloc(const void* h_pol, const void* h_ref, const void* W, c
  * tokens [N] int32; mask [N] uint8, nonzero = the row counts (0 in every row of
  * a completion leaves it empty); workspace of grpo_policy_workspace_bytes bytes,
  * 256-byte aligned; status as everywhere (a token id outside [0, V) in a
- * masked-in row sets GRPO_ERR_SHAPE, and that row contributes 0); fixed
+ * masked-in row sets GRPO_ERR_SHAPE, and that row contributes 0 to sums and
+ * gradients, though it stays among the rows that a mean divides by); fixed
  * reduction orders and no floating-point atomics, so every output is
  * bitwise reproducible; nothing depends on host knowledge of the data, so calls
  * can be captured into a CUDA graph.  With z = h W^T / temperature,

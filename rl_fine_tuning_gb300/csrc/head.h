@@ -166,6 +166,7 @@ struct PairParams {
     const int* off;
     const int* pb;          // nullptr: every pair
     const int* rows;
+    const int* tokens;
     const float* logp;
     const float* logp_ref;
     float* gco;
@@ -173,7 +174,7 @@ struct PairParams {
     double* pair_ell;       // [n_pairs]
     float* pair_stats;      // nullable [n_pairs x 4]
     float beta, smoothing;
-    int kind, length_mean, n_pairs, chunk;
+    int kind, length_mean, n_pairs, chunk, V;
     int64_t N;
     int* status;
 };

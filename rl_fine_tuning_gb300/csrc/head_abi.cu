@@ -414,6 +414,7 @@ struct HeadRun {
         p.off = at<int>(L.off);
         p.pb = chunk < 0 ? nullptr : at<int>(L.pb);
         p.rows = at<int>(L.rows);
+        p.tokens = c.tokens;
         p.logp = c.logp ? c.logp : at<float>(L.q);
         p.logp_ref = c.logp_ref;
         p.gco = c.backward ? at<float>(L.gco) : nullptr;
@@ -426,6 +427,7 @@ struct HeadRun {
         p.length_mean = c.pair.length_mean;
         p.n_pairs = s.n_groups;
         p.chunk = chunk < 0 ? 0 : chunk;
+        p.V = s.V;
         p.N = L.N;
         p.status = c.status;
         HEAD_LAUNCH(GRPO_PROF_MERGE, launch_pair_coef(p, st));

@@ -514,7 +514,8 @@ cudaError_t launch_head_merge(const HeadMergeParams& p, cudaStream_t st) {
 // One block per pair of completions (2i preferred, 2i + 1 not):
 //   S = sum (or mean) over a completion's rows of q - p,   m = beta (S_2i - S_2i+1)
 // and d loss / d q of their rows.  Sums in fp64 in a fixed order.  Pairs
-// without a row are left out of the mean.  8 us (latency).
+// without a row are left out of the mean.  A row whose token is out of range adds
+// 0 to S and gets no gradient.  8 us (latency).
 __global__ void __launch_bounds__(256) k_pair_coef(const PairParams p) {
     __shared__ double sh[256];
     __shared__ float s_g[2];
@@ -527,8 +528,9 @@ __global__ void __launch_bounds__(256) k_pair_coef(const PairParams p) {
         double acc = 0.0;
         for (int i = b[c] + threadIdx.x; i < b[c + 1]; i += 256) {
             const int t = p.rows[i];
-            if (GRPO_DCHECK(t >= 0 && t < p.N, p.status))
-                acc += static_cast<double>(p.logp[t]) - static_cast<double>(p.logp_ref[t]);
+            if (!GRPO_DCHECK(t >= 0 && t < p.N, p.status)) continue;
+            const int tok = p.tokens[t];
+            if (tok >= 0 && tok < p.V) acc += static_cast<double>(p.logp[t]) - static_cast<double>(p.logp_ref[t]);
         }
         S[c] = block_sum(acc, sh);
         if (p.length_mean && b[c + 1] > b[c]) S[c] /= b[c + 1] - b[c];
@@ -573,7 +575,9 @@ __global__ void __launch_bounds__(256) k_pair_coef(const PairParams p) {
     __syncthreads();
     for (int i = b[0] + threadIdx.x; i < b[2]; i += 256) {
         const int t = p.rows[i];
-        if (GRPO_DCHECK(t >= 0 && t < p.N, p.status)) p.gco[t] = i < b[1] ? s_g[0] : s_g[1];
+        if (!GRPO_DCHECK(t >= 0 && t < p.N, p.status)) continue;
+        const int tok = p.tokens[t];
+        p.gco[t] = tok >= 0 && tok < p.V ? (i < b[1] ? s_g[0] : s_g[1]) : 0.f;
     }
 }
 

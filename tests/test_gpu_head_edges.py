@@ -106,3 +106,56 @@ def test_a_bad_token_beside_large_logits(dt, V, cr, far):
         loss, st, dH, dW = c.clip(torch.ones(2, device="cuda"), old, old, rg.clip_opts())
         assert int(c.status) == 2 and int(c.inf) == 0 and not dH[t].any() and not st[t].any()
         assert bool(torch.isfinite(dW.float()).all()) and bool(torch.isfinite(loss))
+
+
+@pytest.mark.parametrize("dt,V,cr", [("bf16", 300, 0), ("bf16", 300, 128), ("fp16", 300, 0), ("bf16", 70001, 0)])
+@pytest.mark.parametrize("mean", [False, True])
+def test_bad_tokens_in_a_pair_contribute_nothing(dt, V, cr, mean):
+    """S counts 0 for such a row (not minus its reference log-prob); with length_mean it stays in the divisor."""
+    c = Case(3, 2, 70, 64, V, dt, "all", seed=43, chunk_rows=cr, beta=2.0 if mean else 0.05)
+    bad = with_bad_tokens(c, [3, 69, 150, 151, 152, 153])
+    bad[280:350] = True                                  # a completion of bad tokens alone
+    c.tok[280:350] = V + 5
+    q = R.logp_entropy(c.P)[0]
+    ref = (q - 0.3 * c.rng.normal(size=len(q))).astype(np.float32)
+    rref = np.where(bad, q, ref)                         # the reference: q - logp_ref = 0 there
+    ref[bad] = -25.0
+    opts = rg.pair_opts(length_mean=mean, dw_f32=True)
+    loss, qq, st, dH, dW = c.pair(torch.from_numpy(ref).cuda(), opts)
+    rl, rs, g, lp = R.pair_loss(c.P, rref, c.beta, length_mean=mean)
+    assert int(c.status) == 2 and int(c.inf) == 0
+    assert not host(qq)[bad].any() and not host(dH)[bad].any()
+    S_err = (1 if mean else 70) * (R.logp_bound(c.P).max() + 2e-6)
+    m_err = 2 * c.beta * S_err + 1e-6 * max(1.0, np.abs(rs).max())
+    assert np.all(np.abs(host(st)[:, :3] - rs[:, :3]) <= m_err)
+    assert np.all(np.abs(host(st)[:, 3] - rs[:, 3]) <= m_err + 1e-6) and abs(float(loss) - rl) <= m_err + 1e-6
+    g = np.where(bad, 0.0, g)
+    rH, bH, rW, bW = B.grad_bounds(c.P, g, lp, dt, V > 1000, "f32", m_err, 1.0)
+    assert np.all(np.abs(host(dH) - rH) <= bH) and np.all(np.abs(host(dW) - rW) <= bW)
+    l2, q2, s2 = c.pair(torch.from_numpy(ref).cuda(), opts, bwd=False)
+    assert torch.equal(l2, loss) and torch.equal(q2, qq) and torch.equal(s2, st)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_bad_tokens_in_the_clipped_loss_contribute_nothing(dt):
+    """Their term is 0; they stay in the number of rows that the mean divides by."""
+    c = Case(2, 2, 60, 64, 200, dt, "ragged", seed=44)
+    old, ref = c.old_ref()
+    bad = with_bad_tokens(c, c.P.rows[::9])
+    adv = c.rng.normal(size=4).astype(np.float32)
+    t = lambda x: torch.from_numpy(x).cuda()  # noqa: E731
+    loss, st, dH, dW = c.clip(t(adv), t(old), t(ref), rg.clip_opts(clip_high=0.28, dw_f32=True))
+    assert int(c.status) == 2 and int(c.inf) == 0
+    keep = c.P.mask & ~bad
+    n_all, n_good = c.P.mask.sum(), keep.sum()
+    mask, c.P.mask = c.P.mask, keep
+    rl, rs, g, lp = R.clip_loss(c.P, adv, clean(old, mask), clean(ref, mask), c.beta, 0.2, 0.28, False)
+    share = n_good / n_all
+    qb = R.logp_bound(c.P)
+    per = (np.abs(adv).max() * rs[:, 1].max() + c.beta * 6) * qb.max() + 2e-6
+    assert abs(float(loss) - share * rl) <= per
+    assert not host(st)[~keep].any() and np.all(np.abs(host(st)[:, 0] - rs[:, 0]) <= qb)
+    check_q = qb[keep].max()
+    rH, bH, rW, bW = B.grad_bounds(c.P, share * g, lp, dt, False, "f32", check_q, 1.0)
+    assert np.all(np.abs(host(dH) - rH) <= bH) and np.all(np.abs(host(dW) - rW) <= bW)
+    assert not host(dH)[~keep].any()
