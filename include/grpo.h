@@ -318,8 +318,8 @@ int grpo_loss_fwd_noalloc(const void* h_pol, const void* h_ref, const void* W, c
  * gradients, though it stays among the rows that a mean divides by); fixed
  * reduction orders and no floating-point atomics, so every output is
  * bitwise reproducible; nothing depends on host knowledge of the data, so calls
- * can be captured into a CUDA graph.  With z = h W^T / temperature,
- * q = z[token] - logsumexp(z).  Log-probs are fp32 numbers whose error stays at
+ * can be captured into a CUDA graph.  With z = h W^T / temperature (1e-6 to
+ * 1e20; others are refused with GRPO_ERR_SHAPE), q = z[token] - logsumexp(z).  Log-probs are fp32 numbers whose error stays at
  * fp32's: the tensor cores' partial sums are added in registers, and the given
  * token's logit is computed by itself.
  *
@@ -344,7 +344,7 @@ int grpo_loss_fwd_noalloc(const void* h_pol, const void* h_ref, const void* W, c
 enum { GRPO_OP_LOGPROBS = 0, GRPO_OP_LOGPROBS_BWD = 1, GRPO_OP_CLIP = 2, GRPO_OP_PAIR = 3 };
 
 /* Options of grpo_clip_loss_*.  grpo_clip_opts_init: temperature 1, clips 0.2.
- *   temperature : > 0; logits are divided by it
+ *   temperature : 1e-6 to 1e20; logits are divided by it
  *   clip_low    : in [0, 1]; clip_high: >= 0 (INFINITY: no upper clip)
  *   dw_f32      : dW is fp32 (1) or of type shape->dtype (0) */
 typedef struct {

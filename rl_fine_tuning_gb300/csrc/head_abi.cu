@@ -24,6 +24,12 @@ constexpr int64_t kRelativeMin = 1 << 22;
 // 44 us at 3e7, 112 against 118 at 1.6e10, 188 against 188 at 2e10, 435 against 420 at 5e10.
 constexpr double kOneLaunchMax = 2e10;
 
+// Temperatures between which the logits kernels' numbers hold.  Above, kNoLogit /
+// temperature, the stand-in for a column that does not count, would come near the
+// logits (at 1e30 it is -1.3).  Below, logits of 100 would pass 1e8, where a step of
+// fp32 is 8: an exponential relative to a rounded maximum can then leave fp16's range.
+constexpr float kLeastTemperature = 1e-6f, kMostTemperature = 1e20f;
+
 struct HeadLayout {
     size_t counts, off, cb, pb, dh_plan, lg_plan, gmax, far, oscale, rowf, rows, zt, lse, gco, ell, q, pair_ell, hc, part, mx, ds, hct, dh_part,
         dw_acc, total;
@@ -172,7 +178,7 @@ int head_validate(const HeadCall& c, HeadLayout* L) {
     const grpo_shape& s = *c.shape;
     if (!dtype_ok(s)) return GRPO_ERR_DTYPE;
     if (!head_layout(s, c.op, c.dw_f32, L)) return GRPO_ERR_SHAPE;
-    if (!(c.temperature > 0.f) || !std::isfinite(c.temperature) || !std::isfinite(1.f / c.temperature)) return GRPO_ERR_SHAPE;
+    if (!(c.temperature >= kLeastTemperature) || !(c.temperature <= kMostTemperature)) return GRPO_ERR_SHAPE;
     if (!c.h || !c.W || !c.tokens || !c.ws || !c.status) return GRPO_ERR_POINTER;
     if (!c.mask && c.mode != HEAD_LOGP) return GRPO_ERR_POINTER;
     if (!aligned(c.h, 16) || !aligned(c.W, 16) || !f32_ok(c.tokens) || !aligned(c.ws, 256) || !f32_ok(c.status))

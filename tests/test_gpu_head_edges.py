@@ -159,3 +159,22 @@ def test_bad_tokens_in_the_clipped_loss_contribute_nothing(dt):
     rH, bH, rW, bW = B.grad_bounds(c.P, share * g, lp, dt, False, "f32", check_q, 1.0)
     assert np.all(np.abs(host(dH) - rH) <= bH) and np.all(np.abs(host(dW) - rW) <= bW)
     assert not host(dH)[~keep].any()
+
+
+# ---------------------------------------------------------------- extreme temperatures
+
+@pytest.mark.parametrize("rows", [4, 60])
+@pytest.mark.parametrize("T", [1e-4, 1e4, 1e20])
+def test_extreme_temperatures(rows, T):
+    """Nearly argmax at one end, uniform at the other: the columns that do not count stay out of the sums."""
+    c = Case(1, 1, rows, 128, 257, "bf16", "all", T=T, seed=45)
+    q, e = c.logp()
+    assert int(c.status) == 0
+    rq, re, _ = R.logp_entropy(c.P)
+    qb = R.logp_bound(c.P) + 4e-7 * np.abs(R.logits(c.P)).max(1)      # the scale of the logits is an fp32 number
+    assert np.all(np.abs(host(q) - rq) <= qb)
+    if T > 1:
+        assert np.all(np.abs(host(e) - re) <= qb * (2 + np.log(257)) + 1e-6 * (1 + np.log(257)))
+        dq = np.ones(rows, np.float32)
+        dH, dW = c.logp_bwd(torch.from_numpy(dq).cuda(), T, True)
+        check(c, dH, dW, dq, R.logp_entropy(c.P)[2], T, True)
