@@ -144,7 +144,7 @@ struct HeadMergeParams {
     const int* rows;
     const int* tokens;
     const double* zt;
-    float* lse;
+    double* lse2;           // [N] logsumexp in base 2
     float* gco;
     float* ell;
     unsigned* gmax;
@@ -196,6 +196,8 @@ struct HeadChunkParams : ChunkParams {
     int dh_cols;            // columns of a dH unit: 256 or 512
     const int2* dh_plan;
     const float* logp;      // [N] q
+    const double* lse2;     // [N] logsumexp in base 2
+    const double* zt;       // [N] logit of the given token
     float* rowf;            // nullable: [R] factor of a dlogits row (relative dlogits)
     uint16_t* hct;          // [d x R]
     const uint16_t* hc;     // [R x d]

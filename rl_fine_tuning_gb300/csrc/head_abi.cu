@@ -31,7 +31,7 @@ constexpr double kOneLaunchMax = 2e10;
 constexpr float kLeastTemperature = 1e-6f, kMostTemperature = 1e20f;
 
 struct HeadLayout {
-    size_t counts, off, cb, pb, dh_plan, lg_plan, gmax, far, oscale, rowf, rows, zt, lse, gco, ell, q, pair_ell, hc, part, mx, ds, hct, dh_part,
+    size_t counts, off, cb, pb, dh_plan, lg_plan, gmax, far, oscale, rowf, rows, zt, lse2, gco, ell, q, pair_ell, hc, part, mx, ds, hct, dh_part,
         dw_acc, total;
     int64_t N;
     int n_seq, R, max_chunks, S, n_ntiles, n_vt, V_pad, nc32, slots, by_pair, relative, one_launch, dh_cols;
@@ -115,7 +115,7 @@ bool head_layout(const grpo_shape& s, int op, int dw_f32, HeadLayout* o) {
     o->oscale = take(mc * 4);
     o->rows = take(n * 4);
     o->zt = take(n * 8);
-    o->lse = take(n * 4);
+    o->lse2 = take(n * 8);
     o->gco = take(n * 4);
     o->ell = take(n * 4);
     o->q = take(n * 4);
@@ -376,7 +376,7 @@ struct HeadRun {
         p.rows = at<int>(L.rows);
         p.tokens = c.tokens;
         p.zt = at<double>(L.zt);
-        p.lse = at<float>(L.lse);
+        p.lse2 = at<double>(L.lse2);
         p.gco = at<float>(L.gco);
         p.ell = c.mode == HEAD_CLIP ? at<float>(L.ell) : nullptr;
         p.gmax = c.backward && !bf16 ? at<unsigned>(L.gmax) : nullptr;
@@ -461,7 +461,8 @@ struct HeadRun {
         p.oscale = at<float>(L.oscale);
         p.rows = at<int>(L.rows);
         p.tokens = c.tokens;
-        p.lse = at<float>(L.lse);
+        p.lse2 = at<double>(L.lse2);
+        p.zt = at<double>(L.zt);
         p.gco = at<float>(L.gco);
         p.mx = at<float>(L.mx);
         p.scale = 1.f;

@@ -427,12 +427,13 @@ constexpr int kHeadMergeThreads = 256;
 
 // One row's merge by one warp; lane 0 writes and returns what its dlogits need.
 struct RowGrad {
-    float g, lse, q;
+    double lse2;
+    float g, q;
     int tok;   // -1: nothing (a bad token id, reported here)
 };
 
 __device__ __forceinline__ RowGrad merge_row(const HeadMergeParams& p, int slot, int c0, int lane) {
-    RowGrad out{0.f, 0.f, 0.f, -1};
+    RowGrad out{0.0, 0.f, 0.f, -1};
     const int S2 = 2 * p.plan[p.chunk].x;
     const int t = p.rows[c0 + slot];
     if (!GRPO_DCHECK(t >= 0 && t < p.N, p.status)) return out;
@@ -468,7 +469,8 @@ __device__ __forceinline__ RowGrad merge_row(const HeadMergeParams& p, int slot,
         g *= w;
     }
     g *= p.inv_t;
-    p.lse[t] = static_cast<float>(r.lse);
+    const double lse2 = r.lse * 1.4426950408889634074;
+    p.lse2[t] = lse2;
     if (p.logp) p.logp[t] = q;
     if (p.entropy) p.entropy[t] = r.ent;
     if (p.stats) {
@@ -479,7 +481,7 @@ __device__ __forceinline__ RowGrad merge_row(const HeadMergeParams& p, int slot,
     if (p.mode == HEAD_GRAD || p.mode == HEAD_CLIP) p.gco[t] = g;
     if (p.ell) p.ell[c0 + slot] = ell;
     out.g = g;
-    out.lse = static_cast<float>(r.lse);
+    out.lse2 = lse2;
     out.q = q;
     out.tok = ok ? tok : -1;
     return out;
@@ -600,6 +602,7 @@ cudaError_t launch_loss(const LossParams& l, const int* counts, cudaStream_t st)
 // ------------------------------------------------------------ dlogits
 // In place: the kept exponentials E = 2^(z log2 e - m) (fp16) of a row become
 //   dS = g (onehot(tok) - E 2^(m - lse log2 e)),   m the base of the column's group of 32
+// (lse log2 e as two fp32 numbers: rounded to one it would be 4 off for logits of 1e7),
 // rounded to the input type, which the two GEMMs need (E's rounding, 2^-12, is
 // small beside bf16's).  fp16 has no exponent range to
 // spare: there g is multiplied by the power of two 2^e that takes the chunk's
@@ -609,16 +612,16 @@ cudaError_t launch_loss(const LossParams& l, const int* counts, cudaStream_t st)
 // Reads and writes the chunk once: bound by HBM.
 // One row by one block; true if a value is not finite.
 template <bool kBf16>
-__device__ __forceinline__ bool dlogits_row(const HeadChunkParams& p, int slot, int tok, float lse, float q, float coef) {
+__device__ __forceinline__ bool dlogits_row(const HeadChunkParams& p, int slot, int tok, double lse2, float q, float coef) {
     uint4* row = reinterpret_cast<uint4*>(p.dS + static_cast<int64_t>(slot) * p.V_pad);
     const int nvec = p.V_pad / 8;
-    const float lse2 = lse * 1.4426950408889634f;
+    const float hi = static_cast<float>(lse2), lo = static_cast<float>(lse2 - static_cast<double>(hi));
     const float dtok = -coef * expm1f(q);   // g (1 - p_tok)
     const float* mrow = p.mx + static_cast<int64_t>(slot) * p.nc32;
     bool bad = false;
     for (int i = threadIdx.x; i < nvec; i += kTransformThreads) {
         const int v0 = i * 8;
-        const float c = coef * exp2f(mrow[v0 >> 5] - lse2);
+        const float c = coef * exp2f((mrow[v0 >> 5] - hi) - lo);
         const uint4 u = row[i];
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
         uint32_t o[4];
@@ -671,7 +674,7 @@ __global__ void __launch_bounds__(kTransformThreads) k_head_dlogits(const HeadCh
             continue;
         }
         const float coef = kBf16 ? p.gco[t] : ldexpf(p.gco[t], e);
-        bad |= dlogits_row<kBf16>(p, slot, tok, p.lse[t], p.logp[t], coef);
+        bad |= dlogits_row<kBf16>(p, slot, tok, p.lse2[t], p.logp[t], coef);
     }
     if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(p.found_inf, 1);
 }
@@ -699,7 +702,7 @@ __global__ void __launch_bounds__(kTransformThreads) k_merge_dlogits(const HeadM
         }
         __syncthreads();
         const RowGrad r = s_row;
-        if (r.tok >= 0) bad |= dlogits_row<true>(p, slot, r.tok, r.lse, r.q, r.g);
+        if (r.tok >= 0) bad |= dlogits_row<true>(p, slot, r.tok, r.lse2, r.q, r.g);
         else zero_row(p, slot);
         __syncthreads();   // s_row is read
     }
@@ -759,10 +762,13 @@ __global__ void __launch_bounds__(256) k_head_scale(const HeadChunkParams p, flo
                     const float q = p.logp[t];
                     f = 1.f;
                     if (!far) {
-                        const float s = expm1f(-q);
+                        // the entries are relative to the fp32 number that z_tok log2 e was rounded to
+                        const double zt2 = p.zt[t] * 1.4426950408889634074;
+                        const float up = exp2f(static_cast<float>(static_cast<double>(static_cast<float>(zt2)) - zt2));
+                        const float s = expm1f(-q) / up;
                         const uint16_t s16 = round16<true>(s);
                         const float sr = __uint_as_float(static_cast<uint32_t>(s16) << 16);
-                        f = -p.gco[t] * (sr > 0.f ? -expm1f(q) / sr : expf(q));
+                        f = -p.gco[t] * (sr > 0.f ? -expm1f(q) / sr : expf(q) * up);
                         if (d0 == 0 && tok >= 0 && tok < p.V)
                             p.dS[static_cast<int64_t>(slot) * p.V_pad + tok] = s16 ^ 0x8000u;
                     }

@@ -82,10 +82,11 @@ __device__ __forceinline__ int lg_items(const LogitsParams& p, const LgSched& sc
 }
 
 // One row's running statistics over the columns a thread sees: with m = max of
-// z log2 e - kUp as rounded, s = sum 2^(z log2 e - m) and u = sum z 2^(z log2 e - m).
+// z log2 e - kUp rounded up, s = sum 2^(z log2 e - m) and u = sum z 2^(z log2 e - m).
 // In base 2 the rounding of m cancels; e^(z - m) with m log2 e rounded would not.
-// kUp lifts the exponentials to at most 2^14, so that fp16 keeps 11 bits of
-// those down to 2^-28 of the largest.
+// Rounded up, because a step of logits of 1e7 is 1: an m too small by that would
+// take the largest exponential out of fp16's range.  kUp lifts the exponentials to
+// at most 2^14, so that fp16 keeps 11 bits of those down to 2^-28 of the largest.
 constexpr float kUp = 14.f;
 
 struct RowStat {
@@ -211,7 +212,7 @@ __device__ __forceinline__ void lg_body(const LogitsParams& p, const CUtensorMap
                         float cmax = v[0];
 #pragma unroll
                         for (int j = 1; j < 32; ++j) cmax = fmaxf(cmax, v[j]);
-                        base = fmaxf(e.m, fmaf(cmax, p.zscale2, -kUp));
+                        base = fmaxf(e.m, __fmaf_ru(cmax, p.zscale2, -kUp));
                     }
                     float s0 = 0.f, s1 = 0.f, u0 = 0.f, u1 = 0.f;
 #pragma unroll
@@ -586,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int n = 0; n < kNC; ++n) {
                 const float z = vr < p.V && vr != s_tok[n] ? a[n] : kNoLogit;
-                const float mn = fmaxf(m[n], z * p.zscale2);
+                const float mn = fmaxf(m[n], __fmul_ru(z, p.zscale2));
                 const float f = fast_exp2(m[n] - mn), x = fast_exp2(fmaf(z, p.zscale2, -mn));
                 s[n] = fmaf(s[n], f, x);
                 u[n] = fmaf(u[n], f, x * z);

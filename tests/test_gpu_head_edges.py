@@ -178,3 +178,29 @@ def test_extreme_temperatures(rows, T):
         dq = np.ones(rows, np.float32)
         dH, dW = c.logp_bwd(torch.from_numpy(dq).cuda(), T, True)
         check(c, dH, dW, dq, R.logp_entropy(c.P)[2], T, True)
+
+
+@pytest.mark.parametrize("dt,V", [("fp16", 257), ("bf16", 257), ("bf16", 70001)])
+@pytest.mark.parametrize("T", [1e-6, 1e-5])
+def test_gradients_at_the_lowest_temperatures(dt, V, T):
+    """Logits of 1e6 to 1e8: every probability is 0 or 1, in the statistics and in the dlogits alike.  Rows whose two
+    largest logits are too close for fp32 to order get no weight."""
+    c = Case(1, 2, 100, 64, V, dt, "all", T=T, seed=46)
+    order = c.rng.permutation(200)[:100]                 # half of the rows: some other row's token, an improbable one
+    c.tok = c.tok.clone()
+    c.tok[torch.from_numpy(order).cuda()] = (c.tok[torch.from_numpy(order).cuda()] + 11) % V
+    c.P.tokens = c.tok.cpu().numpy()
+    rq, _, lp = R.logp_entropy(c.P)
+    two = np.partition(lp, -2, axis=1)[:, -2:]
+    sure = (two[:, 1] - two[:, 0]) > 100 + 2 * R.logp_bound(c.P)
+    assert sure.mean() > 0.8 and (rq[sure] < -1000).any() and (rq[sure] > -1e-9).any()
+    q, _ = c.logp()
+    assert np.all(np.abs(host(q) - rq) <= R.logp_bound(c.P) + 4e-7 * np.abs(R.logits(c.P)).max(1))
+    dq = sure.astype(np.float32)
+    scale = float(np.float32(T))
+    dH, dW = c.logp_bwd(torch.from_numpy(dq).cuda(), scale, True)
+    assert int(c.status) == 0 and int(c.inf) == 0
+    # a sure row's dlogits are +-1 or 0 exactly; the functions and the scale are a few steps of fp32 off
+    rH, bH, rW, bW = B.grad_bounds(c.P, dq.astype(np.float64), lp, dt, False, "f32", 8 * B.STEP32, scale)
+    assert np.all(np.abs(host(dH) - rH) <= bH), np.max(np.abs(host(dH) - rH) / bH)
+    assert np.all(np.abs(host(dW) - rW) <= bW), np.max(np.abs(host(dW) - rW) / bW)
