@@ -35,8 +35,8 @@ constexpr int kFewVocab = 128;      // vocabulary rows per tile of the few-row k
 // power of two, so its product with log2 e is that constant's rounding, exactly
 constexpr float kNoLogit = -1267650600228229401496703205376.f;   // -2^100
 constexpr float kNoLogit2 = kNoLogit * 1.4426950408889634f;
-// Correction of the tensor cores' rounding towards zero: n additions make a sum
-// too small by kAddLoss n of itself (see head_tc.cu)
+// Correction of the tensor cores' rounding towards zero, for the logits: n additions
+// of terms of one size make a sum too small by kAddLoss n of itself (see head_tc.cu)
 constexpr double kAddLoss = 1.45e-8;
 // A chunk with a row whose q is below this takes dlogits relative to the running
 // maximum instead of to the given token (see k_head_scale): bf16 would hold
@@ -207,10 +207,18 @@ struct HeadChunkParams : ChunkParams {
     float loss_scale;
 };
 
-// What the tensor cores' rounding takes from a sum over the vocabulary in `pieces`
-// parts: 1e-4 of it at V = 100352, which fp16 outputs would show
-__device__ __forceinline__ float dh_gain(int V, int pieces) {
-    return 1.f + static_cast<float>(kAddLoss) * static_cast<float>(V / (16 * pieces));
+// dH's share of the same rounding.  A dH row is almost the given token's own term,
+// g (1 - p_tok) W[tok]: the other tokens' terms mostly cancel.  So the running sum
+// has its final size from that token's place on, and each addition after it takes
+// kTokenLoss of it: measured 3.2e-8 to 3.4e-8 with tokens at the start, the quarters
+// and near the end of a vocabulary of 100352 (1.9e-4 of dH at the start, nothing at
+// the end, which fp16 outputs would show).  piece: vocabulary rows of a K piece, V where
+// the sum is whole.  What another likely token's term loses is not covered.
+constexpr float kTokenLoss = 3.2e-8f;
+
+__device__ __forceinline__ float dh_gain(int tok, int V, int piece) {
+    const int t = min(max(tok, 0), V - 1);   // a bad token's row is 0
+    return 1.f + kTokenLoss * static_cast<float>(min(piece - t % piece, V - t) / 16);
 }
 
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t st);

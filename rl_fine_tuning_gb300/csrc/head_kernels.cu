@@ -828,7 +828,8 @@ __global__ void __launch_bounds__(256) k_dh_join(const HeadChunkParams p) {
     const int n_nt = (p.d + cols - 1) / cols;
     const int units = (n_c + 2 * kBM - 1) / (2 * kBM) * n_nt;
     const int rem = units - plan.x;
-    const float scale = p.oscale[p.chunk] * dh_gain(p.V, plan.y);
+    const float scale = p.oscale[p.chunk];
+    const int ks = (p.V + kBK - 1) / kBK, piece = (ks + plan.y - 1) / plan.y * kBK;   // vocabulary rows of a K piece
     const int lane = threadIdx.x & 31;
     bool bad = false;
     for (int it = blockIdx.x * 8 + (threadIdx.x >> 5); it < rem * 2 * kBM * halves; it += gridDim.x * 8) {
@@ -847,7 +848,8 @@ __global__ void __launch_bounds__(256) k_dh_join(const HeadChunkParams p) {
             acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w;
             acc[4] += b.x, acc[5] += b.y, acc[6] += b.z, acc[7] += b.w;
         }
-        const float f = p.rowf ? scale * p.rowf[slot] : scale;
+        float f = scale * dh_gain(p.tokens[t], p.V, piece);
+        if (p.rowf) f *= p.rowf[slot];
         uint32_t o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

@@ -784,8 +784,11 @@ struct HeadDh : Base {
         }
         const int t = valid ? p.rows[sc.c0 + slot] : 0;
         if (valid && !GRPO_DCHECK(t >= 0 && t < p.N, p.status)) valid = false;
-        const float scale = sc.winv * dh_gain(p.V, 1);
-        const float f = p.rowf && valid ? scale * p.rowf[slot] : scale;
+        float f = sc.winv;
+        if (valid) {
+            f *= dh_gain(p.tokens[t], p.V, p.V);
+            if (p.rowf) f *= p.rowf[slot];
+        }
         uint16_t* out = p.dH + static_cast<int64_t>(t) * p.d;
         Finite<kBf16> fin;
 #pragma unroll 1

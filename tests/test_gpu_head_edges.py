@@ -204,3 +204,41 @@ def test_gradients_at_the_lowest_temperatures(dt, V, T):
     rH, bH, rW, bW = B.grad_bounds(c.P, dq.astype(np.float64), lp, dt, False, "f32", 8 * B.STEP32, scale)
     assert np.all(np.abs(host(dH) - rH) <= bH), np.max(np.abs(host(dH) - rH) / bH)
     assert np.all(np.abs(host(dW) - rW) <= bW), np.max(np.abs(host(dW) - rW) / bW)
+
+
+# ---------------------------------------------------------------- the tensor cores' rounding towards zero
+
+@pytest.mark.parametrize("place", [0.0, 0.5, 1.0])
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("N", [9728, 1024])
+def test_dh_is_not_too_small_by_the_place_of_the_token(N, dt, place):
+    """dH against 64 bits along dH itself, where element-wise roundings average out: given tokens at the start of the
+    vocabulary, whose terms all later additions round down, in its middle and at its end.  9728 rows: whole sums over the
+    vocabulary; 1024: sums in pieces.  The loss is 3.2e-8 to 3.4e-8 for each of up to 6272 additions (0.2e-8 of it left:
+    1.3e-5); the roundings of 1024 rows' largest dlogits, 1.4e-4 each on average, leave 0.5e-5 (three times that)."""
+    d, V, span = 512, 100352, 4096
+    g = torch.Generator(device="cuda").manual_seed(47)
+    dtype = {"bf16": torch.bfloat16, "fp16": torch.float16}[dt]
+
+    def randn(*s):
+        return torch.randn(*s, device="cuda", generator=g)
+    W = (randn(V, d) * d ** -0.5).to(dtype)
+    lo = int(place * (V - span))
+    tok = torch.randint(lo, lo + span, (N,), device="cuda", generator=g, dtype=torch.int32)
+    h = (randn(N, d) + (2 + 10 * torch.rand(N, 1, device="cuda", generator=g)) * W[tok.long()].float()).to(dtype)
+    dq = randn(N)
+    shape = rg.make_shape(1, 1, N, d, V, rg.BF16 if dt == "bf16" else rg.FP16)
+    ws = torch.empty(rg.grpo_policy_workspace_bytes(shape, "logp_grad"), dtype=torch.uint8, device="cuda")
+    mask = torch.ones(N, dtype=torch.uint8, device="cuda")
+    dH, dW = torch.empty_like(h), torch.empty_like(W)
+    status, inf = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
+    rg.grpo_logprobs_bwd(h, W, tok, mask, dq, shape, 1.0, 64.0, ws, dH, dW, inf, status)
+    assert int(status) == 0 and int(inf) == 0
+    W64, dot, square = W.double(), 0.0, 0.0
+    for r in torch.arange(N, device="cuda").split(1024):
+        p = torch.softmax(h[r].double() @ W64.t(), 1).neg_()
+        p[torch.arange(len(r), device="cuda"), tok[r].long()] += 1
+        want = (64.0 * dq[r].double()[:, None] * p) @ W64
+        dot += float((dH[r].double() * want).sum())
+        square += float((want * want).sum())
+    assert abs(dot / square - 1) < 3e-5
