@@ -29,6 +29,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -200,10 +201,25 @@ def peaks():
     return dict(FALLBACK_PEAKS), "fallback"
 
 
+def kernel_source_files():
+    """The files that hold the chunk kernels (tc_kernels.cu, and small_kernels.cu for the dlogits pass), and every file of
+    csrc that they include, directly or through another."""
+    csrc = os.path.join(ROOT, "rl_fine_tuning_gb300", "csrc")
+    todo, found = ["tc_kernels.cu", "small_kernels.cu"], set()
+    while todo:
+        f = todo.pop()
+        if f in found or not os.path.exists(os.path.join(csrc, f)):
+            continue
+        found.add(f)
+        with open(os.path.join(csrc, f), encoding="utf-8") as src:
+            todo += re.findall(r'^\s*#\s*include\s+"([^"]+)"', src.read(), re.M)
+    return [os.path.join(csrc, f) for f in sorted(found)]
+
+
 def kernel_source_hash():
     h = hashlib.sha256()
-    for f in ("tc_kernels.cu", "ptx.cuh"):
-        h.update(open(os.path.join(ROOT, "rl_fine_tuning_gb300", "csrc", f), "rb").read())
+    for f in kernel_source_files():
+        h.update(open(f, "rb").read())
     return h.hexdigest()[:16]
 
 
