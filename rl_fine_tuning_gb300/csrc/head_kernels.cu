@@ -603,9 +603,11 @@ cudaError_t launch_loss(const LossParams& l, const int* counts, cudaStream_t st)
 // In place: the kept exponentials E = 2^(z log2 e - m) (fp16) of a row become
 //   dS = g (onehot(tok) - E 2^(m - lse log2 e)),   m the base of the column's group of 32
 // (lse log2 e as two fp32 numbers: rounded to one it would be 4 off for logits of 1e7),
-// rounded to the input type, which the two GEMMs need (E's rounding, 2^-12, is
-// small beside bf16's).  fp16 has no exponent range to
-// spare: there g is multiplied by the power of two 2^e that takes the chunk's
+// rounded to the input type, which the two GEMMs need.  E is fp16 for both types: the
+// chunk buffer has 16 bits an entry, and it is overwritten in place.  Beside bf16's
+// rounding E's is small; fp16 dlogits have two roundings of one size (2.8e-4 of dH and
+// dW together against 64 bits, fp32 exponentials 2.1e-4).  fp16 has no exponent range
+// to spare: there g is multiplied by the power of two 2^e that takes the chunk's
 // largest |g| to 2^13 .. 2^14, and the GEMMs' epilogues undo it (oscale), whatever
 // the caller's loss scale is.  e reaches 162 (a saturated preference pair's g is
 // 1e-36, fp32 goes down to 2^-149), where 2^e is no fp32 number: ldexpf applies it.
@@ -729,11 +731,13 @@ cudaError_t launch_head_dlogits(const HeadChunkParams& p, float* oscale, bool bf
 // s = sum of A over the other columns, p_tok = 1 / (1 + s) and
 //   dS_v = g (onehot - p_v) = f A_v  with  f = -g p_tok  and  A_tok = -s.
 // f is a factor of the row: dH's epilogue applies it, and for dW, where rows are
-// summed, the rows of h carry it.  A is rounded once to bf16, f h once more.  The row's largest entry is
-// the token's: f is taken as -g (1 - p_tok) / A_tok with A_tok as rounded, so
-// that entry is exact and dH has one rounding less than with the pass.  On 4.9K
-// rows of a 152K vocabulary at d = 1536 this kernel and the empty fallback take
-// 0.02 ms where the pass took 0.53.
+// summed, the rows of h carry it.  Roundings to bf16: A, which has to be a tensor
+// core operand beside bf16 W and h, and f h, likewise, for dW.  The row's largest entry
+// is the token's: f is taken as -g (1 - p_tok) / A_tok with A_tok as rounded, so that
+// entry is exact in dH; the others carry A_tok's rounding (in f) beside their own,
+// which is the better trade: half of a row's sum of absolute products is the token's
+// (dH's error on 4.9K rows 1.7e-3 instead of 2.4e-3).  On 4.9K rows of a 152K vocabulary
+// at d = 1536 this kernel and the empty fallback take 0.02 ms where the pass took 0.53.
 //
 // This kernel writes A_tok, f, and f h transposed for dW's K-major operand.  In
 // a chunk that holds a row with q < kLeastQ (far), the logits kernel ran again
