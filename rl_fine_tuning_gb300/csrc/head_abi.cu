@@ -376,7 +376,7 @@ struct HeadRun {
         p.rows = at<int>(L.rows);
         p.tokens = c.tokens;
         p.zt = at<double>(L.zt);
-        p.lse2 = at<double>(L.lse2);
+        p.lse2 = at<float2>(L.lse2);
         p.gco = at<float>(L.gco);
         p.ell = c.mode == HEAD_CLIP ? at<float>(L.ell) : nullptr;
         p.gmax = c.backward && !bf16 ? at<unsigned>(L.gmax) : nullptr;
@@ -461,7 +461,7 @@ struct HeadRun {
         p.oscale = at<float>(L.oscale);
         p.rows = at<int>(L.rows);
         p.tokens = c.tokens;
-        p.lse2 = at<double>(L.lse2);
+        p.lse2 = at<float2>(L.lse2);
         p.zt = at<double>(L.zt);
         p.gco = at<float>(L.gco);
         p.mx = at<float>(L.mx);

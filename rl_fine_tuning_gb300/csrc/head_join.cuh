@@ -10,10 +10,13 @@ namespace grpo {
 //   q = -log(1 + x),   lse = z_tok - q,   H = -sum p log p = lse - E[z].
 // log1p keeps q's relative precision however near the token's probability is
 // to 1.  The differences of numbers of about 10 are in fp64, the functions in
-// fp32 (fp64 ones cost microseconds).
+// fp32 (fp64 ones cost microseconds).  lse2, for the dlogits: lse in base 2 as
+// M + log2(s + e^z_tok / 2^M), two numbers: rounded to one it would be 4 off for
+// logits of 1e7, and a probability of 1 would be 8.
 struct RowSum {
     double lse, q;
     float ent;
+    float2 lse2;
 };
 
 __device__ __forceinline__ float warp_max(float m) {
@@ -38,11 +41,14 @@ __device__ __forceinline__ RowSum finish_row(float m, float s, float u, double z
         const float x = s * f;
         r.q = -static_cast<double>(log1pf(x));
         r.lse = zt - r.q;
+        const float up = -static_cast<float>(dm);
+        r.lse2 = make_float2(m, up > 100.f ? up : log2f(s + exp2f(up)));   // s is below 2^50
         mean = (fmaf(u, f, static_cast<float>(zt))) / (1.f + x);
     } else {   // p below 2^-80: the given token adds nothing
         int ex;
         const float mant = frexpf(s, &ex);
         r.lse = (static_cast<double>(m) + ex + static_cast<double>(log2f(mant))) * kLn2D;
+        r.lse2 = make_float2(m, log2f(s));
         r.q = zt - r.lse;
         mean = u / s;
     }
@@ -100,6 +106,7 @@ __device__ __forceinline__ RowSum join_row_relative(const float4* part, int S2, 
     r.q = -static_cast<double>(log1pf(s * exp2f(static_cast<float>(base - zt * 1.4426950408889634074))));
     r.lse = zt - r.q;
     r.ent = 0.f;
+    r.lse2 = make_float2(0.f, 0.f);   // not used: the dlogits are relative to the token
     return r;
 }
 

@@ -427,19 +427,20 @@ constexpr int kHeadMergeThreads = 256;
 
 // One row's merge by one warp; lane 0 writes and returns what its dlogits need.
 struct RowGrad {
-    double lse2;
+    float2 lse2;
     float g, q;
     int tok;   // -1: nothing (a bad token id, reported here)
 };
 
 __device__ __forceinline__ RowGrad merge_row(const HeadMergeParams& p, int slot, int c0, int lane) {
-    RowGrad out{0.0, 0.f, 0.f, -1};
+    RowGrad out{make_float2(0.f, 0.f), 0.f, 0.f, -1};
     const int S2 = 2 * p.plan[p.chunk].x;
     const int t = p.rows[c0 + slot];
     if (!GRPO_DCHECK(t >= 0 && t < p.N, p.status)) return out;
     const int tok = p.tokens[t];
     const bool ok = tok >= 0 && tok < p.V;
-    RowSum r{0.0, 0.0, 0.f};
+    // a bad token's row has no sum; an infinite one makes its probabilities 0, whatever its logits
+    RowSum r{0.0, 0.0, 0.f, make_float2(INFINITY, 0.f)};
     if (ok) r = p.relative ? join_row_relative(p.part + static_cast<int64_t>(slot) * S2, S2, lane, p.zt[t])
                            : join_row(p.part + static_cast<int64_t>(slot) * S2, S2, lane, p.zt[t]);
     if (lane != 0) return out;
@@ -469,8 +470,7 @@ __device__ __forceinline__ RowGrad merge_row(const HeadMergeParams& p, int slot,
         g *= w;
     }
     g *= p.inv_t;
-    const double lse2 = r.lse * 1.4426950408889634074;
-    p.lse2[t] = lse2;
+    p.lse2[t] = r.lse2;
     if (p.logp) p.logp[t] = q;
     if (p.entropy) p.entropy[t] = r.ent;
     if (p.stats) {
@@ -480,8 +480,8 @@ __device__ __forceinline__ RowGrad merge_row(const HeadMergeParams& p, int slot,
     }
     if (p.mode == HEAD_GRAD || p.mode == HEAD_CLIP) p.gco[t] = g;
     if (p.ell) p.ell[c0 + slot] = ell;
+    out.lse2 = r.lse2;
     out.g = g;
-    out.lse2 = lse2;
     out.q = q;
     out.tok = ok ? tok : -1;
     return out;
@@ -517,7 +517,7 @@ cudaError_t launch_head_merge(const HeadMergeParams& p, cudaStream_t st) {
 //   S = sum (or mean) over a completion's rows of q - p,   m = beta (S_2i - S_2i+1)
 // and d loss / d q of their rows.  Sums in fp64 in a fixed order.  Pairs
 // without a row are left out of the mean.  A row whose token is out of range adds
-// 0 to S and gets no gradient.  8 us (latency).
+// 0 to S (its dlogits are zeros whatever its d loss / d q).  8 us (latency).
 __global__ void __launch_bounds__(256) k_pair_coef(const PairParams p) {
     __shared__ double sh[256];
     __shared__ float s_g[2];
@@ -531,8 +531,10 @@ __global__ void __launch_bounds__(256) k_pair_coef(const PairParams p) {
         for (int i = b[c] + threadIdx.x; i < b[c + 1]; i += 256) {
             const int t = p.rows[i];
             if (!GRPO_DCHECK(t >= 0 && t < p.N, p.status)) continue;
+            // the three loads before the branch, so that their latencies overlap
             const int tok = p.tokens[t];
-            if (tok >= 0 && tok < p.V) acc += static_cast<double>(p.logp[t]) - static_cast<double>(p.logp_ref[t]);
+            const float q = p.logp[t], ref = p.logp_ref[t];
+            if (tok >= 0 && tok < p.V) acc += static_cast<double>(q) - static_cast<double>(ref);
         }
         S[c] = block_sum(acc, sh);
         if (p.length_mean && b[c + 1] > b[c]) S[c] /= b[c + 1] - b[c];
@@ -577,9 +579,7 @@ __global__ void __launch_bounds__(256) k_pair_coef(const PairParams p) {
     __syncthreads();
     for (int i = b[0] + threadIdx.x; i < b[2]; i += 256) {
         const int t = p.rows[i];
-        if (!GRPO_DCHECK(t >= 0 && t < p.N, p.status)) continue;
-        const int tok = p.tokens[t];
-        p.gco[t] = tok >= 0 && tok < p.V ? (i < b[1] ? s_g[0] : s_g[1]) : 0.f;
+        if (GRPO_DCHECK(t >= 0 && t < p.N, p.status)) p.gco[t] = i < b[1] ? s_g[0] : s_g[1];
     }
 }
 
@@ -602,7 +602,7 @@ cudaError_t launch_loss(const LossParams& l, const int* counts, cudaStream_t st)
 // ------------------------------------------------------------ dlogits
 // In place: the kept exponentials E = 2^(z log2 e - m) (fp16) of a row become
 //   dS = g (onehot(tok) - E 2^(m - lse log2 e)),   m the base of the column's group of 32
-// (lse log2 e as two fp32 numbers: rounded to one it would be 4 off for logits of 1e7),
+// (lse log2 e as two fp32 numbers, see RowSum),
 // rounded to the input type, which the two GEMMs need.  E is fp16 for both types: the
 // chunk buffer has 16 bits an entry, and it is overwritten in place.  Beside bf16's
 // rounding E's is small; fp16 dlogits have two roundings of one size (2.8e-4 of dH and
@@ -614,16 +614,15 @@ cudaError_t launch_loss(const LossParams& l, const int* counts, cudaStream_t st)
 // Reads and writes the chunk once: bound by HBM.
 // One row by one block; true if a value is not finite.
 template <bool kBf16>
-__device__ __forceinline__ bool dlogits_row(const HeadChunkParams& p, int slot, int tok, double lse2, float q, float coef) {
+__device__ __forceinline__ bool dlogits_row(const HeadChunkParams& p, int slot, int tok, float2 lse2, float q, float coef) {
     uint4* row = reinterpret_cast<uint4*>(p.dS + static_cast<int64_t>(slot) * p.V_pad);
     const int nvec = p.V_pad / 8;
-    const float hi = static_cast<float>(lse2), lo = static_cast<float>(lse2 - static_cast<double>(hi));
     const float dtok = -coef * expm1f(q);   // g (1 - p_tok)
     const float* mrow = p.mx + static_cast<int64_t>(slot) * p.nc32;
     bool bad = false;
     for (int i = threadIdx.x; i < nvec; i += kTransformThreads) {
         const int v0 = i * 8;
-        const float c = coef * exp2f((mrow[v0 >> 5] - hi) - lo);
+        const float c = coef * exp2f((mrow[v0 >> 5] - lse2.x) - lse2.y);
         const uint4 u = row[i];
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
         uint32_t o[4];
@@ -671,11 +670,7 @@ __global__ void __launch_bounds__(kTransformThreads) k_head_dlogits(const HeadCh
         const int t = p.rows[c0 + slot];
         if (!GRPO_DCHECK(t >= 0 && t < p.N, p.status)) continue;
         const int tok = p.tokens[t];
-        if (tok < 0 || tok >= p.V) {   // no lse to go by: 0 times the exponentials of large logits would be NaN
-            zero_row(p, slot);
-            continue;
-        }
-        const float coef = kBf16 ? p.gco[t] : ldexpf(p.gco[t], e);
+        const float coef = tok >= 0 && tok < p.V ? (kBf16 ? p.gco[t] : ldexpf(p.gco[t], e)) : 0.f;
         bad |= dlogits_row<kBf16>(p, slot, tok, p.lse2[t], p.logp[t], coef);
     }
     if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(p.found_inf, 1);
@@ -704,8 +699,7 @@ __global__ void __launch_bounds__(kTransformThreads) k_merge_dlogits(const HeadM
         }
         __syncthreads();
         const RowGrad r = s_row;
-        if (r.tok >= 0) bad |= dlogits_row<true>(p, slot, r.tok, r.lse2, r.q, r.g);
-        else zero_row(p, slot);
+        bad |= dlogits_row<true>(p, slot, r.tok, r.lse2, r.q, r.tok >= 0 ? r.g : 0.f);
         __syncthreads();   // s_row is read
     }
     if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(p.found_inf, 1);
@@ -852,7 +846,8 @@ __global__ void __launch_bounds__(256) k_dh_join(const HeadChunkParams p) {
             acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w;
             acc[4] += b.x, acc[5] += b.y, acc[6] += b.z, acc[7] += b.w;
         }
-        float f = scale * dh_gain(p.tokens[t], p.V, piece);
+        float f = scale;
+        if (p.V > kEvenVocab) f *= dh_gain(p.tokens[t], p.V, piece);
         if (p.rowf) f *= p.rowf[slot];
         uint32_t o[4];
 #pragma unroll

@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok = s_tok[n];
         const bool on = !p.mask || p.mask[n] != 0;
         const bool ok = tok >= 0 && tok < p.V;
-        RowSum r{0.0, 0.0, 0.f};
+        RowSum r{0.0, 0.0, 0.f, make_float2(0.f, 0.f)};
         if (on && ok) r = join_row_once<kFewCtas / 32>(p.part + static_cast<int64_t>(n) * n_cta, n_cta, lane, p.zt[n]);
         if (lane == 0) {
             if (on && !ok) atomicCAS(status, 0, GRPO_ERR_SHAPE);
@@ -786,7 +786,7 @@ struct HeadDh : Base {
         if (valid && !GRPO_DCHECK(t >= 0 && t < p.N, p.status)) valid = false;
         float f = sc.winv;
         if (valid) {
-            f *= dh_gain(p.tokens[t], p.V, p.V);
+            if (p.V > kEvenVocab) f *= dh_gain(p.tokens[t], p.V, p.V);
             if (p.rowf) f *= p.rowf[slot];
         }
         uint16_t* out = p.dH + static_cast<int64_t>(t) * p.d;
