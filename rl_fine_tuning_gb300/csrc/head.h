@@ -25,7 +25,11 @@ constexpr int kPieceK = 1024;       // K elements the tensor cores add up before
 constexpr int kHeadThreads = 384;   // a warpgroup with the producer and MMA warps, two of epilogue warps
 constexpr int kHeadSplitsMax = 512;    // vocabulary splits of the logits kernel
 constexpr int kHeadChunkTiles = 76;    // default rows per chunk, in tiles of 128
-constexpr int kDhSlotsMax = 304;      // 256 x 256 partial tiles of dH (4 per SM pair, 80 MB)
+// SM pairs of a GB300, for what the host lays out before it asks the device: the size of
+// the workspace and dH's unit width.  The launches and k_plan go by the device's own
+// count; on another count these would only be less well tuned.
+constexpr int kSmPairs = 76;
+constexpr int kDhSlotsMax = 4 * kSmPairs;   // 256 x 256 partial tiles of dH (80 MB)
 constexpr int kDhWideSlotsMax = 256;  // 256 x 512 ones
 constexpr int kFewRows = 32;        // rows of the few-row kernel
 constexpr int kFewCtas = 256;          // most CTAs of the few-row kernel

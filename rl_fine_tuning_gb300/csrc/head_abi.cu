@@ -90,7 +90,7 @@ bool head_layout(const grpo_shape& s, int op, int dw_f32, HeadLayout* o) {
     // against 4.74 ms for dH of 7.5K rows of the 8B head; with fewer units their raggedness costs more
     // (d = 1536, 4.9K rows: 1.45 against 1.37 ms)
     const int row_pairs = (o->R + 2 * kBM - 1) / (2 * kBM);
-    o->dh_cols = !o->one_launch && s.d % (2 * kBN) == 0 && row_pairs * (s.d / (2 * kBN)) >= 2 * 76 ? 2 * kBN : kBN;
+    o->dh_cols = !o->one_launch && s.d % (2 * kBN) == 0 && row_pairs * (s.d / (2 * kBN)) >= 2 * kSmPairs ? 2 * kBN : kBN;
     const int64_t units = static_cast<int64_t>(row_pairs) * ((s.d + o->dh_cols - 1) / o->dh_cols);
     // up to 32 K-stages (V = 2048) a unit is not worth splitting: no partial tiles, and no launch to join them
     const int ks = (s.V + kBK - 1) / kBK;

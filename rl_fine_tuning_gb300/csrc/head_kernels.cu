@@ -589,7 +589,8 @@ cudaError_t launch_pair_coef(const PairParams& p, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------ loss
-// Without a backward; with one, head_grads_kernel does the same.
+// Without a backward; with one, an idle warp of the last chunk's dH kernel (or of the
+// one for dH and dW) does the same.
 __global__ void __launch_bounds__(32) k_loss(const LossParams l, const int* __restrict__ counts) {
     write_loss(l, counts, threadIdx.x);
 }

@@ -74,7 +74,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 
 // After an abort, TMA loads that the CTA issued before its roles stopped may
 // still be writing into its shared memory.  The kernels first wait for them on
-// the full barriers they complete on (see wait_inflight in tc_kernels.cu).
+// the full barriers they complete on (see wait_inflight in tc_pair.cuh).
 // Where that cannot account for every issued load (in a CTA pair, one CTA
 // issued loads for a K-stage the other never armed), the CTA falls back to
 // this fixed wait: an issued load lands within microseconds.
@@ -136,7 +136,7 @@ __device__ __forceinline__ void tma_load_2d(const CUtensorMap* map, uint64_t* ba
 // ---------------------------------------------------------------- tcgen05
 
 // Shared-memory matrix descriptor, 128-byte swizzle, Blackwell version field.
-//   lbo / sbo in bytes (the operand layouts are described in tc_kernels.cu)
+//   lbo / sbo in bytes (the operand layouts are described in tc_pair.cuh)
 __device__ __forceinline__ uint64_t make_sdesc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
