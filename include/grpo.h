@@ -376,7 +376,9 @@ void grpo_pair_opts_init(grpo_pair_opts* o);
  * for GRPO_OP_LOGPROBS): O(chunk_rows * (V + d) + N), plus 4 V d when a 16-bit
  * dW is summed over several chunks.  GRPO_OP_PAIR: chunks hold a whole pair
  * (2 L rows) up to 19456 rows unless chunk_rows says otherwise.  0 for an
- * invalid shape or op. */
+ * invalid shape or op.  The forward-only entry points of GRPO_OP_CLIP and
+ * GRPO_OP_PAIR take the same workspace and leave most of it alone: for a
+ * forward alone, a small chunk_rows and dw_f32 = 1 make it small. */
 size_t grpo_policy_workspace_bytes(const grpo_shape* shape, int op, int dw_f32);
 
 /* Log-probs of given tokens.

@@ -606,7 +606,7 @@ cudaError_t launch_loss(const LossParams& l, const int* counts, cudaStream_t st)
 // (lse log2 e as two fp32 numbers, see RowSum),
 // rounded to the input type, which the two GEMMs need.  E is fp16 for both types: the
 // chunk buffer has 16 bits an entry, and it is overwritten in place.  Beside bf16's
-// rounding E's is small; fp16 dlogits have two roundings of one size (2.8e-4 of dH and
+// rounding E's is small; fp16 dlogits have two roundings of one size (3.0e-4 of dH and
 // dW together against 64 bits, fp32 exponentials 2.1e-4).  fp16 has no exponent range
 // to spare: there g is multiplied by the power of two 2^e that takes the chunk's
 // largest |g| to 2^13 .. 2^14, and the GEMMs' epilogues undo it (oscale), whatever

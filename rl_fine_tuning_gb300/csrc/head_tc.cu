@@ -14,8 +14,8 @@
 // long step by the card's power limit (cuBLAS sustains 1765 TFLOP/s in bf16 then,
 // 1967 in a burst).  7500 rows of the 8B head (d = 4096, V = 128256), inside a step:
 // logits 4.9 ms = 1.61 PFLOP/s (12% of it for storing the exponentials), dH
-// 4.5 ms = 1.75, dW 4.55 ms = 1.73.  The few-row kernel is bound by HBM: 165 us for
-// one row of that head, 6.4 TB/s, 95% of a copy's rate.
+// 4.5 ms = 1.75, dW 4.55 ms = 1.73.  The few-row kernel is bound by HBM: 160 to
+// 169 us for one row of that head on different cards, 93 to 98% of a copy's rate.
 //
 // Sums over K.  tcgen05.mma adds to its fp32 accumulator with rounding towards
 // zero: after d / 16 additions a logit of 11 was 4.6e-5 too small at d = 4096
@@ -31,8 +31,8 @@
 //     the loss is proportional to the sum: kAddLoss n.  Measured per addition:
 //     1.43e-8 of the sum for n = 64, 1.57e-8 for n = 256, within 8% on five kinds
 //     of inputs (half as much again with outlier columns).  The forward
-//     kernels multiply it back in with the scale of the logits; what is left of a
-//     logit of 10 is below 1e-6, and 4e-8 of an average one.
+//     kernels multiply it back in with the scale of the logits; what is left is
+//     below 1.3e-7 of a logit, with outlier columns 5.4e-7.
 #include <atomic>
 #include <cfloat>
 
