@@ -435,6 +435,116 @@ int grpo_pair_loss_fwd_bwd(const void* h, const void* W, const int32_t* tokens, 
                            size_t ws_bytes, float* loss_out, void* dH, void* dW, int32_t* found_inf, float* logp_out,
                            float* pair_stats, int32_t* status, grpo_stream_t stream);
 
+/* ---- the norm before the head, 8-bit checkpoints -----------------------
+ * What stands between a model's residual stream and the hidden states h of the
+ * calls above, in both directions:
+ *   grpo_norm_fwd     adds the residual, norms, and writes h in 16 bits or as the
+ *                     8-bit codes that grpo_loss_*_fp8 read
+ *   grpo_norm_bwd     takes dH on to the residual stream and the norm's weight
+ *   grpo_ckpt_pack    keeps an activation in 8 bits between forward and backward
+ *   grpo_ckpt_unpack  gives it back in 16 bits
+ * grpo_norm_fwd can write such a checkpoint of the stream itself, and
+ * grpo_norm_fwd and grpo_norm_bwd read one in the place of the 16-bit stream, so
+ * that neither form of it needs a pass of its own.  The pages name activation
+ * offload ("Long-context GRPO", section 2) without a format, and no formula of
+ * the model's norm; those used are stated here.
+ *
+ * Common to them: matrices [N x d] of type shape->dtype (GRPO_BF16 or GRPO_FP16;
+ * others are refused with GRPO_ERR_DTYPE), 16-byte aligned; V, beta and what else
+ * describes a loss are not looked at beyond the checks of every shape.  mask: NULL
+ * counts every row, else [N] uint8, nonzero = the row counts.  Rows that do not
+ * count are not read (they may hold anything) and count as rows of zeros: their
+ * outputs are zeros, and scales 2^-126.  Nothing is written behind row N.  Outputs overlap
+ * neither inputs nor one another, but a 16-bit output of the same shape may be
+ * the same pointer as a 16-bit input (sum_out = residual, dx = dy).  Every output
+ * is bitwise reproducible, sums are in fp32 in a fixed order, and calls can be
+ * captured into a CUDA graph. */
+
+/* Columns of a row that share one scale of a checkpoint. */
+#define GRPO_CKPT_BLOCK 64
+
+/* An 8-bit checkpoint of an [N x d] matrix, both parts device memory:
+ *   codes  [N x d] int8, 16-byte aligned
+ *   scales [N x d / GRPO_CKPT_BLOCK] bf16
+ * x stands as code * scale, rounded to the 16-bit type, with
+ *   scale = max |x| of the block / 127 in bf16, at least 2^-126
+ *   code  = x / scale rounded to the nearest integer
+ * so that a value is off by at most 0.501 of its block's scale and by one
+ * rounding to 16 bits.  (Scales are at most 2^121 for bf16 and 2^9 for fp16, so
+ * that no finite value comes back as infinity: blocks with a value above 3.38e38,
+ * or above 65024 in fp16, are off by up to one scale there.)  A block with a value
+ * that is not finite comes back as NaN. */
+typedef struct {
+    int8_t* codes;
+    uint16_t* scales;
+} grpo_ckpt;
+
+/* Options of grpo_norm_*.  grpo_norm_opts_init: eps 1e-6, a weight of type dtype,
+ * y of type dtype.
+ *   eps        : 2^-126 or more, added to the mean square
+ *   weight_f32 : the weight (and its gradient) is fp32 (1) or of type shape->dtype (0)
+ *   plus_one   : y is multiplied by the weight (0) or by 1 + weight (1)
+ *   y_type     : shape->dtype, GRPO_E4M3 or GRPO_E5M2
+ *   y_scale    : 8-bit y only.  2^-126 to 2^126: the one scale of all codes, as
+ *                grpo_loss_*_fp8 want it.  0: a scale per row.  A norm's output is
+ *                at most sqrt(d) max|weight|, so that over 448 (E4M3) is a scale
+ *                with which nothing saturates.
+ * grpo_norm_bwd looks at eps, weight_f32 and plus_one only. */
+typedef struct {
+    float eps;
+    int weight_f32, plus_one;
+    grpo_dtype y_type;
+    float y_scale;
+} grpo_norm_opts;
+
+void grpo_norm_opts_init(grpo_norm_opts* o, grpo_dtype dtype);
+
+/* Bytes of device workspace of grpo_norm_bwd: 4 d for each of up to 456 partial
+ * sums, and their flags.  0 for an invalid shape. */
+size_t grpo_norm_workspace_bytes(const grpo_shape* shape);
+
+/* Root-mean-square norm.  d is at most 16384 (GRPO_ERR_SHAPE above).
+ *   s = x + residual, rounded to 16 bits   (s = x without a residual;
+ *       s = the checkpoint's values with x_ckpt)
+ *   y = s / sqrt(mean(s^2) + eps) * weight
+ *   x, x_ckpt: exactly one is given, the other NULL; residual: NULL or [N x d],
+ *       NULL with x_ckpt
+ *   weight [d], 16-byte aligned
+ *   y [N x d] of type y_type, 16-byte aligned.  8-bit: codes of y / scale, rounded
+ *       to nearest, those above the type's largest value at that value; NaN stays NaN
+ *   row_scale: 8-bit y only, else NULL.  [N] fp32 <- max |y| of the row / the
+ *       type's largest value (448 or 57344), at least 2^-126, NaN left out.  These
+ *       are the codes' scales when y_scale is 0; with a y_scale it may be NULL
+ *   sum_out: NULL or [N x d] <- s
+ *   sum_ckpt: NULL or a checkpoint <- s, NULL with x_ckpt; the same bits as
+ *       grpo_ckpt_pack of sum_out
+ * Squares are summed in fp32: a row's sum of squares has to stay below 3e38. */
+int grpo_norm_fwd(const void* x, const grpo_ckpt* x_ckpt, const void* residual, const void* weight, const uint8_t* mask,
+                  const grpo_shape* shape, const grpo_norm_opts* opts, void* y, float* row_scale, void* sum_out,
+                  const grpo_ckpt* sum_ckpt, grpo_stream_t stream);
+
+/* Gradients of the norm at s, for a loss with the gradients dy in y and dsum in s
+ * on its other way:
+ *   dx = rstd (g - s rstd^2 mean(g s)) + dsum, g = dy weight, rstd = 1 / sqrt(mean(s^2) + eps)
+ *   dweight = the sum over the rows of dy s rstd
+ *   dy [N x d]; x, x_ckpt: s in 16 bits or as a checkpoint, exactly one
+ *   dsum: NULL or [N x d]
+ *   workspace: >= grpo_norm_workspace_bytes(shape) bytes, 256-byte aligned
+ *   dx [N x d] (written): the gradient in x and in residual
+ *   dweight: NULL (a frozen weight) or [d] of the weight's type, 16-byte aligned
+ *       (written)
+ *   found_inf [1] int32 <- 1 if a value of dx or dweight is not finite, else 0
+ * A loss scale in dy and dsum is one in dx and dweight. */
+int grpo_norm_bwd(const void* dy, const void* x, const grpo_ckpt* x_ckpt, const void* weight, const void* dsum,
+                  const uint8_t* mask, const grpo_shape* shape, const grpo_norm_opts* opts, void* workspace, size_t ws_bytes,
+                  void* dx, void* dweight, int32_t* found_inf, grpo_stream_t stream);
+
+/* A checkpoint of x [N x d], any d of a shape. */
+int grpo_ckpt_pack(const void* x, const uint8_t* mask, const grpo_shape* shape, const grpo_ckpt* out, grpo_stream_t stream);
+
+/* A checkpoint's values in 16 bits: x_out [N x d]. */
+int grpo_ckpt_unpack(const grpo_ckpt* ckpt, const uint8_t* mask, const grpo_shape* shape, void* x_out, grpo_stream_t stream);
+
 /* ---- diagnostics ------------------------------------------------------
  * Per-kernel device time.  While enabled, the library records a CUDA event
  * pair on the launching stream around every kernel it launches.
@@ -458,6 +568,9 @@ enum {
     GRPO_PROF_DH,
     GRPO_PROF_DW,
     GRPO_PROF_F8_PREP,   /* the 8-bit backward's group bounds and token sort */
+    GRPO_PROF_NORM,
+    GRPO_PROF_NORM_BWD,
+    GRPO_PROF_CKPT,      /* packing and unpacking of 8-bit checkpoints */
     GRPO_PROF_KINDS
 };
 int grpo_profile_enable(int on);

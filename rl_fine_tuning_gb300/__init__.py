@@ -23,17 +23,20 @@ __all__ = [
     "grpo_kernel_launches", "grpo_device_checks", "grpo_selftest_bounds_check", "grpo_selftest_wait_timeout",
     "PROF_KINDS", "GrpoClipOpts", "GrpoPairOpts", "HEAD_OPS", "PAIR_KINDS", "clip_opts", "pair_opts",
     "grpo_policy_workspace_bytes", "grpo_logprobs", "grpo_logprobs_bwd", "grpo_clip_loss_fwd", "grpo_clip_loss_fwd_bwd",
-    "grpo_pair_loss_fwd", "grpo_pair_loss_fwd_bwd",
+    "grpo_pair_loss_fwd", "grpo_pair_loss_fwd_bwd", "GrpoCkpt", "GrpoNormOpts", "CKPT_BLOCK", "norm_opts",
+    "grpo_norm_workspace_bytes", "grpo_norm_fwd", "grpo_norm_bwd", "grpo_ckpt_pack", "grpo_ckpt_unpack",
 ]
 
 # kernel kinds of the diagnostics interface, in the order of the GRPO_PROF_* enum
-PROF_KINDS = ("advantages", "mask", "index", "fwd", "merge", "clear", "gather", "dlogits", "dh", "dw", "f8_prep")
+PROF_KINDS = ("advantages", "mask", "index", "fwd", "merge", "clear", "gather", "dlogits", "dh", "dw", "f8_prep",
+              "norm", "norm_bwd", "ckpt")
 
 BF16, FP16, E4M3, E5M2 = 0, 1, 2, 3
 TOKEN_MEAN, SEQUENCE_MEAN = 0, 1
 # operators of grpo_policy_workspace_bytes, and kinds of preference loss
 HEAD_OPS = {"logp": 0, "logp_grad": 1, "clip": 2, "pair": 3}
 PAIR_KINDS = {"sigmoid": 0, "hinge": 1, "square": 2}
+CKPT_BLOCK = 64      # columns that share a scale of an 8-bit checkpoint
 OBJECTIVES = {"grpo": 0, "no_detach": 1, "reverse_kl_q": 2, "forward_kl": 3}
 
 
@@ -69,6 +72,17 @@ class GrpoPairOpts(ctypes.Structure):
                 ("dw_f32", ctypes.c_int)]
 
 
+class GrpoCkpt(ctypes.Structure):
+    """Mirror of grpo_ckpt in include/grpo.h."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class GrpoNormOpts(ctypes.Structure):
+    """Mirror of grpo_norm_opts in include/grpo.h."""
+    _fields_ = [("eps", ctypes.c_float), ("weight_f32", ctypes.c_int), ("plus_one", ctypes.c_int), ("y_type", ctypes.c_int),
+                ("y_scale", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -95,7 +109,7 @@ def load(build_if_missing: bool = False):
 def _declare(lib):
     """Argument and result types of every entry point of include/grpo.h."""
     p, i32, sz, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
-    sp = ctypes.POINTER(GrpoShape)
+    sp, ck = ctypes.POINTER(GrpoShape), ctypes.POINTER(GrpoCkpt)
     sigs = {
         "grpo_shape_init": ([sp, i32, i32, i32, i32, i32, i32], None),
         "grpo_workspace_bytes": ([sp], sz),
@@ -122,6 +136,12 @@ def _declare(lib):
         "grpo_pair_loss_fwd": ([p, p, p, p, p, sp, ctypes.POINTER(GrpoPairOpts), p, sz, p, p, p, p, p], i32),
         "grpo_pair_loss_fwd_bwd": ([p, p, p, p, p, sp, ctypes.POINTER(GrpoPairOpts), f32, p, sz, p, p, p, p, p, p, p, p],
                                    i32),
+        "grpo_norm_opts_init": ([ctypes.POINTER(GrpoNormOpts), i32], None),
+        "grpo_norm_workspace_bytes": ([sp], sz),
+        "grpo_norm_fwd": ([p, ck, p, p, p, sp, ctypes.POINTER(GrpoNormOpts), p, p, p, ck, p], i32),
+        "grpo_norm_bwd": ([p, p, ck, p, p, p, sp, ctypes.POINTER(GrpoNormOpts), p, sz, p, p, p, p], i32),
+        "grpo_ckpt_pack": ([p, p, sp, ck, p], i32),
+        "grpo_ckpt_unpack": ([ck, p, sp, p, p], i32),
         "grpo_profile_enable": ([i32], i32),
         "grpo_profile_collect": ([ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_longlong), i32], i32),
         "grpo_kernel_launches": ([], ctypes.c_ulonglong),
@@ -447,3 +467,106 @@ def grpo_pair_loss_fwd_bwd(h, W, tokens, mask, logp_ref, shape, opts, loss_scale
                                          _arg(loss_out, "loss_out", f, 1), *g, _arg(logp_out, "logp_out", f, N),
                                          _arg(pair_stats, "pair_stats", f, 4 * shape.n_groups),
                                          _arg(status, "status", i, 1), _stream(stream)), "grpo_pair_loss_fwd_bwd")
+
+
+# ---------------------------------------------------------------- the norm before the head, 8-bit checkpoints
+# A checkpoint is a pair (codes, scales): int8 of N d elements, bfloat16 of N d / CKPT_BLOCK.  Tensors are checked as above,
+# and have to be on torch's current device.  None stands for what the C interface takes as NULL.
+
+_norm_types = None   # type name -> tuple of torch types
+
+
+def _norm_table(shape):
+    """(type tables, the 16-bit type, the current device's number)"""
+    global _norm_types
+    import torch
+    if _norm_types is None:
+        _norm_types = {**_types(), "codes": (torch.int8,), "scales": (torch.bfloat16,), "u8": (torch.uint8,),
+                       E4M3: (torch.float8_e4m3fn, torch.uint8), E5M2: (torch.float8_e5m2, torch.uint8)}
+    t = _norm_types.get(shape.dtype) if shape.dtype in (BF16, FP16) else None
+    if t is None:
+        raise GrpoError(5, "dtype check")
+    return _norm_types, t, torch.cuda.current_device()
+
+
+def _here(x, name, types, numel, device):
+    """As _arg, on the current device."""
+    if x is None or isinstance(x, int):
+        return x
+    if x.dtype in types and x.numel() == numel and x.is_contiguous() and x.is_cuda and x.get_device() == device:
+        return x.data_ptr()
+    raise ValueError(f"{name}: a contiguous tensor of {numel} elements of type {' or '.join(map(str, types))} on the current "
+                     f"CUDA device is wanted, not {x.dtype}, shape {tuple(x.shape)}, strides {x.stride()}, on {x.device}")
+
+
+def _ckpt(pair, name, n, ty, device):
+    codes, scales = pair
+    return GrpoCkpt(_here(codes, name + " codes", ty["codes"], n, device),
+                    _here(scales, name + " scales", ty["scales"], n // CKPT_BLOCK, device))
+
+
+def _source(src, n, ty, t, device):
+    """(x, x_ckpt) of a 16-bit matrix or a checkpoint"""
+    if isinstance(src, tuple):
+        return None, _ckpt(src, "checkpoint", n, ty, device)
+    return _here(src, "x", t, n, device), None
+
+
+def norm_opts(eps=1e-6, weight_f32=False, plus_one=False, y_type=BF16, y_scale=0.0) -> GrpoNormOpts:
+    o = GrpoNormOpts()
+    load().grpo_norm_opts_init(ctypes.byref(o), int(y_type))
+    o.eps, o.weight_f32, o.plus_one, o.y_scale = eps, int(bool(weight_f32)), int(bool(plus_one)), y_scale
+    return o
+
+
+def grpo_norm_workspace_bytes(shape: GrpoShape) -> int:
+    return int(load().grpo_norm_workspace_bytes(ctypes.byref(shape)))
+
+
+def grpo_norm_fwd(x, residual, weight, mask, shape, opts, y, row_scale=None, sum_out=None, sum_ckpt=None, stream=None):
+    """y (16 or 8 bits, as opts.y_type says) of s = x + residual; x may be a checkpoint (codes, scales)."""
+    ty, t, dev = _norm_table(shape)
+    N, d = shape.N, shape.d
+    n = N * d
+    px, pc = _source(x, n, ty, t, dev)
+    yt = t if opts.y_type == shape.dtype else ty.get(opts.y_type) if opts.y_type in (E4M3, E5M2) else None
+    if yt is None:
+        raise GrpoError(5, "y_type check")
+    out = None if sum_ckpt is None else _ckpt(sum_ckpt, "sum_ckpt", n, ty, dev)
+    f = ty["f32"]
+    _check(load().grpo_norm_fwd(px, pc, _here(residual, "residual", t, n, dev),
+                                _here(weight, "weight", f if opts.weight_f32 else t, d, dev),
+                                _here(mask, "mask", ty["mask"], N, dev), shape, opts, _here(y, "y", yt, n, dev),
+                                _here(row_scale, "row_scale", f, N, dev), _here(sum_out, "sum_out", t, n, dev), out,
+                                _stream(stream)), "grpo_norm_fwd")
+
+
+def grpo_norm_bwd(dy, x, weight, dsum, mask, shape, opts, workspace, dx, dweight, found_inf, stream=None):
+    """dx and dweight (None: frozen) at s = x, a 16-bit matrix or a checkpoint (codes, scales)."""
+    ty, t, dev = _norm_table(shape)
+    N, d = shape.N, shape.d
+    n = N * d
+    px, pc = _source(x, n, ty, t, dev)
+    wt = ty["f32"] if opts.weight_f32 else t
+    size = _nbytes(workspace)
+    _check(load().grpo_norm_bwd(_here(dy, "dy", t, n, dev), px, pc, _here(weight, "weight", wt, d, dev),
+                                _here(dsum, "dsum", t, n, dev), _here(mask, "mask", ty["mask"], N, dev), shape, opts,
+                                _here(workspace, "workspace", (workspace.dtype,), workspace.numel(), dev), size,
+                                _here(dx, "dx", t, n, dev), _here(dweight, "dweight", wt, d, dev),
+                                _here(found_inf, "found_inf", ty["i32"], 1, dev), _stream(stream)), "grpo_norm_bwd")
+
+
+def grpo_ckpt_pack(x, mask, shape, ckpt, stream=None):
+    """A checkpoint (codes, scales) of x."""
+    ty, t, dev = _norm_table(shape)
+    N, n = shape.N, shape.N * shape.d
+    _check(load().grpo_ckpt_pack(_here(x, "x", t, n, dev), _here(mask, "mask", ty["mask"], N, dev), shape,
+                                 _ckpt(ckpt, "ckpt", n, ty, dev), _stream(stream)), "grpo_ckpt_pack")
+
+
+def grpo_ckpt_unpack(ckpt, mask, shape, x_out, stream=None):
+    """A checkpoint's values in 16 bits."""
+    ty, t, dev = _norm_table(shape)
+    N, n = shape.N, shape.N * shape.d
+    _check(load().grpo_ckpt_unpack(_ckpt(ckpt, "ckpt", n, ty, dev), _here(mask, "mask", ty["mask"], N, dev), shape,
+                                   _here(x_out, "x_out", t, n, dev), _stream(stream)), "grpo_ckpt_unpack")

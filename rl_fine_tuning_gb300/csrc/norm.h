@@ -1,0 +1,67 @@
+// The norm before the head, its gradient, and 8-bit checkpoints of activations
+// (see "the norm before the head" in grpo.h): declarations shared by
+// norm_kernels.cu and norm_abi.cu.
+#pragma once
+#include "internal.h"
+
+namespace grpo {
+
+constexpr int kNormMaxD = 16384;       // widest row of the norm (a row stays in one CTA)
+constexpr int kNormParts = 456;        // most partial sums of the weight's gradient
+constexpr int kCkptBlock = GRPO_CKPT_BLOCK;
+constexpr float kLeastScale = 1.17549435e-38f;   // 2^-126: its reciprocal is finite, and neither is subnormal
+
+// s comes from x (+ residual), or from a checkpoint (codes, scales).
+struct NormParams {
+    const uint16_t* x;
+    const uint16_t* residual;
+    const int8_t* codes;
+    const uint16_t* scales;      // bf16, one for each kCkptBlock columns of a row
+    const void* weight;
+    const uint8_t* mask;         // nullable
+    int64_t N;
+    int d;
+    float eps;
+    int weight_f32;
+    float plus;                  // added to the weight: 0 or 1
+    int y_type;                  // grpo_dtype of y
+    float y_inv;                 // 1 / the given scale, 0: a scale per row
+    // outputs of the forward pass, null where not wanted
+    void* y;
+    float* row_scale;
+    uint16_t* sum;
+    int8_t* codes_out;
+    uint16_t* scales_out;
+    // the gradient
+    const uint16_t* dy;
+    const uint16_t* dsum;        // nullable
+    uint16_t* dx;
+    void* dweight;               // nullable
+    float* part;                 // [parts x d]
+    int* bad;                    // [parts] whether a part met a gradient that is not finite
+    int parts;
+    int* found_inf;
+};
+
+struct CkptParams {
+    const uint16_t* x;           // pack: the source; unpack: unused
+    uint16_t* x_out;
+    const int8_t* codes;
+    const uint16_t* scales;
+    int8_t* codes_out;
+    uint16_t* scales_out;
+    const uint8_t* mask;
+    int64_t N;
+    int d;
+};
+
+cudaError_t launch_norm_fwd(const NormParams& p, bool bf16, int sm_count, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormParams& p, bool bf16, int sm_count, cudaStream_t st);
+cudaError_t launch_norm_join(const NormParams& p, bool bf16, cudaStream_t st);
+cudaError_t launch_ckpt_pack(const CkptParams& p, bool bf16, int sm_count, cudaStream_t st);
+cudaError_t launch_ckpt_unpack(const CkptParams& p, bool bf16, int sm_count, cudaStream_t st);
+
+// Partial sums that a gradient of N rows takes (CTAs of launch_norm_bwd).
+int norm_parts(int64_t N, int d, int sm_count);
+
+}  // namespace grpo
