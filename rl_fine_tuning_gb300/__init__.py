@@ -474,26 +474,34 @@ def grpo_pair_loss_fwd_bwd(h, W, tokens, mask, logp_ref, shape, opts, loss_scale
 # and have to be on torch's current device.  None stands for what the C interface takes as NULL.
 
 _norm_types = None   # type name -> tuple of torch types
+_device = None       # torch's current device as a number
+_stream_of = None    # a device's current stream as a number
+
+
+def _norm_setup():
+    global _norm_types, _device, _stream_of
+    import torch
+    _norm_types = {**_types(), "codes": (torch.int8,), "scales": (torch.bfloat16,),
+                   E4M3: (torch.float8_e4m3fn, torch.uint8), E5M2: (torch.float8_e5m2, torch.uint8)}
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _stream_of = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                  or (lambda device: torch.cuda.current_stream(device).cuda_stream))
 
 
 def _norm_table(shape):
     """(type tables, the 16-bit type, the current device's number)"""
-    global _norm_types
-    import torch
     if _norm_types is None:
-        _norm_types = {**_types(), "codes": (torch.int8,), "scales": (torch.bfloat16,), "u8": (torch.uint8,),
-                       E4M3: (torch.float8_e4m3fn, torch.uint8), E5M2: (torch.float8_e5m2, torch.uint8)}
-    t = _norm_types.get(shape.dtype) if shape.dtype in (BF16, FP16) else None
-    if t is None:
+        _norm_setup()
+    if shape.dtype not in (BF16, FP16):
         raise GrpoError(5, "dtype check")
-    return _norm_types, t, torch.cuda.current_device()
+    return _norm_types, _norm_types[shape.dtype], _device()
 
 
 def _here(x, name, types, numel, device):
-    """As _arg, on the current device."""
+    """As _arg, on the current device (a tensor in host memory has the number -1)."""
     if x is None or isinstance(x, int):
         return x
-    if x.dtype in types and x.numel() == numel and x.is_contiguous() and x.is_cuda and x.get_device() == device:
+    if x.dtype in types and x.numel() == numel and x.get_device() == device and x.is_contiguous():
         return x.data_ptr()
     raise ValueError(f"{name}: a contiguous tensor of {numel} elements of type {' or '.join(map(str, types))} on the current "
                      f"CUDA device is wanted, not {x.dtype}, shape {tuple(x.shape)}, strides {x.stride()}, on {x.device}")
@@ -523,50 +531,54 @@ def grpo_norm_workspace_bytes(shape: GrpoShape) -> int:
     return int(load().grpo_norm_workspace_bytes(ctypes.byref(shape)))
 
 
+def _on(stream, device):
+    return _stream_of(device) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def grpo_norm_fwd(x, residual, weight, mask, shape, opts, y, row_scale=None, sum_out=None, sum_ckpt=None, stream=None):
     """y (16 or 8 bits, as opts.y_type says) of s = x + residual; x may be a checkpoint (codes, scales)."""
     ty, t, dev = _norm_table(shape)
     N, d = shape.N, shape.d
-    n = N * d
+    n, f, y_type = N * d, ty["f32"], opts.y_type
     px, pc = _source(x, n, ty, t, dev)
-    yt = t if opts.y_type == shape.dtype else ty.get(opts.y_type) if opts.y_type in (E4M3, E5M2) else None
+    yt = t if y_type == shape.dtype else ty[y_type] if y_type in (E4M3, E5M2) else None
     if yt is None:
         raise GrpoError(5, "y_type check")
-    out = None if sum_ckpt is None else _ckpt(sum_ckpt, "sum_ckpt", n, ty, dev)
-    f = ty["f32"]
     _check(load().grpo_norm_fwd(px, pc, _here(residual, "residual", t, n, dev),
                                 _here(weight, "weight", f if opts.weight_f32 else t, d, dev),
                                 _here(mask, "mask", ty["mask"], N, dev), shape, opts, _here(y, "y", yt, n, dev),
-                                _here(row_scale, "row_scale", f, N, dev), _here(sum_out, "sum_out", t, n, dev), out,
-                                _stream(stream)), "grpo_norm_fwd")
+                                _here(row_scale, "row_scale", f, N, dev), _here(sum_out, "sum_out", t, n, dev),
+                                None if sum_ckpt is None else _ckpt(sum_ckpt, "sum_ckpt", n, ty, dev), _on(stream, dev)),
+           "grpo_norm_fwd")
 
 
 def grpo_norm_bwd(dy, x, weight, dsum, mask, shape, opts, workspace, dx, dweight, found_inf, stream=None):
     """dx and dweight (None: frozen) at s = x, a 16-bit matrix or a checkpoint (codes, scales)."""
     ty, t, dev = _norm_table(shape)
     N, d = shape.N, shape.d
-    n = N * d
+    n, wt = N * d, ty["f32"] if opts.weight_f32 else t
     px, pc = _source(x, n, ty, t, dev)
-    wt = ty["f32"] if opts.weight_f32 else t
-    size = _nbytes(workspace)
+    size = workspace.numel()
     _check(load().grpo_norm_bwd(_here(dy, "dy", t, n, dev), px, pc, _here(weight, "weight", wt, d, dev),
                                 _here(dsum, "dsum", t, n, dev), _here(mask, "mask", ty["mask"], N, dev), shape, opts,
-                                _here(workspace, "workspace", (workspace.dtype,), workspace.numel(), dev), size,
+                                _here(workspace, "workspace", (workspace.dtype,), size, dev), size * workspace.element_size(),
                                 _here(dx, "dx", t, n, dev), _here(dweight, "dweight", wt, d, dev),
-                                _here(found_inf, "found_inf", ty["i32"], 1, dev), _stream(stream)), "grpo_norm_bwd")
+                                _here(found_inf, "found_inf", ty["i32"], 1, dev), _on(stream, dev)), "grpo_norm_bwd")
 
 
 def grpo_ckpt_pack(x, mask, shape, ckpt, stream=None):
     """A checkpoint (codes, scales) of x."""
     ty, t, dev = _norm_table(shape)
-    N, n = shape.N, shape.N * shape.d
+    N = shape.N
+    n = N * shape.d
     _check(load().grpo_ckpt_pack(_here(x, "x", t, n, dev), _here(mask, "mask", ty["mask"], N, dev), shape,
-                                 _ckpt(ckpt, "ckpt", n, ty, dev), _stream(stream)), "grpo_ckpt_pack")
+                                 _ckpt(ckpt, "ckpt", n, ty, dev), _on(stream, dev)), "grpo_ckpt_pack")
 
 
 def grpo_ckpt_unpack(ckpt, mask, shape, x_out, stream=None):
     """A checkpoint's values in 16 bits."""
     ty, t, dev = _norm_table(shape)
-    N, n = shape.N, shape.N * shape.d
+    N = shape.N
+    n = N * shape.d
     _check(load().grpo_ckpt_unpack(_ckpt(ckpt, "ckpt", n, ty, dev), _here(mask, "mask", ty["mask"], N, dev), shape,
-                                   _here(x_out, "x_out", t, n, dev), _stream(stream)), "grpo_ckpt_unpack")
+                                   _here(x_out, "x_out", t, n, dev), _on(stream, dev)), "grpo_ckpt_unpack")

@@ -7,7 +7,7 @@
 namespace grpo {
 
 constexpr int kNormMaxD = 16384;       // widest row of the norm (a row stays in one CTA)
-constexpr int kNormParts = 456;        // most partial sums of the weight's gradient
+constexpr int kNormParts = 1368;        // most partial sums of the weight's gradient
 constexpr int kCkptBlock = GRPO_CKPT_BLOCK;
 constexpr float kLeastScale = 1.17549435e-38f;   // 2^-126: its reciprocal is finite, and neither is subnormal
 
@@ -24,6 +24,7 @@ struct NormParams {
     float eps;
     int weight_f32;
     float plus;                  // added to the weight: 0 or 1
+    int width;                   // threads of a row
     int y_type;                  // grpo_dtype of y
     float y_inv;                 // 1 / the given scale, 0: a scale per row
     // outputs of the forward pass, null where not wanted
@@ -40,6 +41,7 @@ struct NormParams {
     float* part;                 // [parts x d]
     int* bad;                    // [parts] whether a part met a gradient that is not finite
     int parts;
+    int stages;                  // of the ring that rows are copied into
     int* found_inf;
 };
 
@@ -53,15 +55,22 @@ struct CkptParams {
     const uint8_t* mask;
     int64_t N;
     int d;
+    uint64_t per_row;            // ceil(2^64 / (d / 16)): the row of a unit by a product
 };
 
-cudaError_t launch_norm_fwd(const NormParams& p, bool bf16, int sm_count, cudaStream_t st);
-cudaError_t launch_norm_bwd(const NormParams& p, bool bf16, int sm_count, cudaStream_t st);
-cudaError_t launch_norm_join(const NormParams& p, bool bf16, cudaStream_t st);
-cudaError_t launch_ckpt_pack(const CkptParams& p, bool bf16, int sm_count, cudaStream_t st);
-cudaError_t launch_ckpt_unpack(const CkptParams& p, bool bf16, int sm_count, cudaStream_t st);
+// How a row is dealt to threads, and rows to blocks.
+struct NormPlan {
+    int width, upt;              // threads of a row, and units of 16 elements that each has
+    int threads, grid, per_sm;   // of a block; blocks, and how many of them an SM is to have
+    bool wide;                   // a row takes whole warps (else some lanes of one)
+};
+NormPlan norm_fwd_plan(int64_t N, int d, int sm_count);
+NormPlan norm_bwd_plan(int64_t N, int d, int sm_count, bool ckpt, bool dsum);
 
-// Partial sums that a gradient of N rows takes (CTAs of launch_norm_bwd).
-int norm_parts(int64_t N, int d, int sm_count);
+cudaError_t launch_norm_fwd(const NormParams& p, const NormPlan& o, bool bf16, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormParams& p, const NormPlan& o, bool bf16, cudaStream_t st);
+cudaError_t launch_norm_join(const NormParams& p, bool bf16, cudaStream_t st);
+cudaError_t launch_ckpt_pack(const CkptParams& p, bool bf16, cudaStream_t st);
+cudaError_t launch_ckpt_unpack(const CkptParams& p, bool bf16, cudaStream_t st);
 
 }  // namespace grpo

@@ -10,6 +10,8 @@ namespace grpo {
 
 namespace {
 
+constexpr size_t kMatrixAlign = 32;    // of a 16-bit matrix: its 32-byte sectors are loaded and stored whole
+
 // What the gradient's workspace holds: sums of the weight's gradient, and flags.
 struct NormWs {
     size_t part, bad, total;
@@ -22,6 +24,20 @@ NormWs norm_ws(int64_t N, int d) {
     w.bad = align_up(static_cast<size_t>(parts) * d * 4, 256);
     w.total = w.bad + align_up(static_cast<size_t>(parts) * 4, 256);
     return w;
+}
+
+// The current device's SMs; a device is asked once (its attributes take a microsecond a call).
+int sm_count(int* out) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return GRPO_ERR_LAUNCH;
+    if (dev < 64 && (*out = known[dev].load(std::memory_order_relaxed)) > 0) return GRPO_OK;
+    DeviceInfo info;
+    const int rc = device_info(&info);
+    if (rc != GRPO_OK) return rc;
+    *out = info.sm_count;
+    if (dev < 64) known[dev].store(info.sm_count, std::memory_order_relaxed);
+    return GRPO_OK;
 }
 
 int norm_shape(const grpo_shape* s, int most_d) {
@@ -53,7 +69,7 @@ bool ckpt_ok(const grpo_ckpt* c) { return given(c->codes, 16) && given(c->scales
 
 // s comes from exactly one of x and a checkpoint
 bool source_ok(const void* x, const grpo_ckpt* c) {
-    if (x) return !c && aligned(x, 16);
+    if (x) return !c && aligned(x, kMatrixAlign);
     return c && ckpt_ok(c);
 }
 
@@ -79,12 +95,12 @@ NormParams norm_params(const grpo_shape& s, const grpo_norm_opts& o, const void*
     return p;
 }
 
-int launch_as(int kind, cudaStream_t st, cudaError_t (*f)(const CkptParams&, bool, int, cudaStream_t), const CkptParams& p,
+int launch_as(int kind, cudaStream_t st, cudaError_t (*f)(const CkptParams&, bool, cudaStream_t), const CkptParams& p,
               bool bf16) {
-    DeviceInfo dev;
-    const int rc = device_info(&dev);
+    int sms = 0;
+    const int rc = sm_count(&sms);
     if (rc != GRPO_OK) return rc;
-    return launch(kind, st, [&] { return f(p, bf16, dev.sm_count, st); }) == cudaSuccess ? GRPO_OK : GRPO_ERR_LAUNCH;
+    return launch(kind, st, [&] { return f(p, bf16, st); }) == cudaSuccess ? GRPO_OK : GRPO_ERR_LAUNCH;
 }
 
 CkptParams ckpt_params(const grpo_shape& s, const uint8_t* mask) {
@@ -92,6 +108,7 @@ CkptParams ckpt_params(const grpo_shape& s, const uint8_t* mask) {
     p.mask = mask;
     p.N = static_cast<int64_t>(s.n_groups) * s.G * s.L;
     p.d = s.d;
+    p.per_row = ~0ull / static_cast<uint64_t>(s.d / 16) + 1;
     return p;
 }
 
@@ -122,13 +139,13 @@ int grpo_norm_fwd(const void* x, const grpo_ckpt* x_ckpt, const void* residual, 
     if (rc == GRPO_OK) rc = norm_opts_check(*shape, opts, true);
     if (rc != GRPO_OK) return rc;
     const bool y16 = opts->y_type == shape->dtype;
-    if (!source_ok(x, x_ckpt) || !left_or(residual, 16) || !given(weight, 16) || !given(y, 16) || !left_or(row_scale, 4) ||
-        !left_or(sum_out, 16) || (sum_ckpt && !ckpt_ok(sum_ckpt)))
+    if (!source_ok(x, x_ckpt) || !left_or(residual, kMatrixAlign) || !given(weight, 16) || !given(y, y16 ? kMatrixAlign : 16) || !left_or(row_scale, 4) ||
+        !left_or(sum_out, kMatrixAlign) || (sum_ckpt && !ckpt_ok(sum_ckpt)))
         return GRPO_ERR_POINTER;
     if (x_ckpt && (residual || sum_ckpt)) return GRPO_ERR_POINTER;
     if (y16 ? row_scale != nullptr : !row_scale && opts->y_scale == 0.f) return GRPO_ERR_POINTER;
-    DeviceInfo dev;
-    rc = device_info(&dev);
+    int sms = 0;
+    rc = sm_count(&sms);
     if (rc != GRPO_OK) return rc;
     NormParams p = norm_params(*shape, *opts, weight, mask);
     set_source(&p, x, x_ckpt);
@@ -141,7 +158,9 @@ int grpo_norm_fwd(const void* x, const grpo_ckpt* x_ckpt, const void* residual, 
         p.scales_out = sum_ckpt->scales;
     }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return launch(GRPO_PROF_NORM, st, [&] { return launch_norm_fwd(p, shape->dtype == GRPO_BF16, dev.sm_count, st); }) ==
+    const NormPlan plan = norm_fwd_plan(p.N, p.d, sms);
+    p.width = plan.width;
+    return launch(GRPO_PROF_NORM, st, [&] { return launch_norm_fwd(p, plan, shape->dtype == GRPO_BF16, st); }) ==
                    cudaSuccess
                ? GRPO_OK
                : GRPO_ERR_LAUNCH;
@@ -153,14 +172,14 @@ int grpo_norm_bwd(const void* dy, const void* x, const grpo_ckpt* x_ckpt, const 
     int rc = norm_shape(shape, kNormMaxD);
     if (rc == GRPO_OK) rc = norm_opts_check(*shape, opts, false);
     if (rc != GRPO_OK) return rc;
-    if (!given(dy, 16) || !source_ok(x, x_ckpt) || !given(weight, 16) || !left_or(dsum, 16) || !given(workspace, 256) ||
-        !given(dx, 16) || !left_or(dweight, 16) || !given(found_inf, 4))
+    if (!given(dy, kMatrixAlign) || !source_ok(x, x_ckpt) || !given(weight, 16) || !left_or(dsum, kMatrixAlign) || !given(workspace, 256) ||
+        !given(dx, kMatrixAlign) || !left_or(dweight, 16) || !given(found_inf, 4))
         return GRPO_ERR_POINTER;
     NormParams p = norm_params(*shape, *opts, weight, mask);
     const NormWs w = norm_ws(p.N, p.d);
     if (ws_bytes < w.total) return GRPO_ERR_WORKSPACE;
-    DeviceInfo dev;
-    rc = device_info(&dev);
+    int sms = 0;
+    rc = sm_count(&sms);
     if (rc != GRPO_OK) return rc;
     set_source(&p, x, x_ckpt);
     p.dy = static_cast<const uint16_t*>(dy);
@@ -169,11 +188,14 @@ int grpo_norm_bwd(const void* dy, const void* x, const grpo_ckpt* x_ckpt, const 
     p.dweight = dweight;
     p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.part);
     p.bad = reinterpret_cast<int*>(static_cast<char*>(workspace) + w.bad);
-    p.parts = norm_parts(p.N, p.d, dev.sm_count);
+    NormPlan plan = norm_bwd_plan(p.N, p.d, sms, x_ckpt != nullptr, dsum != nullptr);
+    if (plan.grid > kNormParts) plan.grid = kNormParts;
+    p.width = plan.width;
+    p.parts = plan.grid;
     p.found_inf = found_inf;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = shape->dtype == GRPO_BF16;
-    if (launch(GRPO_PROF_NORM_BWD, st, [&] { return launch_norm_bwd(p, bf16, dev.sm_count, st); }) != cudaSuccess ||
+    if (launch(GRPO_PROF_NORM_BWD, st, [&] { return launch_norm_bwd(p, plan, bf16, st); }) != cudaSuccess ||
         launch(GRPO_PROF_NORM_BWD, st, [&] { return launch_norm_join(p, bf16, st); }) != cudaSuccess)
         return GRPO_ERR_LAUNCH;
     return GRPO_OK;
@@ -182,7 +204,7 @@ int grpo_norm_bwd(const void* dy, const void* x, const grpo_ckpt* x_ckpt, const 
 int grpo_ckpt_pack(const void* x, const uint8_t* mask, const grpo_shape* shape, const grpo_ckpt* out, grpo_stream_t stream) {
     const int rc = norm_shape(shape, 65536);
     if (rc != GRPO_OK) return rc;
-    if (!given(x, 16) || !out || !ckpt_ok(out)) return GRPO_ERR_POINTER;
+    if (!given(x, kMatrixAlign) || !out || !ckpt_ok(out)) return GRPO_ERR_POINTER;
     CkptParams p = ckpt_params(*shape, mask);
     p.x = static_cast<const uint16_t*>(x);
     p.codes_out = out->codes;
@@ -193,7 +215,7 @@ int grpo_ckpt_pack(const void* x, const uint8_t* mask, const grpo_shape* shape, 
 int grpo_ckpt_unpack(const grpo_ckpt* ckpt, const uint8_t* mask, const grpo_shape* shape, void* x_out, grpo_stream_t stream) {
     const int rc = norm_shape(shape, 65536);
     if (rc != GRPO_OK) return rc;
-    if (!ckpt || !ckpt_ok(ckpt) || !given(x_out, 16)) return GRPO_ERR_POINTER;
+    if (!ckpt || !ckpt_ok(ckpt) || !given(x_out, kMatrixAlign)) return GRPO_ERR_POINTER;
     CkptParams p = ckpt_params(*shape, mask);
     p.codes = ckpt->codes;
     p.scales = ckpt->scales;

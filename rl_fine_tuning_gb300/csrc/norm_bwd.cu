@@ -1,0 +1,406 @@
+// The gradient of the norm before the head (see norm_abi.cu for its entry point).
+//
+// As the forward pass, it moves bytes: a row of dy and of s is read once and
+// stays in registers between its two sums and dx, while the next row's loads are
+// under way.  The weight's gradient is summed in registers from row to row.
+#include "norm_device.cuh"
+
+namespace grpo {
+
+namespace {
+
+constexpr int kBwdRegs = 80, kBwdRegsTwo = 128;      // of a thread with one or two units: 768 or 512 threads an SM
+constexpr int kStagesMax = 3;
+constexpr int kSmemSm = 226 * 1024;    // of an SM's 228 KB
+
+// Both sums over a row's threads, in a fixed order; every thread gets them.  A
+// block's warps leave theirs in s, of which the next row takes the other half, so
+// that one barrier is enough; entries of warps that are not there hold 0.  There
+// the lower lanes of a warp join a, the upper ones b.
+__device__ __forceinline__ float2 warp_sums(float a, float b, int width) {
+    for (int o = width / 2; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    return make_float2(a, b);
+}
+
+__device__ __forceinline__ float2 block_sums(float a, float b, float* s) {
+    const bool upper = threadIdx.x & 16;
+    float v = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 15) == 0) s[threadIdx.x >> 4] = v;
+    __syncthreads();
+    F2 sum = 0;
+    for (unsigned i = 0; i < blockDim.x; i += 64) {
+        const float4 x = *reinterpret_cast<const float4*>(s + i / 16);
+        sum = f2_add(f2_add(sum, f2(x.x, x.y)), f2(x.z, x.w));
+    }
+    return f2_values(sum);
+}
+
+// A unit's part of both sums: s^2, and s (dy w).
+template <bool kBf16>
+__device__ __forceinline__ float2 unit_sums(const Unit& s, const Unit& dy, const Unit32& w) {
+    const Unit32 v = values<kBf16>(s), g = values<kBf16>(dy);
+    F2 a = 0, b = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        a = f2_fma(v.p[j], v.p[j], a);
+        b = f2_fma(v.p[j], f2_mul(g.p[j], w.p[j]), b);
+    }
+    return make_float2(sum_of(a), sum_of(b));
+}
+
+// dx = rstd dy w - s rstd^3 mean(dy w s) + dsum of a unit, and its dy s rstd added to acc.  c2: the factor of s.
+template <bool kBf16, bool kDsum>
+__device__ __forceinline__ Unit unit_grad(Unit s, Unit dy, const Unit& ds, const Unit32& w, F2 rstd2, F2 c2, F2 (&acc)[8]) {
+    forget_values(&s);
+    forget_values(&dy);
+    const Unit32 v = values<kBf16>(s);
+    Unit32 g = values<kBf16>(dy), x = {};
+    if (kDsum) x = values<kBf16>(ds);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        g.p[j] = f2_mul(g.p[j], rstd2);
+        acc[j] = f2_fma(g.p[j], v.p[j], acc[j]);
+        x.p[j] = kDsum ? f2_fma(g.p[j], w.p[j], x.p[j]) : f2_mul(g.p[j], w.p[j]);
+        x.p[j] = f2_fma(v.p[j], c2, x.p[j]);
+    }
+    return rounded<kBf16>(x);
+}
+
+// A pair that turns NaN with the first value that is not finite.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t mark_bad(uint32_t bad, const Unit& x) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) bad = pair_fma<kBf16>(x.w[j], 0u, bad);
+    return bad;
+}
+template <bool kBf16>
+__device__ __forceinline__ bool is_bad(uint32_t bad) {
+    const float2 v = pair_values<kBf16>(bad);
+    return !(v.x == 0.f && v.y == 0.f);
+}
+
+__device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(to)),
+                 "l"(from), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// Rows of more than 1024 columns: a block takes a row at a time, and copies the rows to
+// come into a ring of p.stages stages in shared memory, one bulk copy a matrix.  Block b
+// leaves its sum of dy s rstd of every column in part[b].
+// A wait that runs out of time leaves garbage in its row; the block goes on, and found_inf says so.
+template <bool kBf16, int kSrc, int kUpt, bool kDsum>
+__global__ void __maxnreg__(kUpt == 1 ? kBwdRegs : kBwdRegsTwo) k_norm_bwd_wide(const NormParams p) {
+    __shared__ alignas(16) float s_join[2][kBlockMax / 16];
+    __shared__ uint64_t s_full[kStagesMax];
+    __shared__ int s_abort;
+    extern __shared__ float4 s_weight[];
+    const int n_unit = p.d / kUnit, width = static_cast<int>(blockDim.x), pad = width * kUpt;
+    const int lane = static_cast<int>(threadIdx.x);
+    const uint32_t N = static_cast<uint32_t>(p.N), step = gridDim.x;      // N < 2^31
+    const float inv_d = 1.f / p.d;
+    chain_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.found_inf = 0;
+
+    // a stage: dy, x or the codes, dsum
+    constexpr int kSrcBytes = kSrc == kCkpt ? 1 : 2;
+    const uint32_t matrix = pad * kUnit * 2, stage = matrix / 2 * (2 + kSrcBytes + (kDsum ? 2 : 0));
+    char* ring = reinterpret_cast<char*>(s_weight + 4 * pad);
+    auto copy_row = [&](int64_t at, int q) {                              // one thread
+        char* to = ring + q * stage;
+        mbar_arrive_expect_tx(&s_full[q], p.d * (2 + kSrcBytes + (kDsum ? 2 : 0)));
+        bulk_load(to, p.dy + at, p.d * 2, &s_full[q]);
+        if (kSrc == kCkpt)
+            bulk_load(to + matrix, p.codes + at, p.d, &s_full[q]);
+        else
+            bulk_load(to + matrix, p.x + at, p.d * 2, &s_full[q]);
+        if (kDsum) bulk_load(to + matrix + matrix / 2 * kSrcBytes, p.dsum + at, p.d * 2, &s_full[q]);
+    };
+    uint32_t t = blockIdx.x;
+    int64_t at = static_cast<int64_t>(t) * p.d;
+    const int64_t at_step = static_cast<int64_t>(step) * p.d;
+    Ahead ahead;
+    ahead.begin(p, t, step, 32);
+    uint32_t alive = ahead.bits(32);           // bit q: row t + q step counts
+    if (threadIdx.x == 0) {
+        for (int q = 0; q < p.stages; ++q) mbar_init(&s_full[q], 1);
+        s_abort = 0;
+        fence_barrier_init();
+        for (int q = 0; q < p.stages; ++q)
+            if (alive >> q & 1) copy_row(at + q * at_step, q);
+    }
+    uint32_t scale[kUpt] = {};                 // (checkpoint) of the next row
+    auto load_scales = [&](int64_t at, bool on) {
+#pragma unroll
+        for (int k = 0; k < (kSrc == kCkpt ? kUpt : 0); ++k) {
+            const int i = lane + k * width;
+            scale[k] = load_scale(p.scales + at / kCkptBlock + i / (kCkptBlock / kUnit), on && i < n_unit);
+        }
+    };
+    load_scales(at, alive & 1);
+    F2 acc[kUpt][8];
+#pragma unroll
+    for (int k = 0; k < kUpt; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[k][j] = 0;
+    uint32_t bad = 0, phase = 0;
+    stage_weight<kBf16>(p, s_weight, pad);
+    if (threadIdx.x < 2 * kBlockMax / 16) s_join[0][threadIdx.x] = 0.f;
+    __syncthreads();
+    int q = 0, turn = 0;
+    for (; t < N; t += step, at += at_step) {
+        const bool live = alive & 1, far = alive >> p.stages & 1;
+        ahead.advance(p, t, step, 32);
+        alive = ahead.bits(32);
+        Unit s[kUpt], dy[kUpt], ds[kDsum ? kUpt : 1];
+        float2 sums = make_float2(0.f, 0.f);
+        if (live) {
+            mbar_wait(&s_full[q], phase >> q & 1, &s_abort, nullptr);
+            phase ^= 1u << q;
+            const uint32_t from = smem_u32(ring) + q * stage;
+#pragma unroll
+            for (int k = 0; k < kUpt; ++k) {
+                const uint32_t i = lane + k * width;
+                dy[k] = read_unit(from + i * (kUnit * 2));
+                if (kSrc == kCkpt)
+                    s[k] = decode<kBf16>(read16(from + matrix + i * kUnit), bf16_value(scale[k]));
+                else
+                    s[k] = read_unit(from + matrix + i * (kUnit * 2));
+                if (kDsum) ds[k] = read_unit(from + matrix + matrix / 2 * kSrcBytes + i * (kUnit * 2));
+            }
+        }
+        load_scales(at + at_step, alive & 1);
+        if (live) {
+#pragma unroll
+            for (int k = 0; k < kUpt; ++k) {
+                const float2 u = unit_sums<kBf16>(s[k], dy[k], staged_weight(s_weight, pad, lane + k * width));
+                if (lane + k * width < n_unit) sums = make_float2(sums.x + u.x, sums.y + u.y);
+            }
+            sums = block_sums(sums.x, sums.y, s_join[turn]);
+            turn ^= 1;
+        }
+        // the whole block has read stage q: of this row above, or of the last one that was in it
+        if (threadIdx.x == 0 && far && !s_abort) copy_row(at + p.stages * at_step, q);
+        q = q + 1 == p.stages ? 0 : q + 1;
+        const float rstd = rsqrtf(sums.x * inv_d + p.eps);
+        const float c = -(rstd * rstd) * (sums.y * inv_d) * rstd;
+        const F2 rstd2 = f2(rstd, rstd), c2 = f2(c, c);
+#pragma unroll
+        for (int k = 0; k < kUpt; ++k) {
+            const int i = lane + k * width;
+            Unit out = {};
+            if (live) out = unit_grad<kBf16, kDsum>(s[k], dy[k], ds[kDsum ? k : 0], staged_weight(s_weight, pad, i), rstd2, c2, acc[k]);
+            if (i < n_unit) {
+                bad = mark_bad<kBf16>(bad, out);
+                store_unit(p.dx + at + i * kUnit, out);
+            }
+        }
+    }
+
+    chain_next();
+    const int any = __syncthreads_or(is_bad<kBf16>(bad) || s_abort);
+    abort_grace(&s_abort);
+    if (threadIdx.x == 0) p.bad[blockIdx.x] = any;
+    if (!p.dweight) return;
+    float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.d;
+#pragma unroll
+    for (int k = 0; k < kUpt; ++k) {
+        const int i = lane + k * width;
+        if (i >= n_unit) break;
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 v = f2_values(acc[k][j]);
+            w[2 * j] = __float_as_uint(v.x);
+            w[2 * j + 1] = __float_as_uint(v.y);
+        }
+        st_global_v8(part + i * kUnit, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+        st_global_v8(part + i * kUnit + 8, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
+    }
+}
+
+// Rows of up to 1024 columns: 4, 16 or 32 lanes of a warp take a row at a time; the next
+// row's loads are under way while one is worked on.
+template <bool kBf16, int kSrc, int kUpt, bool kDsum>
+__global__ void __launch_bounds__(kWarpThreads) k_norm_bwd_rows(const NormParams p) {
+    extern __shared__ float4 s_weight[];       // and at the end the warps' sums of dw
+    const int n_unit = p.d / kUnit, width = p.width, pad = width * kUpt;
+    const int lane = static_cast<int>(threadIdx.x) & (width - 1);
+    const uint32_t rows = kWarpThreads / width, mine = threadIdx.x / width;        // rows that a block works on at once
+    const uint32_t step = gridDim.x * rows, N = static_cast<uint32_t>(p.N);
+    const float inv_d = 1.f / p.d;
+    chain_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.found_inf = 0;
+
+    F2 acc[kUpt][8];
+#pragma unroll
+    for (int k = 0; k < kUpt; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[k][j] = 0;
+    uint32_t bad = 0;
+    Raw<kSrc, kUpt> raw;
+    Unit raw_dy[kUpt], raw_ds[kDsum ? kUpt : 1];
+    uint32_t t = blockIdx.x * rows + mine;
+    int64_t at = static_cast<int64_t>(t) * p.d + lane * kUnit;         // the thread's first element of row t
+    const int64_t at_step = static_cast<int64_t>(step) * p.d;
+    auto load = [&](int64_t at, bool on) {
+        load_row<kSrc, kUpt, false>(p, at, on, lane, width, n_unit, &raw);
+#pragma unroll
+        for (int k = 0; k < kUpt; ++k) {
+            const bool in = on && lane + k * width < n_unit;
+            raw_dy[k] = load_unit(p.dy + at + k * width * kUnit, in);
+            if (kDsum) raw_ds[k] = load_unit(p.dsum + at + k * width * kUnit, in);
+        }
+    };
+    Ahead ahead;
+    ahead.begin(p, t, step, width);
+    uint32_t alive = ahead.bits(width);        // bit q: row t + q step counts
+    load(at, alive & 1);
+    stage_weight<kBf16>(p, s_weight, pad);
+    __syncthreads();
+    for (uint32_t base = blockIdx.x * rows; base < N; base += step, t += step, at += at_step) {   // whole blocks go round together
+        const bool live = alive & 1, next = alive >> 1 & 1;
+        ahead.advance(p, t, step, width);
+        alive = ahead.bits(width);
+        Unit s[kUpt], dy[kUpt], ds[kDsum ? kUpt : 1];
+#pragma unroll
+        for (int k = 0; k < kUpt; ++k) {
+            s[k] = stream_of<kBf16>(raw, k);
+            dy[k] = raw_dy[k];
+            if (kDsum) ds[k] = raw_ds[k];
+        }
+        load(at + at_step, next);
+        float2 sums = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kUpt; ++k) {
+            const float2 u = unit_sums<kBf16>(s[k], dy[k], staged_weight(s_weight, pad, lane + k * width));
+            sums = make_float2(sums.x + u.x, sums.y + u.y);
+        }
+        sums = warp_sums(sums.x, sums.y, width);
+        const float rstd = rsqrtf(sums.x * inv_d + p.eps);
+        const float c = -(rstd * rstd) * (sums.y * inv_d) * rstd;
+        const F2 rstd2 = f2(rstd, rstd), c2 = f2(c, c);
+#pragma unroll
+        for (int k = 0; k < kUpt; ++k) {
+            const int i = lane + k * width;
+            Unit out = unit_grad<kBf16, kDsum>(s[k], dy[k], ds[kDsum ? k : 0], staged_weight(s_weight, pad, i), rstd2, c2, acc[k]);
+            if (!live) out = Unit{};                     // not 0 times a weight that is not finite
+            if (t < N && i < n_unit) {
+                bad = mark_bad<kBf16>(bad, out);
+                store_unit(p.dx + at + k * width * kUnit, out);
+            }
+        }
+    }
+
+    chain_next();
+    const int any = __syncthreads_or(is_bad<kBf16>(bad));
+    if (threadIdx.x == 0) p.bad[blockIdx.x] = any;
+    if (!p.dweight) return;
+    // the rows of a warp, then the warps of the block, in this order; in the weight's place
+    float* s_dw = reinterpret_cast<float*>(s_weight);
+    const int warp = threadIdx.x >> 5, wide = pad * kUnit;
+#pragma unroll
+    for (int k = 0; k < kUpt; ++k) {
+        const int i = lane + k * width;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float2 v = f2_values(acc[k][j]);
+            for (int o = width; o < 32; o <<= 1) {
+                v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+                v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+            }
+            // the pairs of a unit lie pad pairs apart: neighbouring lanes write neighbouring pairs
+            if ((threadIdx.x & 31) < width) *reinterpret_cast<float2*>(s_dw + warp * wide + (j * pad + i) * 2) = v;
+        }
+    }
+    __syncthreads();
+    float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.d;
+    for (int j = threadIdx.x; j < p.d / 2; j += kWarpThreads) {        // pair j % 8 of unit j / 8
+        F2 v = 0;
+        for (int w = 0; w < kWarpThreads / 32; ++w)
+            v = f2_add(v, *reinterpret_cast<const F2*>(s_dw + w * wide + ((j & 7) * pad + (j >> 3)) * 2));
+        *reinterpret_cast<F2*>(part + 2 * j) = v;
+    }
+}
+
+// Writes dw of column j; true if it is not finite.
+template <bool kBf16>
+__device__ __forceinline__ bool store_dweight(const NormParams& p, int j, float v) {
+    if (p.weight_f32) {
+        static_cast<float*>(p.dweight)[j] = v;
+    } else {
+        const uint32_t r = pair_bits<kBf16>(v, 0.f);
+        static_cast<uint16_t*>(p.dweight)[j] = static_cast<uint16_t>(r);
+        v = pair_values<kBf16>(r).x;
+    }
+    return !(fabsf(v) <= FLT_MAX);
+}
+
+// dw and found_inf from the parts.  A block takes 32 columns, each of its 32 warps every 32nd part.
+constexpr int kJoinCols = 32, kJoinWarps = 32;
+
+template <bool kBf16>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_norm_join(const NormParams p) {
+    __shared__ float s_part[kJoinWarps][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int j = blockIdx.x * kJoinCols + lane;
+    bool bad = false;
+    chain_wait();
+    if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b < p.parts; b += 32 * kJoinWarps) bad |= p.bad[b] != 0;
+    if (p.dweight) {
+        float v = 0.f;
+#pragma unroll 8
+        for (int b = warp; b < p.parts; b += kJoinWarps) v += p.part[static_cast<int64_t>(b) * p.d + j];
+        s_part[warp][lane] = v;
+        __syncthreads();
+        v = s_part[lane][warp];            // the block's column `warp`
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) bad |= store_dweight<kBf16>(p, blockIdx.x * kJoinCols + warp, v);
+    }
+    if (bad) *p.found_inf = 1;             // 0 before: k_norm_bwd
+}
+
+template <bool kBf16, int kSrc, bool kDsum>
+cudaError_t bwd_of(const NormParams& p, const NormPlan& o, cudaStream_t st) {
+    const size_t weight = static_cast<size_t>(o.width) * o.upt * kUnit * 4;
+    if (!o.wide) {                             // 16 KB at most: d <= 1024
+        const auto f = o.upt == 1 ? k_norm_bwd_rows<kBf16, kSrc, 1, kDsum> : k_norm_bwd_rows<kBf16, kSrc, 2, kDsum>;
+        return launch_chained(f, o.grid, o.threads, weight * (kWarpThreads / 32), p, st);
+    }
+    const auto f = o.upt == 1 ? k_norm_bwd_wide<kBf16, kSrc, 1, kDsum> : k_norm_bwd_wide<kBf16, kSrc, 2, kDsum>;
+    const size_t stage = weight / 4 * (2 + (kSrc == kCkpt ? 1 : 2) + (kDsum ? 2 : 0));
+    NormParams r = p;
+    const size_t room = static_cast<size_t>(kSmemSm) / o.per_sm - 2048;
+    if (room < weight + stage) return cudaErrorInvalidConfiguration;
+    r.stages = static_cast<int>((room - weight) / stage);
+    if (r.stages > kStagesMax) r.stages = kStagesMax;
+    const size_t smem = weight + r.stages * stage;
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    return launch_chained(f, o.grid, o.threads, smem, r, st);
+}
+
+template <bool kBf16, int kSrc>
+cudaError_t bwd_as(const NormParams& p, const NormPlan& o, cudaStream_t st) {
+    return p.dsum ? bwd_of<kBf16, kSrc, true>(p, o, st) : bwd_of<kBf16, kSrc, false>(p, o, st);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_bwd(const NormParams& p, const NormPlan& o, bool bf16, cudaStream_t st) {
+    if (p.codes) return bf16 ? bwd_as<true, kCkpt>(p, o, st) : bwd_as<false, kCkpt>(p, o, st);
+    return bf16 ? bwd_as<true, kX>(p, o, st) : bwd_as<false, kX>(p, o, st);
+}
+
+cudaError_t launch_norm_join(const NormParams& p, bool bf16, cudaStream_t st) {
+    return launch_chained(bf16 ? k_norm_join<true> : k_norm_join<false>, p.dweight ? p.d / kJoinCols : 1, 32 * kJoinWarps, 0,
+                          p, st);
+}
+
+}  // namespace grpo
