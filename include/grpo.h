@@ -499,8 +499,9 @@ typedef struct {
 
 void grpo_norm_opts_init(grpo_norm_opts* o, grpo_dtype dtype);
 
-/* Bytes of device workspace of grpo_norm_bwd: 4 d for each of up to 456 partial
- * sums, and their flags.  0 for an invalid shape. */
+/* Bytes of device workspace of grpo_norm_bwd: 4 d for each of up to 8 partial
+ * sums an SM, and their flags (7.5 MB for many rows of 4096).  0 for an invalid
+ * shape. */
 size_t grpo_norm_workspace_bytes(const grpo_shape* shape);
 
 /* Root-mean-square norm.  d is at most 16384 (GRPO_ERR_SHAPE above).

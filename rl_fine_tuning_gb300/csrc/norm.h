@@ -7,7 +7,8 @@
 namespace grpo {
 
 constexpr int kNormMaxD = 16384;       // widest row of the norm (a row stays in one CTA)
-constexpr int kNormParts = 1368;        // most partial sums of the weight's gradient
+constexpr int kSmCount = 152;          // of a GB300: what the gradient's workspace is sized for
+constexpr int kClusterMax = 8;
 constexpr int kCkptBlock = GRPO_CKPT_BLOCK;
 constexpr float kLeastScale = 1.17549435e-38f;   // 2^-126: its reciprocal is finite, and neither is subnormal
 
@@ -41,6 +42,7 @@ struct NormParams {
     float* part;                 // [parts x d]
     int* bad;                    // [parts] whether a part met a gradient that is not finite
     int parts;
+    bool joined;                 // the blocks are one cluster and join their sums themselves
     int stages;                  // of the ring that rows are copied into
     int* found_inf;
 };
@@ -63,9 +65,11 @@ struct NormPlan {
     int width, upt;              // threads of a row, and units of 16 elements that each has
     int threads, grid, per_sm;   // of a block; blocks, and how many of them an SM is to have
     bool wide;                   // a row takes whole warps (else some lanes of one)
+    bool joined = false;         // the blocks are one cluster (a power of two of them) and join their sums
 };
 NormPlan norm_fwd_plan(int64_t N, int d, int sm_count);
 NormPlan norm_bwd_plan(int64_t N, int d, int sm_count, bool ckpt, bool dsum);
+int norm_parts(int64_t N, int d);    // most blocks of norm_bwd_plan on kSmCount SMs
 
 cudaError_t launch_norm_fwd(const NormParams& p, const NormPlan& o, bool bf16, cudaStream_t st);
 cudaError_t launch_norm_bwd(const NormParams& p, const NormPlan& o, bool bf16, cudaStream_t st);

@@ -18,7 +18,7 @@ struct NormWs {
 };
 
 NormWs norm_ws(int64_t N, int d) {
-    const int64_t parts = N < kNormParts ? N : kNormParts;
+    const int parts = norm_parts(N, d);
     NormWs w;
     w.part = 0;
     w.bad = align_up(static_cast<size_t>(parts) * d * 4, 256);
@@ -189,13 +189,16 @@ int grpo_norm_bwd(const void* dy, const void* x, const grpo_ckpt* x_ckpt, const 
     p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.part);
     p.bad = reinterpret_cast<int*>(static_cast<char*>(workspace) + w.bad);
     NormPlan plan = norm_bwd_plan(p.N, p.d, sms, x_ckpt != nullptr, dsum != nullptr);
-    if (plan.grid > kNormParts) plan.grid = kNormParts;
+    const int parts = norm_parts(p.N, p.d);          // fewer only on more SMs than kSmCount
+    if (plan.grid > parts) plan.grid = parts;
     p.width = plan.width;
     p.parts = plan.grid;
+    p.joined = plan.joined;
     p.found_inf = found_inf;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = shape->dtype == GRPO_BF16;
-    if (launch(GRPO_PROF_NORM_BWD, st, [&] { return launch_norm_bwd(p, plan, bf16, st); }) != cudaSuccess ||
+    if (launch(GRPO_PROF_NORM_BWD, st, [&] { return launch_norm_bwd(p, plan, bf16, st); }) != cudaSuccess) return GRPO_ERR_LAUNCH;
+    if (!plan.joined &&
         launch(GRPO_PROF_NORM_BWD, st, [&] { return launch_norm_join(p, bf16, st); }) != cudaSuccess)
         return GRPO_ERR_LAUNCH;
     return GRPO_OK;

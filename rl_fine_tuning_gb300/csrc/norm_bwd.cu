@@ -10,7 +10,8 @@ namespace grpo {
 namespace {
 
 constexpr int kBwdRegs = 80, kBwdRegsTwo = 128;      // of a thread with one or two units: 768 or 512 threads an SM
-constexpr int kStagesMax = 3;
+constexpr int kRowsRegs = 96;          // 640 threads an SM
+constexpr int kStagesMax = 2;          // more gain nothing: what is under way is limited by the number of blocks
 constexpr int kSmemSm = 226 * 1024;    // of an SM's 228 KB
 
 // Both sums over a row's threads, in a fixed order; every thread gets them.  A
@@ -84,13 +85,41 @@ __device__ __forceinline__ bool is_bad(uint32_t bad) {
     return !(v.x == 0.f && v.y == 0.f);
 }
 
+// Writes dw of column j; true if it is not finite.
+template <bool kBf16>
+__device__ __forceinline__ bool store_dweight(const NormParams& p, int j, float v) {
+    if (p.weight_f32) {
+        static_cast<float*>(p.dweight)[j] = v;
+    } else {
+        const uint32_t r = pair_bits<kBf16>(v, 0.f);
+        static_cast<uint16_t*>(p.dweight)[j] = static_cast<uint16_t>(r);
+        v = pair_values<kBf16>(r).x;
+    }
+    return !(fabsf(v) <= FLT_MAX);
+}
+
+// dw and found_inf from the parts of one cluster's blocks, which is the whole grid.
+template <bool kBf16>
+__device__ __forceinline__ void join_cluster(const NormParams& p) {
+    cluster_sync();
+    bool bad = false;
+    if (blockIdx.x == 0 && threadIdx.x < gridDim.x) bad = p.bad[threadIdx.x] != 0;
+    if (p.dweight)
+        for (int j = blockIdx.x * blockDim.x + threadIdx.x; j < p.d; j += gridDim.x * blockDim.x) {
+            float v = 0.f;
+            for (unsigned b = 0; b < gridDim.x; ++b) v += p.part[static_cast<int64_t>(b) * p.d + j];
+            bad |= store_dweight<kBf16>(p, j, v);
+        }
+    if (bad) *p.found_inf = 1;             // 0 before, in block 0
+}
+
 __device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(to)),
                  "l"(from), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
 
-// Rows of more than 1024 columns: a block takes a row at a time, and copies the rows to
+// Rows of more than 512 columns: a block takes a row at a time, and copies the rows to
 // come into a ring of p.stages stages in shared memory, one bulk copy a matrix.  Block b
 // leaves its sum of dy s rstd of every column in part[b].
 // A wait that runs out of time leaves garbage in its row; the block goes on, and found_inf says so.
@@ -206,12 +235,11 @@ __global__ void __maxnreg__(kUpt == 1 ? kBwdRegs : kBwdRegsTwo) k_norm_bwd_wide(
     const int any = __syncthreads_or(is_bad<kBf16>(bad) || s_abort);
     abort_grace(&s_abort);
     if (threadIdx.x == 0) p.bad[blockIdx.x] = any;
-    if (!p.dweight) return;
     float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.d;
 #pragma unroll
     for (int k = 0; k < kUpt; ++k) {
         const int i = lane + k * width;
-        if (i >= n_unit) break;
+        if (i >= n_unit || !p.dweight) break;
         uint32_t w[16];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -222,14 +250,15 @@ __global__ void __maxnreg__(kUpt == 1 ? kBwdRegs : kBwdRegsTwo) k_norm_bwd_wide(
         st_global_v8(part + i * kUnit, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
         st_global_v8(part + i * kUnit + 8, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
     }
+    if (p.joined) join_cluster<kBf16>(p);
 }
 
-// Rows of up to 1024 columns: 4, 16 or 32 lanes of a warp take a row at a time; the next
+// Rows of up to 512 columns: 4, 8, 16 or 32 lanes of a warp take a row at a time, a unit each; the next
 // row's loads are under way while one is worked on.
-template <bool kBf16, int kSrc, int kUpt, bool kDsum>
-__global__ void __launch_bounds__(kWarpThreads) k_norm_bwd_rows(const NormParams p) {
+template <bool kBf16, int kSrc, bool kDsum>
+__global__ void __maxnreg__(kRowsRegs) k_norm_bwd_rows(const NormParams p) {
     extern __shared__ float4 s_weight[];       // and at the end the warps' sums of dw
-    const int n_unit = p.d / kUnit, width = p.width, pad = width * kUpt;
+    const int n_unit = p.d / kUnit, width = p.width, pad = width;
     const int lane = static_cast<int>(threadIdx.x) & (width - 1);
     const uint32_t rows = kWarpThreads / width, mine = threadIdx.x / width;        // rows that a block works on at once
     const uint32_t step = gridDim.x * rows, N = static_cast<uint32_t>(p.N);
@@ -237,25 +266,19 @@ __global__ void __launch_bounds__(kWarpThreads) k_norm_bwd_rows(const NormParams
     chain_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.found_inf = 0;
 
-    F2 acc[kUpt][8];
+    F2 acc[8];
 #pragma unroll
-    for (int k = 0; k < kUpt; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[k][j] = 0;
+    for (int j = 0; j < 8; ++j) acc[j] = 0;
     uint32_t bad = 0;
-    Raw<kSrc, kUpt> raw;
-    Unit raw_dy[kUpt], raw_ds[kDsum ? kUpt : 1];
+    Raw<kSrc, 1> raw;
+    Unit raw_dy, raw_ds;
     uint32_t t = blockIdx.x * rows + mine;
     int64_t at = static_cast<int64_t>(t) * p.d + lane * kUnit;         // the thread's first element of row t
     const int64_t at_step = static_cast<int64_t>(step) * p.d;
     auto load = [&](int64_t at, bool on) {
-        load_row<kSrc, kUpt, false>(p, at, on, lane, width, n_unit, &raw);
-#pragma unroll
-        for (int k = 0; k < kUpt; ++k) {
-            const bool in = on && lane + k * width < n_unit;
-            raw_dy[k] = load_unit(p.dy + at + k * width * kUnit, in);
-            if (kDsum) raw_ds[k] = load_unit(p.dsum + at + k * width * kUnit, in);
-        }
+        load_row<kSrc, 1, false>(p, at, on, lane, width, n_unit, &raw);
+        raw_dy = load_unit(p.dy + at, on && lane < n_unit);
+        if (kDsum) raw_ds = load_unit(p.dsum + at, on && lane < n_unit);
     };
     Ahead ahead;
     ahead.begin(p, t, step, width);
@@ -267,78 +290,48 @@ __global__ void __launch_bounds__(kWarpThreads) k_norm_bwd_rows(const NormParams
         const bool live = alive & 1, next = alive >> 1 & 1;
         ahead.advance(p, t, step, width);
         alive = ahead.bits(width);
-        Unit s[kUpt], dy[kUpt], ds[kDsum ? kUpt : 1];
-#pragma unroll
-        for (int k = 0; k < kUpt; ++k) {
-            s[k] = stream_of<kBf16>(raw, k);
-            dy[k] = raw_dy[k];
-            if (kDsum) ds[k] = raw_ds[k];
-        }
+        const Unit s = stream_of<kBf16>(raw, 0), dy = raw_dy;
+        Unit ds;
+        if (kDsum) ds = raw_ds;
         load(at + at_step, next);
-        float2 sums = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < kUpt; ++k) {
-            const float2 u = unit_sums<kBf16>(s[k], dy[k], staged_weight(s_weight, pad, lane + k * width));
-            sums = make_float2(sums.x + u.x, sums.y + u.y);
-        }
+        float2 sums = unit_sums<kBf16>(s, dy, staged_weight(s_weight, pad, lane));
         sums = warp_sums(sums.x, sums.y, width);
         const float rstd = rsqrtf(sums.x * inv_d + p.eps);
         const float c = -(rstd * rstd) * (sums.y * inv_d) * rstd;
         const F2 rstd2 = f2(rstd, rstd), c2 = f2(c, c);
-#pragma unroll
-        for (int k = 0; k < kUpt; ++k) {
-            const int i = lane + k * width;
-            Unit out = unit_grad<kBf16, kDsum>(s[k], dy[k], ds[kDsum ? k : 0], staged_weight(s_weight, pad, i), rstd2, c2, acc[k]);
-            if (!live) out = Unit{};                     // not 0 times a weight that is not finite
-            if (t < N && i < n_unit) {
-                bad = mark_bad<kBf16>(bad, out);
-                store_unit(p.dx + at + k * width * kUnit, out);
-            }
+        Unit out = unit_grad<kBf16, kDsum>(s, dy, ds, staged_weight(s_weight, pad, lane), rstd2, c2, acc);
+        if (!live) out = Unit{};                         // not 0 times a weight that is not finite
+        if (t < N && lane < n_unit) {
+            bad = mark_bad<kBf16>(bad, out);
+            store_unit(p.dx + at, out);
         }
     }
 
     chain_next();
     const int any = __syncthreads_or(is_bad<kBf16>(bad));
     if (threadIdx.x == 0) p.bad[blockIdx.x] = any;
-    if (!p.dweight) return;
     // the rows of a warp, then the warps of the block, in this order; in the weight's place
     float* s_dw = reinterpret_cast<float*>(s_weight);
     const int warp = threadIdx.x >> 5, wide = pad * kUnit;
 #pragma unroll
-    for (int k = 0; k < kUpt; ++k) {
-        const int i = lane + k * width;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float2 v = f2_values(acc[k][j]);
-            for (int o = width; o < 32; o <<= 1) {
-                v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-                v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-            }
-            // the pairs of a unit lie pad pairs apart: neighbouring lanes write neighbouring pairs
-            if ((threadIdx.x & 31) < width) *reinterpret_cast<float2*>(s_dw + warp * wide + (j * pad + i) * 2) = v;
+    for (int j = 0; j < 8; ++j) {
+        float2 v = f2_values(acc[j]);
+        for (int o = width; o < 32; o <<= 1) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
         }
+        // the pairs of a unit lie pad pairs apart: neighbouring lanes write neighbouring pairs
+        if ((threadIdx.x & 31) < width) *reinterpret_cast<float2*>(s_dw + warp * wide + (j * pad + lane) * 2) = v;
     }
     __syncthreads();
     float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.d;
-    for (int j = threadIdx.x; j < p.d / 2; j += kWarpThreads) {        // pair j % 8 of unit j / 8
+    for (int j = threadIdx.x; j < p.d / 2 && p.dweight; j += kWarpThreads) {       // pair j % 8 of unit j / 8
         F2 v = 0;
         for (int w = 0; w < kWarpThreads / 32; ++w)
             v = f2_add(v, *reinterpret_cast<const F2*>(s_dw + w * wide + ((j & 7) * pad + (j >> 3)) * 2));
         *reinterpret_cast<F2*>(part + 2 * j) = v;
     }
-}
-
-// Writes dw of column j; true if it is not finite.
-template <bool kBf16>
-__device__ __forceinline__ bool store_dweight(const NormParams& p, int j, float v) {
-    if (p.weight_f32) {
-        static_cast<float*>(p.dweight)[j] = v;
-    } else {
-        const uint32_t r = pair_bits<kBf16>(v, 0.f);
-        static_cast<uint16_t*>(p.dweight)[j] = static_cast<uint16_t>(r);
-        v = pair_values<kBf16>(r).x;
-    }
-    return !(fabsf(v) <= FLT_MAX);
+    if (p.joined) join_cluster<kBf16>(p);
 }
 
 // dw and found_inf from the parts.  A block takes 32 columns, each of its 32 warps every 32nd part.
@@ -369,10 +362,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_norm_join(const NormParams 
 template <bool kBf16, int kSrc, bool kDsum>
 cudaError_t bwd_of(const NormParams& p, const NormPlan& o, cudaStream_t st) {
     const size_t weight = static_cast<size_t>(o.width) * o.upt * kUnit * 4;
-    if (!o.wide) {                             // 16 KB at most: d <= 1024
-        const auto f = o.upt == 1 ? k_norm_bwd_rows<kBf16, kSrc, 1, kDsum> : k_norm_bwd_rows<kBf16, kSrc, 2, kDsum>;
-        return launch_chained(f, o.grid, o.threads, weight * (kWarpThreads / 32), p, st);
-    }
+    if (!o.wide)                               // 8 KB at most: d <= 512
+        return launch_chained(k_norm_bwd_rows<kBf16, kSrc, kDsum>, o.grid, o.threads, weight * (kWarpThreads / 32), p, st, o.joined ? o.grid : 1);
     const auto f = o.upt == 1 ? k_norm_bwd_wide<kBf16, kSrc, 1, kDsum> : k_norm_bwd_wide<kBf16, kSrc, 2, kDsum>;
     const size_t stage = weight / 4 * (2 + (kSrc == kCkpt ? 1 : 2) + (kDsum ? 2 : 0));
     NormParams r = p;
@@ -383,7 +374,7 @@ cudaError_t bwd_of(const NormParams& p, const NormPlan& o, cudaStream_t st) {
     const size_t smem = weight + r.stages * stage;
     const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    return launch_chained(f, o.grid, o.threads, smem, r, st);
+    return launch_chained(f, o.grid, o.threads, smem, r, st, o.joined ? o.grid : 1);
 }
 
 template <bool kBf16, int kSrc>

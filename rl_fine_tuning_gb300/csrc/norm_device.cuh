@@ -16,17 +16,20 @@ namespace grpo {
 // A kernel whose blocks may be brought onto the SMs while the kernel before it in the stream ends.  It touches no
 // memory before chain_wait, so that for its results it is a launch like any other.
 template <class P>
-cudaError_t launch_chained(void (*f)(P), int64_t grid, int threads, size_t smem, const P& p, cudaStream_t st) {
+cudaError_t launch_chained(void (*f)(P), int64_t grid, int threads, size_t smem, const P& p, cudaStream_t st, int cluster = 1) {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, f, p);
 }
 
