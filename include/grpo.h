@@ -450,22 +450,22 @@ int grpo_pair_loss_fwd_bwd(const void* h, const void* W, const int32_t* tokens, 
  * the model's norm; those used are stated here.
  *
  * Common to them: matrices [N x d] of type shape->dtype (GRPO_BF16 or GRPO_FP16;
- * others are refused with GRPO_ERR_DTYPE), 16-byte aligned; V, beta and what else
- * describes a loss are not looked at beyond the checks of every shape.  mask: NULL
- * counts every row, else [N] uint8, nonzero = the row counts.  Rows that do not
- * count are not read (they may hold anything) and count as rows of zeros: their
- * outputs are zeros, and scales 2^-126.  Nothing is written behind row N.  Outputs overlap
- * neither inputs nor one another, but a 16-bit output of the same shape may be
- * the same pointer as a 16-bit input (sum_out = residual, dx = dy).  Every output
- * is bitwise reproducible, sums are in fp32 in a fixed order, and calls can be
- * captured into a CUDA graph. */
+ * others are refused with GRPO_ERR_DTYPE), 32-byte aligned, N d at most 2^43
+ * (GRPO_ERR_SHAPE above); V, beta and what else describes a loss are not looked at
+ * beyond the checks of every shape.  mask: NULL counts every row, else [N] uint8,
+ * nonzero = the row counts.  Rows that do not count may hold anything and stand for
+ * rows of zeros: their outputs are zeros, and scales 2^-126.  Nothing is written
+ * behind row N.  Outputs overlap neither inputs nor one another, but a 16-bit
+ * output of the same shape may be the same pointer as a 16-bit input (sum_out =
+ * residual, dx = dy).  Sums are in fp32 in a fixed order, every output is bitwise
+ * reproducible, and calls can be captured into a CUDA graph. */
 
 /* Columns of a row that share one scale of a checkpoint. */
 #define GRPO_CKPT_BLOCK 64
 
 /* An 8-bit checkpoint of an [N x d] matrix, both parts device memory:
  *   codes  [N x d] int8, 16-byte aligned
- *   scales [N x d / GRPO_CKPT_BLOCK] bf16
+ *   scales [N x d / GRPO_CKPT_BLOCK] bf16, 2-byte aligned
  * x stands as code * scale, rounded to the 16-bit type, with
  *   scale = max |x| of the block / 127 in bf16, at least 2^-126
  *   code  = x / scale rounded to the nearest integer
@@ -473,7 +473,7 @@ int grpo_pair_loss_fwd_bwd(const void* h, const void* W, const int32_t* tokens, 
  * rounding to 16 bits.  (Scales are at most 2^121 for bf16 and 2^9 for fp16, so
  * that no finite value comes back as infinity: blocks with a value above 3.38e38,
  * or above 65024 in fp16, are off by up to one scale there.)  A block with a value
- * that is not finite comes back as NaN. */
+ * that is not finite has the scale NaN and comes back as NaN. */
 typedef struct {
     int8_t* codes;
     uint16_t* scales;
@@ -511,7 +511,7 @@ size_t grpo_norm_workspace_bytes(const grpo_shape* shape);
  *   x, x_ckpt: exactly one is given, the other NULL; residual: NULL or [N x d],
  *       NULL with x_ckpt
  *   weight [d], 16-byte aligned
- *   y [N x d] of type y_type, 16-byte aligned.  8-bit: codes of y / scale, rounded
+ *   y [N x d] of type y_type.  8-bit (16-byte aligned): codes of y / scale, rounded
  *       to nearest, those above the type's largest value at that value; NaN stays NaN
  *   row_scale: 8-bit y only, else NULL.  [N] fp32 <- max |y| of the row / the
  *       type's largest value (448 or 57344), at least 2^-126, NaN left out.  These
@@ -535,6 +535,8 @@ int grpo_norm_fwd(const void* x, const grpo_ckpt* x_ckpt, const void* residual, 
  *   dweight: NULL (a frozen weight) or [d] of the weight's type, 16-byte aligned
  *       (written)
  *   found_inf [1] int32 <- 1 if a value of dx or dweight is not finite, else 0
+ *       (and 1 if a wait for a copy within the GPU ran out of time: the outputs
+ *       are no gradients then)
  * A loss scale in dy and dsum is one in dx and dweight. */
 int grpo_norm_bwd(const void* dy, const void* x, const grpo_ckpt* x_ckpt, const void* weight, const void* dsum,
                   const uint8_t* mask, const grpo_shape* shape, const grpo_norm_opts* opts, void* workspace, size_t ws_bytes,

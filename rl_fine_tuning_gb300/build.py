@@ -25,7 +25,7 @@ LIB = os.path.join(BUILD, "libgrpo.so")
 LIB_CHECKED = os.path.join(BUILD, "libgrpo_checked.so")
 VARIANTS = {LIB: [], LIB_CHECKED: ["-DGRPO_DEVICE_CHECKS"]}
 SOURCES = ["tc_kernels.cu", "small_kernels.cu", "grpo_abi.cu", "head_tc.cu", "head_kernels.cu", "head_abi.cu",
-           "norm_fwd.cu", "norm_bwd.cu", "norm_ckpt.cu", "norm_abi.cu"]
+           "norm_fwd.cu", "norm_bwd.cu", "norm_ckpt.cu", "norm_plan.cu", "norm_abi.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "tc_pair.cuh", "abi_common.h", "head.h", "head_join.cuh", "norm.h",
            "norm_device.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,14 +1,17 @@
 // The norm before the head, its gradient, and 8-bit checkpoints of activations
-// (see "the norm before the head" in grpo.h): declarations shared by
-// norm_kernels.cu and norm_abi.cu.
+// (see "the norm before the head" in grpo.h): what norm_fwd.cu, norm_bwd.cu,
+// norm_ckpt.cu, norm_plan.cu and norm_abi.cu share.
 #pragma once
 #include "internal.h"
 
 namespace grpo {
 
-constexpr int kNormMaxD = 16384;       // widest row of the norm (a row stays in one CTA)
+constexpr int kNormMaxD = 16384;       // widest row of the norm (a row stays in one block)
 constexpr int kSmCount = 152;          // of a GB300: what the gradient's workspace is sized for
 constexpr int kClusterMax = 8;
+constexpr int kUnit = 16;              // elements of a thread's load: a 32-byte sector of a 16-bit matrix
+constexpr int kWarpThreads = 128;      // block whose warps, or parts of them, take a row each
+constexpr int kBlockMax = 512;         // widest block that takes a row as a whole
 constexpr int kCkptBlock = GRPO_CKPT_BLOCK;
 constexpr float kLeastScale = 1.17549435e-38f;   // 2^-126: its reciprocal is finite, and neither is subnormal
 

@@ -10,7 +10,8 @@ namespace grpo {
 
 namespace {
 
-constexpr size_t kMatrixAlign = 32;    // of a 16-bit matrix: its 32-byte sectors are loaded and stored whole
+constexpr int64_t kMostElements = 1LL << 43;   // 2^30 blocks of a checkpoint's kernels
+constexpr size_t kMatrixAlign = 32;            // of a 16-bit matrix: its 32-byte sectors are loaded and stored whole
 
 // What the gradient's workspace holds: sums of the weight's gradient, and flags.
 struct NormWs {
@@ -40,10 +41,12 @@ int sm_count(int* out) {
     return GRPO_OK;
 }
 
+int64_t rows_of(const grpo_shape& s) { return static_cast<int64_t>(s.n_groups) * s.G * s.L; }
+
 int norm_shape(const grpo_shape* s, int most_d) {
     if (!s) return GRPO_ERR_SHAPE;
     if (!dtype_ok(*s)) return GRPO_ERR_DTYPE;
-    if (!shape_ok(*s) || s->d > most_d) return GRPO_ERR_SHAPE;
+    if (!shape_ok(*s) || s->d > most_d || rows_of(*s) * s->d > kMostElements) return GRPO_ERR_SHAPE;
     return GRPO_OK;
 }
 
@@ -85,7 +88,7 @@ NormParams norm_params(const grpo_shape& s, const grpo_norm_opts& o, const void*
     NormParams p = {};
     p.weight = weight;
     p.mask = mask;
-    p.N = static_cast<int64_t>(s.n_groups) * s.G * s.L;
+    p.N = rows_of(s);
     p.d = s.d;
     p.eps = o.eps;
     p.weight_f32 = o.weight_f32;
@@ -95,18 +98,17 @@ NormParams norm_params(const grpo_shape& s, const grpo_norm_opts& o, const void*
     return p;
 }
 
-int launch_as(int kind, cudaStream_t st, cudaError_t (*f)(const CkptParams&, bool, cudaStream_t), const CkptParams& p,
-              bool bf16) {
+int launch_ckpt(cudaError_t (*f)(const CkptParams&, bool, cudaStream_t), const CkptParams& p, bool bf16, cudaStream_t st) {
     int sms = 0;
     const int rc = sm_count(&sms);
     if (rc != GRPO_OK) return rc;
-    return launch(kind, st, [&] { return f(p, bf16, st); }) == cudaSuccess ? GRPO_OK : GRPO_ERR_LAUNCH;
+    return launch(GRPO_PROF_CKPT, st, [&] { return f(p, bf16, st); }) == cudaSuccess ? GRPO_OK : GRPO_ERR_LAUNCH;
 }
 
 CkptParams ckpt_params(const grpo_shape& s, const uint8_t* mask) {
     CkptParams p = {};
     p.mask = mask;
-    p.N = static_cast<int64_t>(s.n_groups) * s.G * s.L;
+    p.N = rows_of(s);
     p.d = s.d;
     p.per_row = ~0ull / static_cast<uint64_t>(s.d / 16) + 1;
     return p;
@@ -129,7 +131,7 @@ void grpo_norm_opts_init(grpo_norm_opts* o, grpo_dtype dtype) {
 
 size_t grpo_norm_workspace_bytes(const grpo_shape* shape) {
     if (norm_shape(shape, kNormMaxD) != GRPO_OK) return 0;
-    return norm_ws(static_cast<int64_t>(shape->n_groups) * shape->G * shape->L, shape->d).total;
+    return norm_ws(rows_of(*shape), shape->d).total;
 }
 
 int grpo_norm_fwd(const void* x, const grpo_ckpt* x_ckpt, const void* residual, const void* weight, const uint8_t* mask,
@@ -139,8 +141,9 @@ int grpo_norm_fwd(const void* x, const grpo_ckpt* x_ckpt, const void* residual, 
     if (rc == GRPO_OK) rc = norm_opts_check(*shape, opts, true);
     if (rc != GRPO_OK) return rc;
     const bool y16 = opts->y_type == shape->dtype;
-    if (!source_ok(x, x_ckpt) || !left_or(residual, kMatrixAlign) || !given(weight, 16) || !given(y, y16 ? kMatrixAlign : 16) || !left_or(row_scale, 4) ||
-        !left_or(sum_out, kMatrixAlign) || (sum_ckpt && !ckpt_ok(sum_ckpt)))
+    if (!source_ok(x, x_ckpt) || !left_or(residual, kMatrixAlign) || !given(weight, 16) ||
+        !given(y, y16 ? kMatrixAlign : 16) || !left_or(row_scale, 4) || !left_or(sum_out, kMatrixAlign) ||
+        (sum_ckpt && !ckpt_ok(sum_ckpt)))
         return GRPO_ERR_POINTER;
     if (x_ckpt && (residual || sum_ckpt)) return GRPO_ERR_POINTER;
     if (y16 ? row_scale != nullptr : !row_scale && opts->y_scale == 0.f) return GRPO_ERR_POINTER;
@@ -172,8 +175,8 @@ int grpo_norm_bwd(const void* dy, const void* x, const grpo_ckpt* x_ckpt, const 
     int rc = norm_shape(shape, kNormMaxD);
     if (rc == GRPO_OK) rc = norm_opts_check(*shape, opts, false);
     if (rc != GRPO_OK) return rc;
-    if (!given(dy, kMatrixAlign) || !source_ok(x, x_ckpt) || !given(weight, 16) || !left_or(dsum, kMatrixAlign) || !given(workspace, 256) ||
-        !given(dx, kMatrixAlign) || !left_or(dweight, 16) || !given(found_inf, 4))
+    if (!given(dy, kMatrixAlign) || !source_ok(x, x_ckpt) || !given(weight, 16) || !left_or(dsum, kMatrixAlign) ||
+        !given(workspace, 256) || !given(dx, kMatrixAlign) || !left_or(dweight, 16) || !given(found_inf, 4))
         return GRPO_ERR_POINTER;
     NormParams p = norm_params(*shape, *opts, weight, mask);
     const NormWs w = norm_ws(p.N, p.d);
@@ -212,7 +215,7 @@ int grpo_ckpt_pack(const void* x, const uint8_t* mask, const grpo_shape* shape, 
     p.x = static_cast<const uint16_t*>(x);
     p.codes_out = out->codes;
     p.scales_out = out->scales;
-    return launch_as(GRPO_PROF_CKPT, reinterpret_cast<cudaStream_t>(stream), launch_ckpt_pack, p, shape->dtype == GRPO_BF16);
+    return launch_ckpt(launch_ckpt_pack, p, shape->dtype == GRPO_BF16, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int grpo_ckpt_unpack(const grpo_ckpt* ckpt, const uint8_t* mask, const grpo_shape* shape, void* x_out, grpo_stream_t stream) {
@@ -223,7 +226,7 @@ int grpo_ckpt_unpack(const grpo_ckpt* ckpt, const uint8_t* mask, const grpo_shap
     p.codes = ckpt->codes;
     p.scales = ckpt->scales;
     p.x_out = static_cast<uint16_t*>(x_out);
-    return launch_as(GRPO_PROF_CKPT, reinterpret_cast<cudaStream_t>(stream), launch_ckpt_unpack, p, shape->dtype == GRPO_BF16);
+    return launch_ckpt(launch_ckpt_unpack, p, shape->dtype == GRPO_BF16, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,8 +1,13 @@
-// The gradient of the norm before the head (see norm_abi.cu for its entry point).
-//
-// As the forward pass, it moves bytes: a row of dy and of s is read once and
-// stays in registers between its two sums and dx, while the next row's loads are
-// under way.  The weight's gradient is summed in registers from row to row.
+// The gradient of the norm before the head (norm_abi.cu has the entry point, norm_plan.cu
+// deals the rows).  With rstd = 1 / sqrt(mean s^2 + eps):
+//   dx = rstd dy w - s rstd^3 mean(dy w s) + dsum;  dw = the sum over the rows of dy s rstd
+// Both means come from one pass over the row, so nothing of the forward pass has to be
+// kept but s.  12 operations an element against 5 to 8 bytes: HBM bounds it, with
+// instructions close behind (the codes of a checkpoint take 5 an element).  dw is
+// summed in registers from row to row, then over the blocks in a fixed order.
+// Measured: 160,000 x 4096 from a checkpoint, 54% of the rows: 373 us, 6.4 TB/s (a copy reaches 6.8);
+// 40,000 x 4096 from 16 bits 148 us, with dsum 190 us (6.6 and 6.9 TB/s); 8192 x 1536, 60% of the rows,
+// with dsum: 18 us, of which the last 4 are the sum of dw over the blocks.
 #include "norm_device.cuh"
 
 namespace grpo {
@@ -14,10 +19,7 @@ constexpr int kRowsRegs = 96;          // 640 threads an SM
 constexpr int kStagesMax = 2;          // more gain nothing: what is under way is limited by the number of blocks
 constexpr int kSmemSm = 226 * 1024;    // of an SM's 228 KB
 
-// Both sums over a row's threads, in a fixed order; every thread gets them.  A
-// block's warps leave theirs in s, of which the next row takes the other half, so
-// that one barrier is enough; entries of warps that are not there hold 0.  There
-// the lower lanes of a warp join a, the upper ones b.
+// Both sums over a row's threads, in a fixed order; every thread gets them.
 __device__ __forceinline__ float2 warp_sums(float a, float b, int width) {
     for (int o = width / 2; o > 0; o >>= 1) {
         a += __shfl_xor_sync(0xffffffffu, a, o);
@@ -26,6 +28,8 @@ __device__ __forceinline__ float2 warp_sums(float a, float b, int width) {
     return make_float2(a, b);
 }
 
+// Here the lower lanes of a warp join a, the upper ones b.  The warps leave theirs in s, of which the next row takes
+// the other half, so that one barrier is enough; entries of warps that are not there hold 0.
 __device__ __forceinline__ float2 block_sums(float a, float b, float* s) {
     const bool upper = threadIdx.x & 16;
     float v = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
@@ -120,8 +124,9 @@ __device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t b
 }
 
 // Rows of more than 512 columns: a block takes a row at a time, and copies the rows to
-// come into a ring of p.stages stages in shared memory, one bulk copy a matrix.  Block b
-// leaves its sum of dy s rstd of every column in part[b].
+// come into a ring of p.stages stages in shared memory, one bulk copy a matrix: loads
+// into registers took 16 to 24 of them, and so fewer rows an SM (475 us with two rows of 4096, 408 with three).
+// Block b leaves its sum of dy s rstd of every column in part[b].
 // A wait that runs out of time leaves garbage in its row; the block goes on, and found_inf says so.
 template <bool kBf16, int kSrc, int kUpt, bool kDsum>
 __global__ void __maxnreg__(kUpt == 1 ? kBwdRegs : kBwdRegsTwo) k_norm_bwd_wide(const NormParams p) {
@@ -334,29 +339,34 @@ __global__ void __maxnreg__(kRowsRegs) k_norm_bwd_rows(const NormParams p) {
     if (p.joined) join_cluster<kBf16>(p);
 }
 
-// dw and found_inf from the parts.  A block takes 32 columns, each of its 32 warps every 32nd part.
-constexpr int kJoinCols = 32, kJoinWarps = 32;
+// dw and found_inf from the parts.  A block takes 16 columns, and every thread each `slots`-th part of one.
+constexpr int kJoinCols = 16, kJoinThreads = 1024;
 
 template <bool kBf16>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_norm_join(const NormParams p) {
-    __shared__ float s_part[kJoinWarps][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int j = blockIdx.x * kJoinCols + lane;
+__global__ void __launch_bounds__(kJoinThreads) k_norm_join(const NormParams p) {
+    __shared__ float s_part[kJoinThreads / kJoinCols][kJoinCols + 1];
+    const int slots = static_cast<int>(blockDim.x) / kJoinCols, lane = threadIdx.x & 31;
+    const int slot = threadIdx.x / kJoinCols, col = threadIdx.x % kJoinCols;
     bool bad = false;
     chain_wait();
     if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < p.parts; b += 32 * kJoinWarps) bad |= p.bad[b] != 0;
+        for (int b = threadIdx.x; b < p.parts; b += blockDim.x) bad |= p.bad[b] != 0;
     if (p.dweight) {
+        const float* part = p.part + blockIdx.x * kJoinCols + col;
         float v = 0.f;
 #pragma unroll 8
-        for (int b = warp; b < p.parts; b += kJoinWarps) v += p.part[static_cast<int64_t>(b) * p.d + j];
-        s_part[warp][lane] = v;
+        for (int b = slot; b < p.parts; b += slots) v += part[static_cast<int64_t>(b) * p.d];
+        s_part[slot][col] = v;
         __syncthreads();
-        v = s_part[lane][warp];            // the block's column `warp`
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) bad |= store_dweight<kBf16>(p, blockIdx.x * kJoinCols + warp, v);
+        const int j = threadIdx.x >> 5;            // a warp for each column
+        if (j < kJoinCols) {
+            v = 0.f;
+            for (int i = lane; i < slots; i += 32) v += s_part[i][j];
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane == 0) bad |= store_dweight<kBf16>(p, blockIdx.x * kJoinCols + j, v);
+        }
     }
-    if (bad) *p.found_inf = 1;             // 0 before: k_norm_bwd
+    if (bad) *p.found_inf = 1;             // 0 before: the kernel that left the parts
 }
 
 template <bool kBf16, int kSrc, bool kDsum>
@@ -390,8 +400,10 @@ cudaError_t launch_norm_bwd(const NormParams& p, const NormPlan& o, bool bf16, c
 }
 
 cudaError_t launch_norm_join(const NormParams& p, bool bf16, cudaStream_t st) {
-    return launch_chained(bf16 ? k_norm_join<true> : k_norm_join<false>, p.dweight ? p.d / kJoinCols : 1, 32 * kJoinWarps, 0,
-                          p, st);
+    // 32 or 64 slots: 304 parts of 5120 columns 12.6 us (the whole gradient of 1505 rows) against 14.5, 760 parts of
+    // 1536 (8192 rows) 19.0 against 18.0
+    const int threads = p.parts > 512 ? kJoinThreads : kJoinThreads / 2;
+    return launch_chained(bf16 ? k_norm_join<true> : k_norm_join<false>, p.dweight ? p.d / kJoinCols : 1, threads, 0, p, st);
 }
 
 }  // namespace grpo

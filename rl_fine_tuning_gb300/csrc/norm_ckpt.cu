@@ -1,5 +1,9 @@
-// 8-bit checkpoints of activations (see norm_abi.cu for the entry points), and
-// how the norm's rows are dealt to threads.
+// 8-bit checkpoints of activations: packing and unpacking (norm_abi.cu has the entry
+// points; the norm's kernels write and read them too).
+//
+// Per element 2 bytes on one side and 1 + 1/32 on the other, and nothing but HBM to
+// bound them: 655M elements take 275 us to pack (7.2 TB/s) and 281 to unpack (7.1),
+// where a copy reaches 6.8.  A block works on 8192 elements, 16 a thread at a time, and ends.
 #include "norm_device.cuh"
 
 namespace grpo {
@@ -60,84 +64,13 @@ __global__ void __launch_bounds__(kCkptThreads) k_ckpt_unpack(const CkptParams p
     }
 }
 
-// a block for each 8192 elements: at most 2^31 blocks for 2^31 rows of 8192 columns; the caller refuses more
+// at most 2^30: see kMostElements
 int64_t ckpt_blocks(const CkptParams& p) {
     const int64_t each = kCkptThreads * kCkptUpt;
     return (p.N * (p.d / kUnit) + each - 1) / each;
 }
 
 }  // namespace
-
-namespace {
-
-// the row's threads, and their units; rows of up to `most` units take some lanes of a warp
-NormPlan row_plan(int d, int most, bool two) {
-    NormPlan o;
-    const int n_unit = d / kUnit;
-    o.wide = n_unit > most;
-    if (!o.wide) {
-        o.width = n_unit <= 4 ? 4 : n_unit <= 8 ? 8 : n_unit <= 16 ? 16 : 32;
-        o.upt = (n_unit + o.width - 1) / o.width;
-        o.threads = kWarpThreads;
-    } else {
-        o.upt = n_unit > kBlockMax || two ? 2 : 1;
-        o.threads = o.width = (n_unit + 32 * o.upt - 1) / (32 * o.upt) * 32;
-    }
-    return o;
-}
-
-}  // namespace
-
-// A block goes through at least 8 turns of rows, in whole waves of blocks: with many rows, blocks that
-// come and go keep the rows that are worked on near one another in memory.  160,000 rows of 4096 with the
-// residual: 661 us with one wave, 595 with 8, 589 with 16; 10,000 rows to 8 bits: 41 us up to 8 turns a
-// block or more, 46 with 4, 57 with 2.
-NormPlan norm_fwd_plan(int64_t N, int d, int sm_count) {
-    NormPlan o = row_plan(d, 64, false);
-    const int64_t rows = o.threads / o.width, turns = (N + rows - 1) / rows;
-    o.per_sm = (o.upt == 1 ? 1024 : 512) / o.threads;
-    const int64_t once = static_cast<int64_t>(o.per_sm) * sm_count, waves = turns / 8 / once;
-    o.grid = static_cast<int>(turns < once ? turns : waves > 1 ? waves * once : once);
-    return o;
-}
-
-// Two units a thread where a block of one would fill an SM (d > 6144), and from a checkpoint, whose codes cost
-// instructions, where that leaves no thread without one (160,000 x 4096, 54% of the rows: 375 against 388 us).
-// Of wide rows an SM takes as many as bring its copies under way, two rows a
-// block, to about 80 KB (96 with dsum): 40,000 rows of 4096: 161 us with 64 KB, 149 with 96, 163 with
-// 144; of 2048: 170 with 48 KB, 153 with 64, 164 with 96, 176 with 144.
-NormPlan norm_bwd_plan(int64_t N, int d, int sm_count, bool ckpt, bool dsum) {
-    const bool two = d / kUnit > 384 || (ckpt && !dsum && d / kUnit % 64 == 0 && N >= 64LL * sm_count);
-    NormPlan o = row_plan(d, 32, two);
-    const int64_t rows = o.threads / o.width, turns = (N + rows - 1) / rows;
-    if (o.wide) {
-        const int row = d * (2 + (ckpt ? 1 : 2) + (dsum ? 2 : 0)), most = (o.upt == 1 ? 768 : 512) / o.threads;
-        o.per_sm = ((dsum ? 96 : 80) * 1024 + row) / (2 * row);
-        if (o.per_sm > most) o.per_sm = most;
-        if (o.per_sm > 8) o.per_sm = 8;
-        if (o.per_sm < 1) o.per_sm = 1;
-    } else {
-        o.per_sm = 5;                          // what 96 registers a thread leave: 155 us; 4 take 167, 6 in two waves 200
-    }
-    const int64_t grid = static_cast<int64_t>(o.per_sm) * sm_count;
-    o.grid = static_cast<int>(turns < grid ? turns : grid);
-    // One cluster of blocks joins its sums itself, even if that takes a second turn of rows.
-    o.joined = turns <= 2 * kClusterMax;
-    if (o.joined) {
-        const int want = turns < kClusterMax ? static_cast<int>(turns) : kClusterMax;
-        for (o.grid = 1; o.grid < want;) o.grid *= 2;
-    }
-    return o;
-}
-
-int norm_parts(int64_t N, int d) {
-    int most = 0;
-    for (int i = 0; i < 4; ++i) {
-        const NormPlan o = norm_bwd_plan(N, d, kSmCount, i & 1, i & 2);
-        if (o.grid > most) most = o.grid;
-    }
-    return most;
-}
 
 cudaError_t launch_ckpt_pack(const CkptParams& p, bool bf16, cudaStream_t st) {
     return launch_chained(bf16 ? k_ckpt_pack<true> : k_ckpt_pack<false>, ckpt_blocks(p), kCkptThreads, 0, p, st);

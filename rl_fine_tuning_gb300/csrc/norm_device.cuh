@@ -35,10 +35,10 @@ cudaError_t launch_chained(void (*f)(P), int64_t grid, int threads, size_t smem,
 
 // ---------------------------------------------------------------- pairs of fp32 numbers
 // sm_103 adds and multiplies two fp32 numbers in one instruction, each rounded as by
-// itself.  These kernels are short of instruction slots before they are short of
-// anything but bandwidth: a gradient from a checkpoint with one number an instruction
-// (and the weight unpacked at each use) took 488 instructions per 8 elements and 929 us where
-// HBM needs 351.
+// itself.  Next to bandwidth these kernels are short of instructions: with one number an
+// instruction, 8 elements a thread and the weight unpacked at each use, a gradient from a
+// checkpoint took 929 us where HBM needs 351.  (The assembler may join a product with the sum
+// after it into one rounding: where that matters the product is a single one, see encode.)
 
 using F2 = unsigned long long;
 
@@ -109,8 +109,6 @@ constexpr uint32_t kPairOne = kBf16 ? 0x3f803f80u : 0x3c003c00u;
 
 // ---------------------------------------------------------------- a thread's 16 elements
 
-constexpr int kUnit = 16;              // elements of a thread's load: a 32-byte sector of a 16-bit matrix
-
 // in 16 bits, and in fp32
 struct Unit {
     uint32_t w[8];
@@ -119,8 +117,8 @@ struct Unit32 {
     F2 p[8];
 };
 
-// What follows works from the 16 registers-in-8 again: without this the compiler keeps the fp32 values of a
-// unit from their first use to their second, and spills others for them.
+// Later uses unpack x anew.  Without this the compiler keeps the 16 fp32 values of a unit from their first use to
+// their second, beside the 8 registers that hold it, and spills for them (gradient from a checkpoint: 512 against 408 us).
 __device__ __forceinline__ void forget_values(Unit* x) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) asm volatile("" : "+r"(x->w[i]));
@@ -298,9 +296,6 @@ __device__ __forceinline__ uint4 codes8(const Unit32& v) {
 }
 
 // ---------------------------------------------------------------- a row's threads
-
-constexpr int kWarpThreads = 128;      // block whose warps, or parts of them, take a row each
-constexpr int kBlockMax = 512;         // widest block that takes a row as a whole
 
 enum Source { kX, kXResidual, kCkpt };
 

@@ -1,9 +1,14 @@
-// The norm before the head: forward pass (see norm_abi.cu for its entry point).
-//
-// A handful of operations per element against 3 to 8 bytes: HBM bounds it.  A row
-// is read once and stays in registers, 16-bit values in pairs, between its sum of
-// squares and its outputs; while a row is worked on, the next one's loads are
-// under way.
+// The norm before the head: forward pass (norm_abi.cu has the entry point, norm_plan.cu
+// deals the rows).
+//   s = x + residual, or a checkpoint's values;  y = s / sqrt(mean s^2 + eps) w
+// 5 operations an element against 3 to 8 bytes: HBM bounds it.  A row is read
+// once and stays in registers, 16-bit values in pairs, between its sum of squares
+// and its outputs (s, its checkpoint, y), and while it is worked on, the next row's
+// loads are under way.  A thread has 16 elements of a row, a whole sector to load and to store, or twice
+// that in the widest rows.  Rows that do not count cost the stores of their zeros.
+// Measured: 160,000 x 4096 with the residual, 54% of the rows: 579 us, 7.0 TB/s (a copy reaches 6.8);
+// 10,000 x 4096 to E4M3 and a checkpoint: 39 us, 6.3 TB/s.  Copies of the rows to come
+// into shared memory by each thread for itself (cp.async) were slower: 764 us against 626 at the time.
 #include "norm_device.cuh"
 
 namespace grpo {
@@ -12,11 +17,12 @@ namespace {
 
 constexpr int kFwdRegs = 64, kFwdRegsTwo = 128;     // of a thread with one or two units: 1024 or 512 threads an SM
 
+template <bool kMax>
+__device__ __forceinline__ float both(float a, float b) { return kMax ? fmaxf(a, b) : a + b; }
+
 // Sum (or maximum) over a row's threads, in a fixed order; every thread gets it.
 // A block's: the warps' values lie in s, of which the next call takes another
 // part, so that one barrier is enough; entries of warps that are not there hold 0.
-template <bool kMax>
-__device__ __forceinline__ float both(float a, float b) { return kMax ? fmaxf(a, b) : a + b; }
 
 template <bool kWide, bool kMax>
 __device__ __forceinline__ float row_join(float v, int width, float* s) {
@@ -32,6 +38,7 @@ __device__ __forceinline__ float row_join(float v, int width, float* s) {
     return v;
 }
 
+// kUpt units a thread.  kWide: a block takes one row at a time; else 4 to 32 lanes of its warps take one each.
 template <bool kBf16, int kSrc, int kUpt, bool kWide, bool kOut8>
 __global__ void __maxnreg__(kUpt == 1 ? kFwdRegs : kFwdRegsTwo) k_norm_fwd(const NormParams p) {
     __shared__ alignas(16) float s_join[4][kBlockMax / 32];
@@ -165,9 +172,9 @@ __global__ void __maxnreg__(kUpt == 1 ? kFwdRegs : kFwdRegsTwo) k_norm_fwd(const
 template <bool kBf16, int kSrc, bool kOut8>
 cudaError_t fwd_of(const NormParams& p, const NormPlan& o, cudaStream_t st) {
     auto f = o.wide ? o.upt == 1 ? k_norm_fwd<kBf16, kSrc, 1, true, kOut8> : k_norm_fwd<kBf16, kSrc, 2, true, kOut8>
-                     : o.upt == 1 ? k_norm_fwd<kBf16, kSrc, 1, false, kOut8> : k_norm_fwd<kBf16, kSrc, 2, false, kOut8>;
+                    : o.upt == 1 ? k_norm_fwd<kBf16, kSrc, 1, false, kOut8> : k_norm_fwd<kBf16, kSrc, 2, false, kOut8>;
     const size_t smem = static_cast<size_t>(o.width) * o.upt * kUnit * 4;
-    if (smem > 48 * 1024 - 256) {
+    if (smem > 40 * 1024) {                    // 48 KB with the rest need no permission
         const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxD * 4);
         if (e != cudaSuccess) return e;
     }

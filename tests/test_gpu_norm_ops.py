@@ -282,6 +282,25 @@ def test_checkpoints_at_the_ends_of_the_type(dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_checkpoint_scales_of_every_size(dt):
+    """Each positive finite number of the type as a block's largest value: scales and codes are the definition's bit for bit, so
+    the reciprocal of every scale is the correctly rounded one.  (Blocks whose scale would be past its limit are left to
+    the test above.)"""
+    t = R.TORCH[dt]
+    limit = 2.0 ** 121 if dt == "bf16" else 512.0
+    top = torch.arange(1, 0x7f80 if dt == "bf16" else 0x7c00, dtype=torch.int32).to(torch.int16).view(t)
+    top = top[(top.double() / 127 <= limit)]
+    n = (len(top) + 1) // 2 * 2
+    top = torch.cat([top, top[:n - len(top)]])
+    part = torch.linspace(-1, 1, 63, dtype=torch.float64)
+    x = torch.cat([top.double()[:, None], top.double()[:, None] * part], 1).to(t).view(n // 2, 128).cuda()
+    c = Case(n // 2, 128, dt)
+    codes, scales = c.pack(x)
+    wc, ws = torch_pack(x)
+    assert same(scales, ws) and torch.equal(codes, wc)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
 @pytest.mark.parametrize("y", ["16", "e4m3"])
 def test_norm_of_a_checkpoint_is_the_norm_of_its_values(dt, y):
     for N, d in ((1, 64), (60, 1536), (9, 4160), (2, 16384)):
@@ -532,6 +551,136 @@ def test_profile_counts_the_launches():
         rg.grpo_profile_enable(False)
     assert got["norm"][1] == 2 and got["norm_bwd"][1] in (1, 2) and got["ckpt"][1] == 2
     assert rg.grpo_kernel_launches() - before == sum(n for _, n in got.values())
+
+
+# ---------------------------------------------------------------- many rows: blocks that take several, rings, lookahead
+
+def gpu64(c, s, dsum):
+    """y's and the gradient's definitions in 64 bits on the GPU, with the bounds of norm_reference."""
+    d, e = c.d, R.rel32(c.d)
+    w, keep = c.w.double() + c.plus_one, torch.from_numpy(c.keep).cuda()[:, None]
+    zero = torch.zeros((), dtype=torch.float64, device="cuda")
+    s = torch.where(keep, s.double(), zero)
+    dy = torch.where(keep, c.dy.double(), zero)
+    rstd = 1 / torch.sqrt((s * s).mean(1, keepdim=True) + EPS)
+    y = s * rstd * w
+    g = dy * w
+    dx = rstd * (g - s * rstd ** 2 * (g * s).mean(1, keepdim=True))
+    bx = 4 * e * rstd * (g.abs() + s.abs() * rstd ** 2 * (g * s).abs().mean(1, keepdim=True))
+    if dsum:
+        ds = torch.where(keep, c.ds.double(), zero)
+        dx, bx = dx + ds, bx + 2.0 ** -24 * (dx + ds).abs()
+    each = dy * s * rstd
+    return y, dx, bx, each.sum(0), (4 * e + (c.N + 16) * R.STEP32) * each.abs().sum(0)
+
+
+def within(got, want, bound, dtype):
+    return bool(((got.double() - want).abs() <= bound + R.HALF_STEP[dtype] * (want.abs() + bound) + R.TINY[dtype]).all())
+
+
+MANY = [(40000, 64), (30001, 192), (20000, 512), (9999, 576), (9000, 1088), (10001, 2048), (12000, 4096), (3000, 5120),
+        (2000, 6208), (1500, 8192), (900, 16384)]
+
+
+@pytest.mark.parametrize("N,d", MANY)
+@pytest.mark.parametrize("mask", ["some", "runs"])
+@pytest.mark.parametrize("dsum,ckpt", [(False, False), (True, False), (False, True), (True, True)])
+def test_many_rows(N, d, mask, dsum, ckpt):
+    """More rows than blocks, with masks that leave whole windows of rows out, and others in part."""
+    dt = "fp16" if N % 2 else "bf16"
+    c = Case(N, d, dt, weight="f32" if dsum else "16", seed=3)
+    if mask == "runs":                       # runs of 1 to 5000 rows that count or do not
+        ends = np.cumsum(np.exp(c.rng.uniform(0, np.log(5000), size=4000)).astype(int))
+        c.m = np.searchsorted(ends, np.arange(N), side="right") % 2 == 0
+    else:
+        c.m = c.rng.random(N) < 0.7
+    c.keep = c.m
+    c.mask = torch.from_numpy(c.m.astype(np.uint8)).cuda()
+    out = torch.from_numpy(~c.keep).cuda()
+    for t in (c.x, c.r, c.dy, c.ds):
+        t[out] = float("nan")
+    ck = c.pack() if ckpt else None
+    s = c.unpack(ck) if ckpt else c.x
+    y, dx, bx, dw, bw = gpu64(c, s, dsum)
+    got = c.fwd(x=ck)["y"]
+    assert within(got, y, R.rel32(d) * y.abs(), dt)
+    gx, gw, inf = c.bwd(x=ck, dsum=dsum)
+    dx[out] = 0.0
+    assert inf == 0 and not bool(gx[out].any())
+    assert within(gx, dx, bx, dt) and within(gw, dw, bw, "f32" if c.weight_f32 else dt)
+
+
+@pytest.mark.parametrize("d", [64, 128, 192, 512, 576, 4096])
+@pytest.mark.parametrize("turns", [1, 2, 3, 7, 8, 9, 15, 16, 17])
+def test_few_turns_of_rows(d, turns):
+    """Grids of one cluster, and the first ones beyond."""
+    rows = {64: 32, 128: 16, 192: 8, 512: 4}.get(d, 1)
+    for N in {turns * rows, max(1, turns * rows - rows + 1)}:
+        c = Case(N, d, "bf16", "some" if N > 3 else None)
+        check_grad(c, c.clean(c.x), True, True, c.bwd(dsum=True))
+        assert c.bwd(dsum=True, dweight=False)[2] == 0
+        c.dy[int(np.flatnonzero(c.keep)[-1]), d - 1] = float("inf")
+        assert c.bwd()[2] == 1 and c.bwd(dweight=False)[2] == 1
+
+
+@pytest.mark.parametrize("N,d", [(40, 64), (40, 1536)])
+def test_weights_that_are_not_finite(N, d):
+    """They reach their own column of the rows that count, and nothing of the others."""
+    c = Case(N, d, "bf16", "some", weight="f32")
+    c.w[3], c.w[5] = float("inf"), float("nan")
+    for y in ("16", "e4m3"):
+        v = host(c.fwd(y=y, y_scale=0.0 if y == "16" else 0.05, row_scale=False)["y"])
+        assert not v[~c.keep].any() and np.isnan(v[c.keep, 5]).all()
+        assert np.isfinite(np.delete(v, (3, 5), 1)).all()
+        assert (np.isinf(v) if y == "16" else np.abs(v) == 448)[c.keep, 3].all()
+    dx, _, inf = c.bwd()
+    assert inf == 1 and not host(dx)[~c.keep].any()
+
+
+def test_checked_build_gives_the_same_bits(monkeypatch):
+    from rl_fine_tuning_gb300 import build
+    c = Case(500, 1536, "bf16", "some")
+    k = _buffers(c)
+    _everything(c, k)
+    torch.cuda.synchronize()
+    want = _results(k)
+    monkeypatch.setattr(build, "LIB", build.LIB_CHECKED)
+    monkeypatch.setattr(rg, "_lib", None)
+    assert rg.grpo_device_checks()
+    k = _buffers(c)
+    _everything(c, k)
+    torch.cuda.synchronize()
+    assert _all_same(_results(k), want)
+
+
+def test_calls_follow_one_another_without_waits():
+    """Each call's input is the output of the one before, over and over on one stream, with other kernels between: the same
+    bits as with the device waited for after each."""
+    c = Case(700, 1536, "bf16")
+    o = rg.norm_opts(eps=EPS)
+    e = torch.empty_like
+    ws = torch.empty(rg.grpo_norm_workspace_bytes(c.shape), dtype=torch.uint8, device="cuda")
+    ck = torch.empty(c.N, c.d, dtype=torch.int8, device="cuda"), torch.empty(c.N, c.d // 64, dtype=torch.bfloat16, device="cuda")
+
+    def go(wait):
+        x, r, dx, dw = c.x.clone(), c.r.clone(), e(c.x), e(c.w)
+        y, inf = e(c.x), torch.zeros(1, dtype=torch.int32, device="cuda")
+        for i in range(12):
+            for call in (lambda: rg.grpo_norm_fwd(x, r, c.w, None, c.shape, o, y, None, r, ck),
+                         lambda: rg.grpo_ckpt_unpack(ck, None, c.shape, x),
+                         lambda: rg.grpo_norm_bwd(y, ck, c.w, x, None, c.shape, o, ws, dx, dw, inf),
+                         lambda: x.add_(dx, alpha=0.1),
+                         lambda: rg.grpo_ckpt_pack(x, None, c.shape, ck),
+                         lambda: rg.grpo_norm_bwd(x, ck, c.w, None, None, c.shape, o, ws, x, dw, inf)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return [x, r, y, dx, dw, *ck]
+
+    want = [t.clone() for t in go(True)]
+    for _ in range(3):
+        assert _all_same(go(False), want)
 
 
 def test_binding_checks_tensors():

@@ -55,7 +55,8 @@ def test_norm_forward_refusals(lib):
                      (dict(x=None, xc=ckpt(), r=None, out=ckpt()), 1), (dict(x=None, r=None, xc=ckpt(codes=None)), 1),
                      (dict(x=None, r=None, xc=ckpt(codes=P + 8)), 1), (dict(x=None, r=None, xc=ckpt(scales=P + 1)), 1),
                      (dict(x=None, r=None, xc=ckpt(scales=None)), 1), (dict(r=P + 2), 1), (dict(w=None), 1), (dict(w=P + 8), 1),
-                     (dict(y=None), 1), (dict(y=P + 8), 1), (dict(sum_=P + 8), 1), (dict(out=ckpt(codes=P + 4)), 1),
+                     (dict(x=P + 16), 1), (dict(r=P + 16), 1), (dict(y=P + 16), 1), (dict(sum_=P + 16), 1),
+                     (dict(y=P + 8, y_type=rg.E4M3, rs=P), 1), (dict(y=None), 1), (dict(y=P + 8), 1), (dict(sum_=P + 8), 1), (dict(out=ckpt(codes=P + 4)), 1),
                      (dict(out=ckpt(scales=None)), 1), (dict(rs=P), 1), (dict(y_type=rg.E4M3), 1),
                      (dict(y_type=rg.E4M3, rs=P + 2), 1), (dict(y_type=rg.E4M3, y_scale=1.0, rs=P + 1), 1),
                      (dict(s=False), 2), (dict(o=False), 2), (dict(eps=0.0), 2), (dict(eps=1e-39), 2), (dict(eps=-1.0), 2),
@@ -76,7 +77,7 @@ def test_norm_forward_refusals(lib):
             assert fwd(lib, o=o) == 2 and bwd(lib, o=o) == 2, field
     # calls that have nothing wrong with them come to the device
     for kw in (dict(), dict(r=None, sum_=None, mask=None), dict(x=None, xc=ckpt(), r=None), dict(out=ckpt(scales=P + 2)),
-               dict(y_type=rg.E4M3, rs=P), dict(y_type=rg.E5M2, y_scale=2.0 ** -126), dict(y_type=rg.E5M2, y_scale=2.0 ** 126),
+               dict(y_type=rg.E4M3, rs=P, y=P + 16), dict(w=P + 16), dict(y_type=rg.E5M2, y_scale=2.0 ** -126), dict(y_type=rg.E5M2, y_scale=2.0 ** 126),
                dict(y_type=rg.E4M3, y_scale=0.1, rs=P), dict(s=shape(d=16384)), dict(weight_f32=True, plus_one=True)):
         assert _has_gpu() or fwd(lib, **kw) in OK_SO_FAR, kw
 
@@ -84,7 +85,7 @@ def test_norm_forward_refusals(lib):
 def test_norm_gradient_refusals(lib):
     import rl_fine_tuning_gb300 as rg
     need = rg.grpo_norm_workspace_bytes(shape())
-    for kw, code in ((dict(dy=None), 1), (dict(dy=P + 8), 1), (dict(x=None), 1), (dict(xc=ckpt()), 1), (dict(x=P + 2), 1),
+    for kw, code in ((dict(dy=None), 1), (dict(dy=P + 16), 1), (dict(x=P + 16), 1), (dict(ds=P + 16), 1), (dict(dx=P + 16), 1), (dict(x=None), 1), (dict(xc=ckpt()), 1), (dict(x=P + 2), 1),
                      (dict(x=None, xc=ckpt(scales=P + 1)), 1), (dict(w=None), 1), (dict(w=P + 4), 1), (dict(ds=P + 8), 1),
                      (dict(ws=None), 1), (dict(ws=P + 128), 1), (dict(dx=None), 1), (dict(dx=P + 8), 1), (dict(dw=P + 8), 1),
                      (dict(inf=None), 1), (dict(inf=P + 2), 1), (dict(n=need - 1), 3), (dict(n=0), 3), (dict(s=False), 2),
@@ -96,10 +97,12 @@ def test_norm_gradient_refusals(lib):
 
 def test_checkpoint_refusals(lib):
     import rl_fine_tuning_gb300 as rg
+    huge = rg.make_shape(1, 1 << 10, (1 << 21) - (1 << 7), 65536, 1)     # 2^47 elements
+    assert rg.grpo_workspace_bytes(huge) > 0
     pack = lambda x=P, mask=None, s=shape(), c=ckpt(): lib.grpo_ckpt_pack(x, mask, s, c, None)  # noqa: E731
     unpack = lambda c=ckpt(), mask=None, s=shape(), x=P: lib.grpo_ckpt_unpack(c, mask, s, x, None)  # noqa: E731
     for f in (pack, unpack):
-        for kw, code in ((dict(x=None), 1), (dict(x=P + 8), 1), (dict(c=None), 1), (dict(c=ckpt(codes=P + 8)), 1),
+        for kw, code in ((dict(x=None), 1), (dict(x=P + 16), 1), (dict(s=huge), 2), (dict(c=None), 1), (dict(c=ckpt(codes=P + 8)), 1),
                          (dict(c=ckpt(codes=None)), 1), (dict(c=ckpt(scales=None)), 1), (dict(c=ckpt(scales=P + 1)), 1),
                          (dict(s=None), 2), (dict(s=shape(d=96)), 2), (dict(s=shape(G=0)), 2), (dict(s=shape(dtype=rg.E5M2)), 5)):
             assert f(**kw) == code, kw
@@ -155,3 +158,46 @@ def test_binding_refusals_of_types(lib):
                  lambda: rg.grpo_ckpt_pack(x, None, s8, (x, x)), lambda: rg.grpo_ckpt_unpack((x, x), None, s8, x)):
         with pytest.raises(rg.GrpoError):
             call()
+
+
+def test_plans_fit_an_sm(tmp_path, lib):
+    """How rows are dealt to blocks, for every width and a range of row counts: all of a row has a thread, the blocks an SM is
+    to have fit its registers and shared memory, and the partial sums fit the workspace."""
+    from rl_fine_tuning_gb300 import build
+    csrc, cuda = build.CSRC, os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build.nvcc()))), "include")
+    prog = tmp_path / "p.cpp"
+    prog.write_text('''#include <cstdio>
+#include "norm.h"
+using namespace grpo;
+int main() {
+    long n = 0, bad = 0;
+    for (int d = 64; d <= kNormMaxD; d += 64)
+        for (long N : {1L, 2L, 8L, 9L, 16L, 17L, 100L, 1000L, 9727L, 9728L, 1000000L, 2147418112L})
+            for (int i = 0; i < 4; ++i) {
+                const bool ck = i & 1, ds = i & 2;
+                const NormPlan o = norm_bwd_plan(N, d, kSmCount, ck, ds), f = norm_fwd_plan(N, d, kSmCount);
+                bool ok = o.width * o.upt * kUnit >= d && o.grid >= 1 && o.grid <= norm_parts(N, d) && o.threads <= kBlockMax;
+                ok = ok && norm_parts(N, d) <= 8 * kSmCount && (!o.joined || (o.grid <= 8 && (o.grid & (o.grid - 1)) == 0));
+                if (o.wide) {
+                    const long weight = long(o.width) * o.upt * kUnit * 4, row = weight / 4 * (2 + (ck ? 1 : 2) + (ds ? 2 : 0));
+                    ok = ok && o.threads == o.width && o.width % 32 == 0 && o.threads * (o.upt == 1 ? 80 : 128) * o.per_sm <= 65536;
+                    ok = ok && (weight + row + 2048) * o.per_sm <= 226 * 1024;          // one stage of the ring at least
+                } else {
+                    ok = ok && o.upt == 1 && o.threads == kWarpThreads && o.threads % o.width == 0 && o.threads * 96 * o.per_sm <= 65536;
+                }
+                ok = ok && f.width * f.upt * kUnit >= d && f.grid >= 1 && f.upt <= 2;
+                ok = ok && f.per_sm >= 1 && f.threads * (f.upt == 1 ? 64 : 128) * f.per_sm <= 65536;
+                const long turns = (N + f.threads / f.width - 1) / (f.threads / f.width);
+                ok = ok && f.grid <= turns && (f.grid >= turns || f.grid >= f.per_sm * kSmCount);
+                ++n;
+                bad += !ok;
+            }
+    printf("%ld %ld", n, bad);
+    return 0;
+}
+''')
+    exe = tmp_path / "p"
+    subprocess.check_call(["g++", "-std=c++17", "-I" + os.path.join(ROOT, "include"), "-I" + csrc, "-I" + cuda,
+                           "-x", "c++", str(prog), os.path.join(csrc, "norm_plan.cu"), "-o", str(exe)])
+    n, bad = (int(x) for x in subprocess.check_output([str(exe)], text=True).split())
+    assert n == 256 * 12 * 4 and bad == 0
