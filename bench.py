@@ -58,6 +58,9 @@ def parse():
     ap.add_argument("--cpu-seconds", type=float, default=15.0, help="target length of one oracle sample")
     ap.add_argument("--forward", action="store_true",
                     help="time the forward-only entry points (bf16 and e4m3 inputs) instead of fwd+bwd")
+    ap.add_argument("--stream", action="store_true",
+                    help="time the 8-bit step from the residual stream on: the model's last norm to E4M3 codes with an 8-bit "
+                         "checkpoint, the loss and its gradients, and the norm's gradient from the checkpoint")
     ap.add_argument("--split", action="store_true",
                     help="with N>1: one batch of N prompt groups split over the ranks (data-parallel shards), "
                          "the batch counts and dW summed over the ranks every step; default: N replicas")
@@ -748,6 +751,90 @@ def run_forward_modes(args, ranks):
         print(json.dumps(line), flush=True)
 
 
+def run_stream_mode(args, ranks):
+    """The 8-bit step from the residual stream to its gradient: grpo_norm_fwd of the policy's stream (E4M3 codes and an
+    8-bit checkpoint) and of the reference's, grpo_loss_fwd_bwd_fp8, and grpo_norm_bwd from the checkpoint."""
+    import math
+
+    import numpy as np
+    import torch
+
+    import rl_fine_tuning_gb300 as rg
+    import synth
+
+    torch.cuda.set_device(ranks.local)
+    rg.load(build_if_missing=True)
+    cfg = synth.make_config(args.config)
+    N, d, V = cfg.N, cfg.d, cfg.V
+    lengths_host = np.minimum(np.maximum(synth.lengths_for(cfg, 0), 0), cfg.L)
+    n_valid = int(lengths_host.sum())
+    shape8 = rg.make_shape(cfg.n_groups, cfg.G, cfg.L, d, V, rg.E4M3, beta=cfg.beta, eps=cfg.eps, chunk_rows=args.chunk_rows)
+    shape = rg.make_shape(cfg.n_groups, cfg.G, cfg.L, d, V, rg.BF16, beta=cfg.beta, eps=cfg.eps)
+    g = torch.Generator(device="cuda").manual_seed(0)
+
+    def randn(*size):
+        return torch.randn(*size, device="cuda", generator=g)
+
+    def empty(*size, dtype):
+        return torch.empty(*size, dtype=dtype, device="cuda")
+
+    # streams of both models before their last addition, a norm's weight, and a head in E4M3
+    x = randn(N, d).bfloat16()
+    block = (0.5 * randn(N, d)).bfloat16()
+    x_ref = (x.float() + 0.02 * randn(N, d)).bfloat16()
+    weight = (1.0 + 0.1 * randn(d)).bfloat16()
+    w_scale = 2.0 ** -9
+    W = (randn(V, d) * (d ** -0.5 / w_scale)).clamp(-448, 448).to(torch.float8_e4m3fn)
+    tokens = torch.randint(0, V, (N,), device="cuda", generator=g, dtype=torch.int32)
+    lengths = torch.from_numpy(lengths_host.astype(np.int32)).cuda()
+    rewards = randn(cfg.n_seq)
+    adv, mask = empty(cfg.n_seq, dtype=torch.float32), empty(N, dtype=torch.uint8)
+    h, h_ref = empty(N, d, dtype=torch.float8_e4m3fn), empty(N, d, dtype=torch.float8_e4m3fn)
+    ckpt = empty(N, d, dtype=torch.int8), empty(N, d // rg.CKPT_BLOCK, dtype=torch.bfloat16)
+    dH, dx, dweight = empty(N, d, dtype=torch.bfloat16), empty(N, d, dtype=torch.bfloat16), torch.empty_like(weight)
+    dW, loss = empty(V, d, dtype=torch.float32), empty(1, dtype=torch.float32)
+    status, inf = empty(1, dtype=torch.int32), empty(1, dtype=torch.int32)
+    ws = empty(rg.grpo_workspace_bytes(shape8), dtype=torch.uint8)
+    norm_ws = empty(rg.grpo_norm_workspace_bytes(shape), dtype=torch.uint8)
+    h_scale = math.sqrt(d) * float(weight.abs().max()) / 448      # nothing saturates
+    to8 = rg.norm_opts(y_type=rg.E4M3, y_scale=h_scale)
+
+    def step():
+        rg.grpo_group_advantages(rewards, cfg.n_groups, cfg.G, cfg.eps, True, adv)
+        rg.grpo_build_mask(lengths, shape, mask)
+        rg.grpo_norm_fwd(x, block, weight, mask, shape, to8, h, sum_ckpt=ckpt)
+        rg.grpo_norm_fwd(x_ref, block, weight, mask, shape, to8, h_ref)
+        rg.grpo_loss_fwd_bwd_fp8(h, h_ref, W, h_scale, h_scale, w_scale, tokens, mask, adv, shape8, ws, loss, dH, dW, None,
+                                 status)
+        rg.grpo_norm_bwd(dH, ckpt, weight, None, mask, shape, to8, norm_ws, dx, dweight, inf)
+
+    for _ in range(max(args.warmup, 1)):
+        step()
+    torch.cuda.synchronize()
+    if int(status.item()) != 0 or int(inf.item()) != 0:
+        raise SystemExit(f"device status {int(status.item())}, found_inf {int(inf.item())}")
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    for _ in range(args.steps):
+        step()
+    b.record()
+    torch.cuda.synchronize()
+    ms = a.elapsed_time(b) / args.steps
+    rg.grpo_profile_enable(True)                # per-kernel breakdown from a second, instrumented pass
+    for _ in range(args.steps):
+        step()
+    torch.cuda.synchronize()
+    rg.grpo_profile_enable(False)
+    kern = {k: round(v[0] / args.steps, 3) for k, v in rg.grpo_profile_collect().items() if v[1]}
+    line = {"metric": "GRPO 8-bit step from the residual stream, tokens/s", "value": n_valid / (ms / 1e3), "unit": "tokens/s",
+            "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms, "higher_is_better": True,
+            "scaling": "weak", "vs_baseline": None, "dtype": "e4m3", "data": "synthetic",
+            "config": cfg_dict(cfg, {"n_valid": n_valid}), "kernel_ms_per_step": kern, "loss": float(loss.item()),
+            "checkpoint_bytes": ckpt[0].numel() + 2 * ckpt[1].numel(), "stream_bytes": 2 * N * d}
+    if ranks.rank == 0:
+        print(json.dumps(line), flush=True)
+
+
 def cpu_baseline(cfg, wl, args):
     """The oracle, as it stands, on the host cores: a bounded sample of rows."""
     import oracle
@@ -772,6 +859,8 @@ def main():
             run_reference(args, ranks)
         elif args.forward:
             run_forward_modes(args, ranks)
+        elif args.stream:
+            run_stream_mode(args, ranks)
         else:
             run_ours(args, ranks)
     finally:

@@ -489,17 +489,18 @@ def _norm_setup():
 
 
 def _norm_table(shape):
-    """(type tables, the 16-bit type, the current device's number)"""
+    """(type tables, the 16-bit type, the current device's number, rows, columns)"""
     if _norm_types is None:
         _norm_setup()
-    if shape.dtype not in (BF16, FP16):
+    dtype = shape.dtype
+    if dtype != BF16 and dtype != FP16:
         raise GrpoError(5, "dtype check")
-    return _norm_types, _norm_types[shape.dtype], _device()
+    return _norm_types, _norm_types[dtype], _device(), shape.n_groups * shape.G * shape.L, shape.d
 
 
 def _here(x, name, types, numel, device):
     """As _arg, on the current device (a tensor in host memory has the number -1)."""
-    if x is None or isinstance(x, int):
+    if x is None or type(x) is int:
         return x
     if x.dtype in types and x.numel() == numel and x.get_device() == device and x.is_contiguous():
         return x.data_ptr()
@@ -537,8 +538,7 @@ def _on(stream, device):
 
 def grpo_norm_fwd(x, residual, weight, mask, shape, opts, y, row_scale=None, sum_out=None, sum_ckpt=None, stream=None):
     """y (16 or 8 bits, as opts.y_type says) of s = x + residual; x may be a checkpoint (codes, scales)."""
-    ty, t, dev = _norm_table(shape)
-    N, d = shape.N, shape.d
+    ty, t, dev, N, d = _norm_table(shape)
     n, f, y_type = N * d, ty["f32"], opts.y_type
     px, pc = _source(x, n, ty, t, dev)
     yt = t if y_type == shape.dtype else ty[y_type] if y_type in (E4M3, E5M2) else None
@@ -554,8 +554,7 @@ def grpo_norm_fwd(x, residual, weight, mask, shape, opts, y, row_scale=None, sum
 
 def grpo_norm_bwd(dy, x, weight, dsum, mask, shape, opts, workspace, dx, dweight, found_inf, stream=None):
     """dx and dweight (None: frozen) at s = x, a 16-bit matrix or a checkpoint (codes, scales)."""
-    ty, t, dev = _norm_table(shape)
-    N, d = shape.N, shape.d
+    ty, t, dev, N, d = _norm_table(shape)
     n, wt = N * d, ty["f32"] if opts.weight_f32 else t
     px, pc = _source(x, n, ty, t, dev)
     size = workspace.numel()
@@ -568,17 +567,15 @@ def grpo_norm_bwd(dy, x, weight, dsum, mask, shape, opts, workspace, dx, dweight
 
 def grpo_ckpt_pack(x, mask, shape, ckpt, stream=None):
     """A checkpoint (codes, scales) of x."""
-    ty, t, dev = _norm_table(shape)
-    N = shape.N
-    n = N * shape.d
+    ty, t, dev, N, d = _norm_table(shape)
+    n = N * d
     _check(load().grpo_ckpt_pack(_here(x, "x", t, n, dev), _here(mask, "mask", ty["mask"], N, dev), shape,
                                  _ckpt(ckpt, "ckpt", n, ty, dev), _on(stream, dev)), "grpo_ckpt_pack")
 
 
 def grpo_ckpt_unpack(ckpt, mask, shape, x_out, stream=None):
     """A checkpoint's values in 16 bits."""
-    ty, t, dev = _norm_table(shape)
-    N = shape.N
-    n = N * shape.d
+    ty, t, dev, N, d = _norm_table(shape)
+    n = N * d
     _check(load().grpo_ckpt_unpack(_ckpt(ckpt, "ckpt", n, ty, dev), _here(mask, "mask", ty["mask"], N, dev), shape,
                                    _here(x_out, "x_out", t, n, dev), _on(stream, dev)), "grpo_ckpt_unpack")

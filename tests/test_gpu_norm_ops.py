@@ -797,3 +797,18 @@ def test_norm_to_8_bits_grpo_loss_and_back():
     # the 8-bit loss's own dH is within 2e-2 of its largest entry; the rest is bf16's
     for got, want in ((host(dx), wx), (host(dw), ww)):
         assert np.linalg.norm(got - want) <= 0.05 * np.linalg.norm(want)
+
+
+def test_the_bench_runs_the_step_from_the_stream():
+    """Both norms, the 8-bit loss and its gradients, and the norm's gradient from the checkpoint, as one command."""
+    import json
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "bench.py", "--stream", "--config", "tiny", "--steps", "2", "--warmup", "1"], cwd=root,
+                         capture_output=True, text=True, timeout=280)
+    assert out.returncode == 0, out.stderr[-2000:]
+    line = json.loads(out.stdout.strip().splitlines()[-1])
+    assert np.isfinite(line["loss"]) and line["kernel_ms_per_step"]["norm"] > 0 and line["kernel_ms_per_step"]["norm_bwd"] > 0
+    assert line["checkpoint_bytes"] * 2 < line["stream_bytes"] * 1.04
