@@ -17,7 +17,7 @@ namespace {
 constexpr int kBwdRegs = 80, kBwdRegsTwo = 128;      // of a thread with one or two units: 768 or 512 threads an SM
 constexpr int kRowsRegs = 96;          // 640 threads an SM
 constexpr int kStagesMax = 2;          // more gain nothing: what is under way is limited by the number of blocks
-constexpr int kSmemSm = 226 * 1024;    // of an SM's 228 KB
+constexpr int kSmemSm = 226 * 1024, kSmemBlock = 2048;     // of an SM's 228 KB; what a block takes beside the ring and the weight
 
 // Both sums over a row's threads, in a fixed order; every thread gets them.
 __device__ __forceinline__ float2 warp_sums(float a, float b, int width) {
@@ -377,12 +377,13 @@ cudaError_t bwd_of(const NormParams& p, const NormPlan& o, cudaStream_t st) {
     const auto f = o.upt == 1 ? k_norm_bwd_wide<kBf16, kSrc, 1, kDsum> : k_norm_bwd_wide<kBf16, kSrc, 2, kDsum>;
     const size_t stage = weight / 4 * (2 + (kSrc == kCkpt ? 1 : 2) + (kDsum ? 2 : 0));
     NormParams r = p;
-    const size_t room = static_cast<size_t>(kSmemSm) / o.per_sm - 2048;
+    const size_t room = static_cast<size_t>(kSmemSm) / o.per_sm - kSmemBlock;
     if (room < weight + stage) return cudaErrorInvalidConfiguration;
     r.stages = static_cast<int>((room - weight) / stage);
     if (r.stages > kStagesMax) r.stages = kStagesMax;
     const size_t smem = weight + r.stages * stage;
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static MostSmem most[2];
+    const cudaError_t e = most[o.upt - 1].allow(f, kSmemSm - kSmemBlock);
     if (e != cudaSuccess) return e;
     return launch_chained(f, o.grid, o.threads, smem, r, st, o.joined ? o.grid : 1);
 }

@@ -1,6 +1,7 @@
 // Device helpers of the norm and the checkpoints: 16-bit pairs, pairs of fp32
 // numbers in one instruction, a row's loads, and the checkpoint's codes.
 #pragma once
+#include <atomic>
 #include <cfloat>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -32,6 +33,24 @@ cudaError_t launch_chained(void (*f)(P), int64_t grid, int threads, size_t smem,
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, f, p);
 }
+
+// Lets a kernel have the most shared memory that any call of it takes, once a device: the permission is the kernel's, not
+// a launch's, so that with each call's own size calls from two threads would take it from one another.
+struct MostSmem {
+    std::atomic<unsigned long long> given{0};          // a bit a device
+
+    template <class P>
+    cudaError_t allow(void (*f)(P), int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+        if (given.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) given.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
 
 // ---------------------------------------------------------------- pairs of fp32 numbers
 // sm_103 adds and multiplies two fp32 numbers in one instruction, each rounded as by

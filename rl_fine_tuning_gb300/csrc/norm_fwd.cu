@@ -174,8 +174,9 @@ cudaError_t fwd_of(const NormParams& p, const NormPlan& o, cudaStream_t st) {
     auto f = o.wide ? o.upt == 1 ? k_norm_fwd<kBf16, kSrc, 1, true, kOut8> : k_norm_fwd<kBf16, kSrc, 2, true, kOut8>
                     : o.upt == 1 ? k_norm_fwd<kBf16, kSrc, 1, false, kOut8> : k_norm_fwd<kBf16, kSrc, 2, false, kOut8>;
     const size_t smem = static_cast<size_t>(o.width) * o.upt * kUnit * 4;
-    if (smem > 40 * 1024) {                    // 48 KB with the rest need no permission
-        const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxD * 4);
+    if (smem > 40 * 1024) {                    // only the widest rows, two units a thread; 48 KB need no permission
+        static MostSmem most;
+        const cudaError_t e = most.allow(f, kNormMaxD * 4);
         if (e != cudaSuccess) return e;
     }
     return launch_chained(f, o.grid, o.threads, smem, p, st);

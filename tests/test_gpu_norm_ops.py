@@ -523,6 +523,34 @@ def test_two_host_threads():
     assert not errors and _all_same(_results(ka), wa) and _all_same(_results(kb), wb)
 
 
+def test_two_host_threads_with_different_shared_memory():
+    """The same kernel with 30 KB a block from one thread and 200 KB from another, first and in turn: no call takes the other's
+    permission away."""
+    cases = [Case(300, 1536, "fp16"), Case(40, 8128, "fp16"), Case(200, 5120, "fp16")]
+    want = [c.bwd(dsum=True) for c in cases]
+    start, errors = threading.Barrier(3), []
+
+    def work(c, w):
+        try:
+            start.wait(timeout=60)
+            with torch.cuda.stream(torch.cuda.Stream()):
+                o, ws = rg.norm_opts(eps=EPS), torch.empty(rg.grpo_norm_workspace_bytes(c.shape), dtype=torch.uint8, device="cuda")
+                dx, dw, inf = torch.empty_like(c.dy), torch.empty_like(c.w), torch.zeros(1, dtype=torch.int32, device="cuda")
+                for _ in range(300):
+                    rg.grpo_norm_bwd(c.dy, c.x, c.w, c.ds, None, c.shape, o, ws, dx, dw, inf)
+                torch.cuda.current_stream().synchronize()
+                assert same(dx, w[0]) and same(dw, w[1])
+        except Exception as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=x) for x in zip(cases, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
 def test_rows_alone_or_together():
     """A row's y, checkpoint and dx do not depend on the rows beside it."""
     c = Case(257, 1536, "bf16")
