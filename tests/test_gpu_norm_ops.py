@@ -497,6 +497,45 @@ def test_streams_and_graphs():
     assert _all_same(_results(ka), _results(fresh))
 
 
+def test_a_captured_fork_and_join():
+    """Calls that wait for two streams, captured and replayed, and next to other kernels, copies and memsets on their own."""
+    c = Case(600, 1536, "bf16")
+    o = rg.norm_opts(eps=EPS)
+    ws = torch.empty(rg.grpo_norm_workspace_bytes(c.shape), dtype=torch.uint8, device="cuda")
+    y, y2, dx, dw = torch.empty_like(c.x), torch.empty_like(c.x), torch.empty_like(c.x), torch.empty_like(c.w)
+    dy, x = torch.empty_like(c.x), torch.empty_like(c.x)
+    inf = torch.zeros(1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+
+    def go():
+        main = torch.cuda.current_stream()
+        x.copy_(c.x)
+        side.wait_stream(main)
+        rg.grpo_norm_fwd(x, None, c.w, None, c.shape, o, y)
+        with torch.cuda.stream(side):
+            y2.zero_()
+            rg.grpo_norm_fwd(x, c.r, c.w, None, c.shape, o, y2)
+            dy.copy_(y2)
+        main.wait_stream(side)
+        rg.grpo_norm_bwd(dy, y, c.w, y2, None, c.shape, o, ws, dx, dw, inf)
+        dx.mul_(0.5)
+        rg.grpo_norm_bwd(dx, y, c.w, None, None, c.shape, o, ws, dx, dw, inf)
+
+    go()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (y, y2, dx, dw, inf)]
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        go()
+    for _ in range(3):
+        for t in (y, y2, dx, dw):
+            t.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert _all_same([y, y2, dx, dw, inf], want)
+
+
 def test_two_host_threads():
     a, b = Case(500, 1536, "bf16", "some"), Case(1, 4096, "bf16")
     ka, kb = _buffers(a), _buffers(b)
