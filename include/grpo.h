@@ -499,7 +499,7 @@ typedef struct {
 
 void grpo_norm_opts_init(grpo_norm_opts* o, grpo_dtype dtype);
 
-/* Bytes of device workspace of grpo_norm_bwd: 4 d for each of up to 8 partial
+/* Bytes of device workspace of grpo_norm_bwd: 4 d for each of up to 12 partial
  * sums an SM, and their flags (7.5 MB for many rows of 4096).  0 for an invalid
  * shape. */
 size_t grpo_norm_workspace_bytes(const grpo_shape* shape);

@@ -38,18 +38,20 @@ NormPlan norm_fwd_plan(int64_t N, int d, int sm_count) {
 
 // Two units a thread where a block of one would fill an SM (d > 6144), and from a checkpoint, whose codes cost
 // instructions, where that leaves no thread without one (160,000 x 4096, 54% of the rows: 373 against 388 us).
-// Of wide rows an SM takes as many as bring its copies under way, two rows a
-// block, to about 80 KB (96 with dsum): 40,000 rows of 4096: 161 us with 64 KB, 149 with 96, 163 with
-// 144; of 2048: 170 with 48 KB, 153 with 64, 164 with 96, 176 with 144.
+// Of wide rows an SM takes as many as bring its copies under way, two rows a block, to 60 KB
+// and somewhat more than two rows: 40,000 rows of 4096: 162 us with 64 KB, 149 with 96, 163 with 144; 80,000 of 2048:
+// 170 with 48 KB, 153 with 64, 164 with 96; 160,000 of 1024: 149 with 64 KB, 162 with 80; 284,444 of 576: 255 with 36 KB,
+// 226 with 54.  With dsum, or from a checkpoint, where instructions count too, more does less harm; and rows that leave
+// threads without elements take longer and need more of them (131,072 of 1280: 171 us with 6 blocks, 159 with 8).
 NormPlan norm_bwd_plan(int64_t N, int d, int sm_count, bool ckpt, bool dsum) {
     const bool two = d / kUnit > 384 || (ckpt && !dsum && d / kUnit % 64 == 0 && N >= 64LL * sm_count);
     NormPlan o = row_plan(d, 32, two);
     const int64_t rows = o.threads / o.width, turns = (N + rows - 1) / rows;
     if (o.wide) {
         const int row = d * (2 + (ckpt ? 1 : 2) + (dsum ? 2 : 0)), most = (o.upt == 1 ? 768 : 512) / o.threads;
-        o.per_sm = ((dsum ? 96 : 80) * 1024 + row) / (2 * row);
+        const int64_t room = (60 + 4 * ckpt + 16 * dsum) * 1024 + row * 9 / 4;
+        o.per_sm = static_cast<int>(room * (o.width * o.upt * kUnit) / (2LL * row * d));
         if (o.per_sm > most) o.per_sm = most;
-        if (o.per_sm > 8) o.per_sm = 8;
         if (o.per_sm < 1) o.per_sm = 1;
     } else {
         o.per_sm = 5;                          // what 96 registers a thread leave: 155 us; 4 take 167, 6 in two waves 200

@@ -114,7 +114,7 @@ def test_norm_workspace(lib):
     import rl_fine_tuning_gb300 as rg
     w = lambda L, d: rg.grpo_norm_workspace_bytes(rg.make_shape(1, 8, L, d, 1))  # noqa: E731
     assert 456 * 4 * 4096 <= w(20000, 4096) < 456 * 4 * 4096 + 4096 and w(20000, 4096) == w(1000, 4096)
-    assert 4 * 64 <= w(1, 64) <= 1024 and all(w(100000, d) <= 8 * 152 * 4 * d + 8192 for d in range(64, 16385, 64))
+    assert 4 * 64 <= w(1, 64) <= 1024 and all(w(100000, d) <= 12 * 152 * 4 * d + 8192 for d in range(64, 16385, 64))
 
 
 def test_norm_structs_and_binding_refusals(tmp_path, lib):
@@ -177,7 +177,7 @@ int main() {
                 const bool ck = i & 1, ds = i & 2;
                 const NormPlan o = norm_bwd_plan(N, d, kSmCount, ck, ds), f = norm_fwd_plan(N, d, kSmCount);
                 bool ok = o.width * o.upt * kUnit >= d && o.grid >= 1 && o.grid <= norm_parts(N, d) && o.threads <= kBlockMax;
-                ok = ok && norm_parts(N, d) <= 8 * kSmCount && (!o.joined || (o.grid <= 8 && (o.grid & (o.grid - 1)) == 0));
+                ok = ok && norm_parts(N, d) <= 12 * kSmCount && (!o.joined || (o.grid <= 8 && (o.grid & (o.grid - 1)) == 0));
                 if (o.wide) {
                     const long weight = long(o.width) * o.upt * kUnit * 4, row = weight / 4 * (2 + (ck ? 1 : 2) + (ds ? 2 : 0));
                     ok = ok && o.threads == o.width && o.width % 32 == 0 && o.threads * (o.upt == 1 ? 80 : 128) * o.per_sm <= 65536;
