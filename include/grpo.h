@@ -537,7 +537,8 @@ int grpo_norm_fwd(const void* x, const grpo_ckpt* x_ckpt, const void* residual, 
  *   found_inf [1] int32 <- 1 if a value of dx or dweight is not finite, else 0
  *       (and 1 if a wait for a copy within the GPU ran out of time: the outputs
  *       are no gradients then)
- * A loss scale in dy and dsum is one in dx and dweight. */
+ * A loss scale in dy and dsum is one in dx and dweight.  rstd^2 |g| is formed in
+ * fp32 and has to stay below 3e38. */
 int grpo_norm_bwd(const void* dy, const void* x, const grpo_ckpt* x_ckpt, const void* weight, const void* dsum,
                   const uint8_t* mask, const grpo_shape* shape, const grpo_norm_opts* opts, void* workspace, size_t ws_bytes,
                   void* dx, void* dweight, int32_t* found_inf, grpo_stream_t stream);

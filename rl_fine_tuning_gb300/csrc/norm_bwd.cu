@@ -5,8 +5,8 @@
 // kept but s.  12 operations an element against 5 to 8 bytes: HBM bounds it, with
 // instructions close behind (the codes of a checkpoint take 5 an element).  dw is
 // summed in registers from row to row, then over the blocks in a fixed order.
-// Measured: 160,000 x 4096 from a checkpoint, 54% of the rows: 373 us, 6.4 TB/s (a copy reaches 6.8);
-// 40,000 x 4096 from 16 bits 148 us, with dsum 190 us (6.6 and 6.9 TB/s); 8192 x 1536, 60% of the rows,
+// Measured: 160,000 x 4096 from a checkpoint, 54% of the rows: 372 us, 6.4 TB/s (a copy reaches 6.8);
+// 40,000 x 4096 from 16 bits 149 us, with dsum 191 us (6.6 and 6.9 TB/s); 8192 x 1536, 60% of the rows,
 // with dsum: 18 us, of which the last 4 are the sum of dw over the blocks.
 #include "norm_device.cuh"
 
@@ -17,7 +17,8 @@ namespace {
 constexpr int kBwdRegs = 80, kBwdRegsTwo = 128;      // of a thread with one or two units: 768 or 512 threads an SM
 constexpr int kRowsRegs = 96;          // 640 threads an SM
 constexpr int kStagesMax = 2;          // more gain nothing: what is under way is limited by the number of blocks
-constexpr int kSmemSm = 226 * 1024, kSmemBlock = 2048;     // of an SM's 228 KB; what a block takes beside the ring and the weight
+constexpr int kSmemSm = 226 * 1024;    // of an SM's 228 KB
+constexpr int kSmemBlock = 2048;       // what a block takes of it beside the ring and the weight, and more
 
 // Both sums over a row's threads, in a fixed order; every thread gets them.
 __device__ __forceinline__ float2 warp_sums(float a, float b, int width) {
@@ -228,7 +229,8 @@ __global__ void __maxnreg__(kUpt == 1 ? kBwdRegs : kBwdRegsTwo) k_norm_bwd_wide(
         for (int k = 0; k < kUpt; ++k) {
             const int i = lane + k * width;
             Unit out = {};
-            if (live) out = unit_grad<kBf16, kDsum>(s[k], dy[k], ds[kDsum ? k : 0], staged_weight(s_weight, pad, i), rstd2, c2, acc[k]);
+            if (live)
+                out = unit_grad<kBf16, kDsum>(s[k], dy[k], ds[kDsum ? k : 0], staged_weight(s_weight, pad, i), rstd2, c2, acc[k]);
             if (i < n_unit) {
                 bad = mark_bad<kBf16>(bad, out);
                 store_unit(p.dx + at + i * kUnit, out);
@@ -373,7 +375,8 @@ template <bool kBf16, int kSrc, bool kDsum>
 cudaError_t bwd_of(const NormParams& p, const NormPlan& o, cudaStream_t st) {
     const size_t weight = static_cast<size_t>(o.width) * o.upt * kUnit * 4;
     if (!o.wide)                               // 8 KB at most: d <= 512
-        return launch_chained(k_norm_bwd_rows<kBf16, kSrc, kDsum>, o.grid, o.threads, weight * (kWarpThreads / 32), p, st, o.joined ? o.grid : 1);
+        return launch_chained(k_norm_bwd_rows<kBf16, kSrc, kDsum>, o.grid, o.threads, weight * (kWarpThreads / 32), p, st,
+                              o.joined ? o.grid : 1);
     const auto f = o.upt == 1 ? k_norm_bwd_wide<kBf16, kSrc, 1, kDsum> : k_norm_bwd_wide<kBf16, kSrc, 2, kDsum>;
     const size_t stage = weight / 4 * (2 + (kSrc == kCkpt ? 1 : 2) + (kDsum ? 2 : 0));
     NormParams r = p;
