@@ -185,7 +185,7 @@ __global__ void __maxnreg__(kUpt == 1 ? kBwdRegs : kBwdRegsTwo) k_norm_bwd_wide(
         for (int j = 0; j < 8; ++j) acc[k][j] = 0;
     uint32_t bad = 0, phase = 0;
     stage_weight<kBf16>(p, s_weight, pad);
-    if (threadIdx.x < 2 * kBlockMax / 16) s_join[0][threadIdx.x] = 0.f;
+    for (int i = lane; i < 2 * kBlockMax / 16; i += width) s_join[0][i] = 0.f;     // a block may be one warp
     __syncthreads();
     int q = 0, turn = 0;
     for (; t < N; t += step, at += at_step) {

@@ -64,7 +64,7 @@ __global__ void __maxnreg__(kUpt == 1 ? kFwdRegs : kFwdRegsTwo) k_norm_fwd(const
     uint32_t alive = ahead.bits(kWide ? 32 : width);       // bit q: row t + q step counts
     load_row<kSrc, kUpt, kWide>(p, at, alive & 1, lane, width, n_unit, &raw);
     stage_weight<kBf16>(p, s_weight, pad);
-    if (threadIdx.x < 4 * kBlockMax / 32) s_join[0][threadIdx.x] = 0.f;
+    for (unsigned i = threadIdx.x; i < 4 * kBlockMax / 32; i += blockDim.x) s_join[0][i] = 0.f;
     __syncthreads();
     int turn = 0;
     for (uint32_t base = first; base < N; base += step, t += step, at += at_step) {   // whole blocks go round together

@@ -772,6 +772,46 @@ def test_binding_checks_tensors():
                          torch.zeros(1, dtype=torch.int32, device="cuda"))
 
 
+# ---------------------------------------------------------------- gradients from a checkpoint, many rows
+
+def _gpu_stream(N, d, dt="bf16", seed=0):
+    """dy and a checkpoint of random rows, made on the device."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x, dy = (torch.randn(N, d, device="cuda", generator=g).to(R.TORCH[dt]) for _ in range(2))
+    ck = torch.empty(N, d, dtype=torch.int8, device="cuda"), torch.empty(N, d // 64, dtype=torch.bfloat16, device="cuda")
+    rg.grpo_ckpt_pack(x, None, rg.make_shape(1, 1, N, d, 1, DT[dt]), ck)
+    return dy, ck
+
+
+def _ckpt_grad(dy, ck, w, dt="bf16"):
+    N, d = dy.shape
+    s = rg.make_shape(1, 1, N, d, 1, DT[dt])
+    ws = torch.empty(rg.grpo_norm_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+    dx, dw, inf = torch.empty_like(dy), torch.empty_like(w), torch.zeros(1, dtype=torch.int32, device="cuda")
+    rg.grpo_norm_bwd(dy, ck, w, None, None, s, rg.norm_opts(eps=EPS), ws, dx, dw, inf)
+    return dx, dw, inf
+
+
+@pytest.mark.parametrize("N", [9700, 9728, 40000])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("mask", [None, "some"])
+def test_gradient_of_rows_in_one_warp(N, dt, mask):
+    """1024 columns from a checkpoint, after calls of other widths, which leave their rows' sums in shared memory: within the
+    bounds, and the same bits each time."""
+    c = Case(N, 1024, dt, mask, seed=11)
+    ck = c.pack()
+    _, dx, bx, dw, bw = gpu64(c, c.unpack(ck), False)
+    dx[~torch.from_numpy(c.keep).cuda()] = 0.0
+    first = None
+    for d in (2048, 4096, 512):
+        other = _gpu_stream(9728, d, dt)
+        _ckpt_grad(*other, torch.ones(d, dtype=R.TORCH[dt], device="cuda"), dt)
+        gx, gw, inf = c.bwd(x=ck)
+        assert inf == 0 and within(gx, dx, bx, dt) and within(gw, dw, bw, dt)
+        first = first or (gx, gw)
+        assert same(gx, first[0]) and same(gw, first[1])
+
+
 # ---------------------------------------------------------------- together with the losses
 
 def _chain(dt8):

@@ -205,3 +205,32 @@ int main() {
                            "-x", "c++", str(prog), os.path.join(csrc, "norm_plan.cu"), "-o", str(exe)])
     n, bad = (int(x) for x in subprocess.check_output([str(exe)], text=True).split())
     assert n == 256 * 12 * 4 and bad == 0
+
+
+def test_blocks_of_wide_rows(tmp_path, lib):
+    """What the kernels of wide rows ask of a block: whole warps, one at least, as many as their sums in shared memory have
+    places for, and elements for every one of the warps."""
+    from rl_fine_tuning_gb300 import build
+    csrc, cuda = build.CSRC, os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build.nvcc()))), "include")
+    prog = tmp_path / "p.cpp"
+    prog.write_text('''#include <cstdio>
+#include "norm.h"
+using namespace grpo;
+int main() {
+    int bad = 0;
+    for (int d = 64; d <= kNormMaxD; d += 64)
+        for (long N : {1L, 9727L, 9728L, 1000000L})
+            for (int i = 0; i < 5; ++i) {
+                const NormPlan o = i < 4 ? norm_bwd_plan(N, d, kSmCount, i & 1, i & 2) : norm_fwd_plan(N, d, kSmCount);
+                if (!o.wide) continue;
+                bad += o.threads != o.width || o.threads % 32 || o.threads < 32 || o.threads > kBlockMax;
+                bad += (o.width - 32) * o.upt * kUnit >= d || o.upt < 1 || o.upt > 2;
+            }
+    printf("%d", bad);
+    return 0;
+}
+''')
+    exe = tmp_path / "p"
+    subprocess.check_call(["g++", "-std=c++17", "-I" + os.path.join(ROOT, "include"), "-I" + csrc, "-I" + cuda,
+                           "-x", "c++", str(prog), os.path.join(csrc, "norm_plan.cu"), "-o", str(exe)])
+    assert subprocess.check_output([str(exe)], text=True) == "0"
