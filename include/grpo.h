@@ -458,7 +458,9 @@ int grpo_pair_loss_fwd_bwd(const void* h, const void* W, const int32_t* tokens, 
  * behind row N.  Outputs overlap neither inputs nor one another, but a 16-bit
  * output of the same shape may be the same pointer as a 16-bit input (sum_out =
  * residual, dx = dy).  Sums are in fp32 in a fixed order, every output is bitwise
- * reproducible, and calls can be captured into a CUDA graph. */
+ * reproducible, and no row's outputs depend on the rows beside it or on how many
+ * there are (dweight, a sum over the rows, does).  Calls can be captured into a
+ * CUDA graph. */
 
 /* Columns of a row that share one scale of a checkpoint. */
 #define GRPO_CKPT_BLOCK 64

@@ -31,19 +31,34 @@ __device__ __forceinline__ float2 warp_sums(float a, float b, int width) {
 
 // Here the lower lanes of a warp join a, the upper ones b.  The warps leave theirs in s, of which the next row takes
 // the other half, so that one barrier is enough; entries of warps that are not there hold 0.
+// From a checkpoint without dsum (kEither) a row may have two units a thread or one, as the number of rows has it.  Its
+// gradient is not to depend on that, so both add the same numbers in the same order:
+//   two:  units half a row apart in the thread; lanes 16, 1, 2, 4 and 8 apart; the warps in turn
+//   one:  those are lanes 16 apart, and 16 units lanes 8 (see one_as_two); lanes 1, 2 and 4 apart; two warps, 8 units
+//         apart; these pairs in turn
+template <int kUpt, bool kEither>
 __device__ __forceinline__ float2 block_sums(float a, float b, float* s) {
     const bool upper = threadIdx.x & 16;
     float v = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int i = 0; i < 4; ++i)
+        v += __shfl_xor_sync(0xffffffffu, v, !kEither ? 8 >> i : kUpt == 2 ? 1 << i : i == 0 ? 8 : 1 << (i - 1));
     if ((threadIdx.x & 15) == 0) s[threadIdx.x >> 4] = v;
     __syncthreads();
     F2 sum = 0;
     for (unsigned i = 0; i < blockDim.x; i += 64) {
         const float4 x = *reinterpret_cast<const float4*>(s + i / 16);
-        sum = f2_add(f2_add(sum, f2(x.x, x.y)), f2(x.z, x.w));
+        if (kEither && kUpt == 1)
+            sum = f2_add(sum, f2_add(f2(x.x, x.y), f2(x.z, x.w)));
+        else
+            sum = f2_add(f2_add(sum, f2(x.x, x.y)), f2(x.z, x.w));
     }
     return f2_values(sum);
+}
+
+// The unit of a thread that has one, dealt as above: 8 lanes have 8 units that lie together.
+__device__ __forceinline__ int one_as_two(int lane, int n_unit) {
+    return (lane >> 6) * 32 + (lane >> 3 & 1) * 16 + (lane >> 5 & 1) * 8 + (lane & 7) + (lane >> 4 & 1) * (n_unit / 2);
 }
 
 // A unit's part of both sums: s^2, and s (dy w).
@@ -136,7 +151,9 @@ __global__ void __maxnreg__(kUpt == 1 ? kBwdRegs : kBwdRegsTwo) k_norm_bwd_wide(
     __shared__ int s_abort;
     extern __shared__ float4 s_weight[];
     const int n_unit = p.d / kUnit, width = static_cast<int>(blockDim.x), pad = width * kUpt;
+    constexpr bool kEither = kSrc == kCkpt && !kDsum;
     const int lane = static_cast<int>(threadIdx.x);
+    const int unit0 = kUpt == 1 && kEither && n_unit % 64 == 0 ? one_as_two(lane, n_unit) : lane;      // the thread's first unit
     const uint32_t N = static_cast<uint32_t>(p.N), step = gridDim.x;      // N < 2^31
     const float inv_d = 1.f / p.d;
     chain_wait();
@@ -173,7 +190,7 @@ __global__ void __maxnreg__(kUpt == 1 ? kBwdRegs : kBwdRegsTwo) k_norm_bwd_wide(
     auto load_scales = [&](int64_t at, bool on) {
 #pragma unroll
         for (int k = 0; k < (kSrc == kCkpt ? kUpt : 0); ++k) {
-            const int i = lane + k * width;
+            const int i = unit0 + k * width;
             scale[k] = load_scale(p.scales + at / kCkptBlock + i / (kCkptBlock / kUnit), on && i < n_unit);
         }
     };
@@ -200,7 +217,7 @@ __global__ void __maxnreg__(kUpt == 1 ? kBwdRegs : kBwdRegsTwo) k_norm_bwd_wide(
             const uint32_t from = smem_u32(ring) + q * stage;
 #pragma unroll
             for (int k = 0; k < kUpt; ++k) {
-                const uint32_t i = lane + k * width;
+                const uint32_t i = unit0 + k * width;
                 dy[k] = read_unit(from + i * (kUnit * 2));
                 if (kSrc == kCkpt)
                     s[k] = decode<kBf16>(read16(from + matrix + i * kUnit), bf16_value(scale[k]));
@@ -213,10 +230,10 @@ __global__ void __maxnreg__(kUpt == 1 ? kBwdRegs : kBwdRegsTwo) k_norm_bwd_wide(
         if (live) {
 #pragma unroll
             for (int k = 0; k < kUpt; ++k) {
-                const float2 u = unit_sums<kBf16>(s[k], dy[k], staged_weight(s_weight, pad, lane + k * width));
-                if (lane + k * width < n_unit) sums = make_float2(sums.x + u.x, sums.y + u.y);
+                const float2 u = unit_sums<kBf16>(s[k], dy[k], staged_weight(s_weight, pad, unit0 + k * width));
+                if (unit0 + k * width < n_unit) sums = make_float2(sums.x + u.x, sums.y + u.y);
             }
-            sums = block_sums(sums.x, sums.y, s_join[turn]);
+            sums = block_sums<kUpt, kEither>(sums.x, sums.y, s_join[turn]);
             turn ^= 1;
         }
         // the whole block has read stage q: of this row above, or of the last one that was in it
@@ -227,7 +244,7 @@ __global__ void __maxnreg__(kUpt == 1 ? kBwdRegs : kBwdRegsTwo) k_norm_bwd_wide(
         const F2 rstd2 = f2(rstd, rstd), c2 = f2(c, c);
 #pragma unroll
         for (int k = 0; k < kUpt; ++k) {
-            const int i = lane + k * width;
+            const int i = unit0 + k * width;
             Unit out = {};
             if (live)
                 out = unit_grad<kBf16, kDsum>(s[k], dy[k], ds[kDsum ? k : 0], staged_weight(s_weight, pad, i), rstd2, c2, acc[k]);
@@ -245,7 +262,7 @@ __global__ void __maxnreg__(kUpt == 1 ? kBwdRegs : kBwdRegsTwo) k_norm_bwd_wide(
     float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.d;
 #pragma unroll
     for (int k = 0; k < kUpt; ++k) {
-        const int i = lane + k * width;
+        const int i = unit0 + k * width;
         if (i >= n_unit || !p.dweight) break;
         uint32_t w[16];
 #pragma unroll

@@ -812,6 +812,18 @@ def test_gradient_of_rows_in_one_warp(N, dt, mask):
         assert same(gx, first[0]) and same(gw, first[1])
 
 
+@pytest.mark.parametrize("d", [1024, 2048, 4096, 6144, 8192])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_rows_from_a_checkpoint_alone_or_together(d, dt):
+    """dx of a row from a checkpoint does not depend on how many rows are beside it."""
+    dy, ck = _gpu_stream(10000, d, dt, seed=d)
+    w = torch.ones(d, dtype=R.TORCH[dt], device="cuda")
+    whole = _ckpt_grad(dy, ck, w, dt)[0]
+    for a, b in ((0, 1), (3, 20), (100, 1000), (9990, 10000), (0, 9727)):
+        part = _ckpt_grad(dy[a:b], (ck[0][a:b], ck[1][a:b]), w, dt)[0]
+        assert same(part, whole[a:b]), (a, b)
+
+
 # ---------------------------------------------------------------- together with the losses
 
 def _chain(dt8):
