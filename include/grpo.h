@@ -536,9 +536,10 @@ int grpo_norm_fwd(const void* x, const grpo_ckpt* x_ckpt, const void* residual, 
  *   dx [N x d] (written): the gradient in x and in residual
  *   dweight: NULL (a frozen weight) or [d] of the weight's type, 16-byte aligned
  *       (written)
- *   found_inf [1] int32 <- 1 if a value of dx or dweight is not finite, else 0
- *       (and 1 if a wait for a copy within the GPU ran out of time: the outputs
- *       are no gradients then)
+ *   found_inf [1] int32 <- 0; 1 if a value of dx or dweight is not finite; 2 if a
+ *       wait for a copy within the GPU ran out of time (GRPO_ERR_TIMEOUT of the
+ *       calls that have a status word): the outputs are no gradients then, whatever
+ *       the loss scale
  * A loss scale in dy and dsum is one in dx and dweight.  rstd^2 |g| is formed in
  * fp32 and has to stay below 3e38. */
 int grpo_norm_bwd(const void* dy, const void* x, const grpo_ckpt* x_ckpt, const void* weight, const void* dsum,

@@ -553,7 +553,8 @@ def grpo_norm_fwd(x, residual, weight, mask, shape, opts, y, row_scale=None, sum
 
 
 def grpo_norm_bwd(dy, x, weight, dsum, mask, shape, opts, workspace, dx, dweight, found_inf, stream=None):
-    """dx and dweight (None: frozen) at s = x, a 16-bit matrix or a checkpoint (codes, scales)."""
+    """dx and dweight (None: frozen) at s = x, a 16-bit matrix or a checkpoint (codes, scales).  found_inf: 1 if they are not
+    all finite, 2 if a wait on the device ran out of time and they are no gradients, else 0."""
     ty, t, dev, N, d = _norm_table(shape)
     n, wt = N * d, ty["f32"] if opts.weight_f32 else t
     px, pc = _source(x, n, ty, t, dev)

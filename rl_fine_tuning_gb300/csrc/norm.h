@@ -43,7 +43,7 @@ struct NormParams {
     uint16_t* dx;
     void* dweight;               // nullable
     float* part;                 // [parts x d]
-    int* bad;                    // [parts] whether a part met a gradient that is not finite
+    int* bad;                    // [parts] whether a part met a gradient that is not finite (1), or a wait ran out (2)
     int parts;
     bool joined;                 // the blocks are one cluster and join their sums themselves
     int stages;                  // of the ring that rows are copied into

@@ -92,6 +92,9 @@ __device__ __forceinline__ Unit unit_grad(Unit s, Unit dy, const Unit& ds, const
     return rounded<kBf16>(x);
 }
 
+// What found_inf says; the larger one, where it could say both.
+constexpr int kNotFiniteValue = 1, kWaitRanOut = 2;
+
 // A pair that turns NaN with the first value that is not finite.
 template <bool kBf16>
 __device__ __forceinline__ uint32_t mark_bad(uint32_t bad, const Unit& x) {
@@ -122,15 +125,15 @@ __device__ __forceinline__ bool store_dweight(const NormParams& p, int j, float 
 template <bool kBf16>
 __device__ __forceinline__ void join_cluster(const NormParams& p) {
     cluster_sync();
-    bool bad = false;
-    if (blockIdx.x == 0 && threadIdx.x < gridDim.x) bad = p.bad[threadIdx.x] != 0;
+    int bad = 0;
+    if (blockIdx.x == 0 && threadIdx.x < gridDim.x) bad = p.bad[threadIdx.x];
     if (p.dweight)
         for (int j = blockIdx.x * blockDim.x + threadIdx.x; j < p.d; j += gridDim.x * blockDim.x) {
             float v = 0.f;
             for (unsigned b = 0; b < gridDim.x; ++b) v += p.part[static_cast<int64_t>(b) * p.d + j];
-            bad |= store_dweight<kBf16>(p, j, v);
+            if (store_dweight<kBf16>(p, j, v)) bad = max(bad, kNotFiniteValue);
         }
-    if (bad) *p.found_inf = 1;             // 0 before, in block 0
+    if (bad) atomicMax(p.found_inf, bad);  // 0 before, in block 0
 }
 
 __device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
@@ -143,7 +146,7 @@ __device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t b
 // come into a ring of p.stages stages in shared memory, one bulk copy a matrix: loads
 // into registers took 16 to 24 of them, and so fewer rows an SM (475 us with two rows of 4096, 408 with three).
 // Block b leaves its sum of dy s rstd of every column in part[b].
-// A wait that runs out of time leaves garbage in its row; the block goes on, and found_inf says so.
+// A wait that runs out of time leaves garbage in its row; the block goes on, and found_inf says so (2).
 template <bool kBf16, int kSrc, int kUpt, bool kDsum>
 __global__ void __maxnreg__(kUpt == 1 ? kBwdRegs : kBwdRegsTwo) k_norm_bwd_wide(const NormParams p) {
     __shared__ alignas(16) float s_join[2][kBlockMax / 16];
@@ -256,9 +259,9 @@ __global__ void __maxnreg__(kUpt == 1 ? kBwdRegs : kBwdRegsTwo) k_norm_bwd_wide(
     }
 
     chain_next();
-    const int any = __syncthreads_or(is_bad<kBf16>(bad) || s_abort);
+    const int any = __syncthreads_or(is_bad<kBf16>(bad));
     abort_grace(&s_abort);
-    if (threadIdx.x == 0) p.bad[blockIdx.x] = any;
+    if (threadIdx.x == 0) p.bad[blockIdx.x] = s_abort ? kWaitRanOut : any ? kNotFiniteValue : 0;
     float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.d;
 #pragma unroll
     for (int k = 0; k < kUpt; ++k) {
@@ -333,7 +336,7 @@ __global__ void __maxnreg__(kRowsRegs) k_norm_bwd_rows(const NormParams p) {
 
     chain_next();
     const int any = __syncthreads_or(is_bad<kBf16>(bad));
-    if (threadIdx.x == 0) p.bad[blockIdx.x] = any;
+    if (threadIdx.x == 0) p.bad[blockIdx.x] = any ? kNotFiniteValue : 0;
     // the rows of a warp, then the warps of the block, in this order; in the weight's place
     float* s_dw = reinterpret_cast<float*>(s_weight);
     const int warp = threadIdx.x >> 5, wide = pad * kUnit;
@@ -366,10 +369,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_norm_join(const NormParams p) 
     __shared__ float s_part[kJoinThreads / kJoinCols][kJoinCols + 1];
     const int slots = static_cast<int>(blockDim.x) / kJoinCols, lane = threadIdx.x & 31;
     const int slot = threadIdx.x / kJoinCols, col = threadIdx.x % kJoinCols;
-    bool bad = false;
+    int bad = 0;
     chain_wait();
     if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < p.parts; b += blockDim.x) bad |= p.bad[b] != 0;
+        for (int b = threadIdx.x; b < p.parts; b += blockDim.x) bad = max(bad, p.bad[b]);
     if (p.dweight) {
         const float* part = p.part + blockIdx.x * kJoinCols + col;
         float v = 0.f;
@@ -382,10 +385,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_norm_join(const NormParams p) 
             v = 0.f;
             for (int i = lane; i < slots; i += 32) v += s_part[i][j];
             for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (lane == 0) bad |= store_dweight<kBf16>(p, blockIdx.x * kJoinCols + j, v);
+            if (lane == 0 && store_dweight<kBf16>(p, blockIdx.x * kJoinCols + j, v)) bad = max(bad, kNotFiniteValue);
         }
     }
-    if (bad) *p.found_inf = 1;             // 0 before: the kernel that left the parts
+    if (bad) atomicMax(p.found_inf, bad);  // 0 before: the kernel that left the parts
 }
 
 template <bool kBf16, int kSrc, bool kDsum>
