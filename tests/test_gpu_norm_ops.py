@@ -690,6 +690,16 @@ def test_few_turns_of_rows(d, turns):
         assert c.bwd()[2] == 1 and c.bwd(dweight=False)[2] == 1
 
 
+@pytest.mark.parametrize("d", [6208, 8192, 16384])
+@pytest.mark.parametrize("N", [1, 8, 9, 16, 17])
+@pytest.mark.parametrize("dsum,ckpt", [(True, False), (False, True), (True, True)])
+def test_the_widest_rows_of_one_cluster(d, N, dsum, ckpt):
+    """Up to eight blocks of a cluster, each with most of an SM's shared memory, and the first grid beyond."""
+    c = Case(N, d, "fp16" if N % 2 else "bf16", "some" if N > 3 else None, weight="f32")
+    ck = c.pack() if ckpt else None
+    check_grad(c, host(c.unpack(ck)) if ckpt else c.clean(c.x), dsum, True, c.bwd(x=ck, dsum=dsum))
+
+
 @pytest.mark.parametrize("N,d", [(40, 64), (40, 1536)])
 def test_weights_that_are_not_finite(N, d):
     """They reach their own column of the rows that count, and nothing of the others."""

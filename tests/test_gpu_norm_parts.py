@@ -22,6 +22,38 @@ def run(tmp_path, source):
                                    env={**os.environ, "LD_LIBRARY_PATH": os.path.dirname(lib)}).split()
 
 
+def test_the_reciprocal_of_every_scale(tmp_path):
+    """Each bf16 number from 2^-126 to 2^121, the scales of a checkpoint: the correctly rounded 1 / scale.  (In 64 bits 1 / s of an
+    8-bit s lies at least 2^-33 of itself from where fp32 rounds the other way, so that rounding it again changes nothing.)"""
+    out = run(tmp_path, '''#include <cstdio>
+#include <cstring>
+#include "norm_device.cuh"
+using namespace grpo;
+constexpr int kFirst = 0x0080, kLast = 0x7c00, kN = kLast - kFirst + 1;
+__global__ void k(float* r) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < kN) r[i] = scale_reciprocal(bf16_value(kFirst + i));
+}
+int main() {
+    static float r[kN];
+    float* dev;
+    if (cudaMalloc(&dev, sizeof(r)) != cudaSuccess) return 1;
+    k<<<(kN + 255) / 256, 256>>>(dev);
+    if (cudaMemcpy(r, dev, sizeof(r), cudaMemcpyDeviceToHost) != cudaSuccess) return 1;
+    int bad = 0;
+    for (int i = 0; i < kN; ++i) {
+        const uint32_t bits = uint32_t(kFirst + i) << 16;
+        float s;
+        memcpy(&s, &bits, 4);
+        bad += r[i] != float(1.0 / double(s));
+    }
+    printf("%d %d", kN, bad);
+    return 0;
+}
+''')
+    assert out == [str(0x7c00 - 0x80 + 1), "0"]
+
+
 def test_a_wait_that_ran_out_is_not_an_overflow(tmp_path):
     """What the blocks leave (0: nothing, 1: a value that is not finite, 2: a wait that ran out of time) and a sum of dw that is not
     finite, joined: found_inf is the largest."""
