@@ -540,8 +540,8 @@ int grpo_norm_fwd(const void* x, const grpo_ckpt* x_ckpt, const void* residual, 
  *       wait for a copy within the GPU ran out of time (GRPO_ERR_TIMEOUT of the
  *       calls that have a status word): the outputs are no gradients then, whatever
  *       the loss scale
- * A loss scale in dy and dsum is one in dx and dweight.  rstd^2 |g| is formed in
- * fp32 and has to stay below 3e38. */
+ * A loss scale in dy and dsum is one in dx and dweight.  rstd^2 |g|, and a row's
+ * sums of s^2 and of |g s|, are formed in fp32 and have to stay below 3e38. */
 int grpo_norm_bwd(const void* dy, const void* x, const grpo_ckpt* x_ckpt, const void* weight, const void* dsum,
                   const uint8_t* mask, const grpo_shape* shape, const grpo_norm_opts* opts, void* workspace, size_t ws_bytes,
                   void* dx, void* dweight, int32_t* found_inf, grpo_stream_t stream);
@@ -589,8 +589,9 @@ unsigned long long grpo_kernel_launches(void);
  * device data (the valid-row list) and the offset arithmetic of the chunk
  * buffers: a failing check skips the access and sets *status to
  * GRPO_ERR_BOUNDS.  It stands in for a memory checker; the pages have no
- * counterpart.  grpo_device_checks() returns 1 in that build, 0 in the normal
- * one.  grpo_selftest_bounds_check makes one such check fail on purpose (a
+ * counterpart.  The kernels of grpo_norm_* and grpo_ckpt_* take no index from
+ * device data and are the same in both builds.  grpo_device_checks() returns 1 in
+ * that build, 0 in the normal one.  grpo_selftest_bounds_check makes one such check fail on purpose (a
  * guarded store one past a 16-element shared array, refused by the check):
  * *status (device int32) then reads GRPO_ERR_BOUNDS.  In the normal build it
  * launches nothing and returns GRPO_ERR_DEVICE. */

@@ -15,6 +15,8 @@ namespace grpo {
 // skips the access.  In the normal build it is the constant true and costs
 // nothing.  The checks cover every global index a kernel takes from device
 // data (the valid-row list) and the offset arithmetic of the chunk buffers.
+// (The norm's and the checkpoints' kernels take no index from device data and have
+// none: both builds of them are the same code.)
 #ifdef GRPO_DEVICE_CHECKS
 __device__ inline bool dcheck(bool ok, int* status) {
     if (!ok) atomicCAS(status, 0, GRPO_ERR_BOUNDS);

@@ -7,7 +7,7 @@
 // summed in registers from row to row, then over the blocks in a fixed order.
 // Measured: 160,000 x 4096 from a checkpoint, 54% of the rows: 372 us, 6.4 TB/s (a copy reaches 6.8);
 // 40,000 x 4096 from 16 bits 149 us, with dsum 191 us (6.6 and 6.9 TB/s); 8192 x 1536, 60% of the rows,
-// with dsum: 18 us, of which the last 4 are the sum of dw over the blocks.
+// with dsum: 18 us, or 14.9 where the inputs stay in L2, and there 12.6 without dw (its parts and their sum).
 #include "norm_device.cuh"
 
 namespace grpo {
@@ -15,7 +15,7 @@ namespace grpo {
 namespace {
 
 constexpr int kBwdRegs = 80, kBwdRegsTwo = 128;      // of a thread with one or two units: 768 or 512 threads an SM
-constexpr int kRowsRegs = 96;          // 640 threads an SM
+constexpr int kRowsRegs = 96;          // 640 threads an SM; with dsum 48 to 72 bytes a thread are spilled for it
 constexpr int kStagesMax = 2;          // more gain nothing: what is under way is limited by the number of blocks
 constexpr int kSmemSm = 226 * 1024;    // of an SM's 228 KB
 constexpr int kSmemBlock = 2048;       // what a block takes of it beside the ring and the weight, and more
@@ -424,8 +424,9 @@ cudaError_t launch_norm_bwd(const NormParams& p, const NormPlan& o, bool bf16, c
 }
 
 cudaError_t launch_norm_join(const NormParams& p, bool bf16, cudaStream_t st) {
-    // 32 or 64 slots: 304 parts of 5120 columns 12.6 us (the whole gradient of 1505 rows) against 14.5, 760 parts of
-    // 1536 (8192 rows) 19.0 against 18.0
+    // 32 or 64 slots, us of the whole gradient: 456 parts of 4096 columns (2000 rows) 14.4 and 14.3, 304 of 5120 15.9 and
+    // 18.1, 608 of 2048 9.9 and 9.4, 1216 of 1024 9.7 and 8.2.  Parts are not all of it: up to 4864 columns the blocks of 64
+    // slots are on the SMs at once, and few parts of few columns would gain as well (200 of 1024 6.0 and 5.3)
     const int threads = p.parts > 512 ? kJoinThreads : kJoinThreads / 2;
     return launch_chained(bf16 ? k_norm_join<true> : k_norm_join<false>, p.dweight ? p.d / kJoinCols : 1, threads, 0, p, st);
 }

@@ -248,7 +248,7 @@ constexpr uint32_t kNotFinite = kBf16 ? 0x7f80u : 0x7c00u;
 constexpr float kToInt = 12582912.f;   // 1.5 * 2^23: adding it leaves the nearest integer in the low bits
 
 // 1 / s by one step of Newton's method from the approximate reciprocal: for every
-// bf16 number from 2^-126 to 2^121 the correctly rounded one (a test goes through all).
+// bf16 number from 2^-126 to 2^121 the correctly rounded one (a test runs it for all).
 // __frcp_rn's handling of other numbers costs branches.
 __device__ __forceinline__ float scale_reciprocal(float s) {
     float r;
@@ -335,7 +335,7 @@ __device__ __forceinline__ void load_matrix(const uint16_t* a, bool on, Unit* x)
         *x = load_unit(a, on);
 }
 
-// A row's threads: `lane` of `width` (4, 16 or 32 lanes of a warp, or whole warps), with units lane, lane + width.
+// A row's threads: `lane` of `width` (4, 8, 16 or 32 lanes of a warp, or whole warps), with units lane, lane + width.
 // at: the thread's first element.  The rows of a warp get zeros where they do not count, and behind their end.  A wide
 // row's threads keep there what they had: such a row is left out as a whole, and what lies behind a
 // row's end is left out of the sums and of the outputs, so that it needs no zeros.
@@ -371,7 +371,7 @@ __device__ __forceinline__ Unit stream_of(const Raw<kSrc, kUpt>& raw, int k) {
 }
 
 // Which of the rows to come count, for rows t, t + step, ...  The lanes of a row look
-// ahead together, each at one row, a window of 32 rows (of 4 or 16 where fewer lanes have a row) and the one
+// ahead together, each at one row, a window of 32 rows (of 4, 8 or 16 where fewer lanes have a row) and the one
 // after it: a mask byte's way from memory takes longer than a row that does not count.
 struct Ahead {
     uint32_t now, then;          // bit i: row i of this window, and of the next

@@ -15,7 +15,8 @@ namespace grpo {
 
 namespace {
 
-constexpr int kFwdRegs = 64, kFwdRegsTwo = 128;     // of a thread with one or two units: 1024 or 512 threads an SM
+// of a thread with one or two units: 1024 or 512 threads an SM; 8-bit y of a sum in rows of a warp spills 8 bytes a thread
+constexpr int kFwdRegs = 64, kFwdRegsTwo = 128;
 
 template <bool kMax>
 __device__ __forceinline__ float both(float a, float b) { return kMax ? fmaxf(a, b) : a + b; }
@@ -23,7 +24,6 @@ __device__ __forceinline__ float both(float a, float b) { return kMax ? fmaxf(a,
 // Sum (or maximum) over a row's threads, in a fixed order; every thread gets it.
 // A block's: the warps' values lie in s, of which the next call takes another
 // part, so that one barrier is enough; entries of warps that are not there hold 0.
-
 template <bool kWide, bool kMax>
 __device__ __forceinline__ float row_join(float v, int width, float* s) {
     for (int o = kWide ? 16 : width / 2; o > 0; o >>= 1) v = both<kMax>(v, __shfl_xor_sync(0xffffffffu, v, o));

@@ -38,8 +38,9 @@ NormPlan norm_fwd_plan(int64_t N, int d, int sm_count) {
 
 // Two units a thread where a block of one would fill an SM (d > 6144), and from a checkpoint, whose codes cost
 // instructions, where that leaves no thread without one (160,000 x 4096, 54% of the rows: 373 against 388 us).
-// Of wide rows an SM takes as many as bring its copies under way, two rows a block, to 60 KB
-// and somewhat more than two rows: 40,000 rows of 4096: 162 us with 64 KB, 149 with 96, 163 with 144; 80,000 of 2048:
+// Of wide rows an SM takes as many blocks as bring its copies under way, two rows a block, to 60 KB and 9/4 of a row (64
+// with a checkpoint, 16 more with dsum); no block has less than one.  These numbers are fitted to the times that follow, and
+// another machine or kernel would want others: 40,000 rows of 4096: 162 us with 64 KB, 149 with 96, 163 with 144; 80,000 of 2048:
 // 170 with 48 KB, 153 with 64, 164 with 96; 160,000 of 1024: 149 with 64 KB, 162 with 80; 284,444 of 576: 255 with 36 KB,
 // 226 with 54.  With dsum, or from a checkpoint, where instructions count too, more does less harm; and rows that leave
 // threads without elements take longer and need more of them (131,072 of 1280: 171 us with 6 blocks, 159 with 8).
